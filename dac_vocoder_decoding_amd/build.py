@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libvocoder.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["conv_gemm.hip", "fused_ru.hip", "stream_kernels.hip", "peak_kernels.hip", "runtime.hip",
-           "host_config.cpp"]
+           "host_config.cpp", "rows_kernels.hip", "int_matmul.hip", "cache_kernels.hip", "attention.hip",
+           "ops_host.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",

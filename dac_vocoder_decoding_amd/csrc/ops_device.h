@@ -1,0 +1,49 @@
+// ops_device.h -- device building blocks shared by the 8-bit transformer
+// operators: element types, the 8-bit row's scale, block reductions.
+#pragma once
+#include "ops.h"
+
+namespace voc {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+template <int T> struct Elem;
+template <> struct Elem<EL_F32> { typedef float type; };
+template <> struct Elem<EL_BF16> { typedef __bf16 type; };
+template <> struct Elem<EL_F16> { typedef _Float16 type; };
+
+// The scale of a group whose largest magnitude has the bit pattern `bits`
+// (magnitudes compare like their bits, with NaN above infinity above every
+// finite value, so an integer maximum carries a NaN along).
+constexpr uint32_t kInfBits = 0x7f800000u;
+__device__ __forceinline__ float scale_of_bits(uint32_t bits) {
+  if (bits >= kInfBits) return __uint_as_float(0x7fc00000u);
+  const float m = __uint_as_float(bits);
+  return m < 0x1p-100f ? 0.f : m * (1.0f / 127.0f);
+}
+// 1 / scale, or 0 where every code is 0 (scale 0 or NaN).
+__device__ __forceinline__ float inverse_of(float scale) { return scale > 0.f ? 1.0f / scale : 0.f; }
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+__device__ __forceinline__ int code_of(float v, float inv) {
+  // inv is 0 where the group holds an infinity: 0 times it must not become a code.
+  const float r = inv > 0.f ? __builtin_rintf(v * inv) : 0.f;
+  return static_cast<int>(fminf(fmaxf(r, -127.f), 127.f));
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int m = 32; m; m >>= 1) v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), m)));
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
+}  // namespace voc

@@ -29,7 +29,8 @@ VOC_DEVICE_ERROR = -4
 VOC_NOT_LOADED = -5
 VOC_CANCELLED = -6
 
-VOC_F32, VOC_BF16 = 0, 1
+VOC_F32, VOC_BF16, VOC_F16 = 0, 1, 2
+VOC_ACT_NONE, VOC_ACT_GELU = 0, 1
 VOC_SNAKE, VOC_SNAKE_BETA = 0, 1
 
 KERNEL_KINDS = ["conv_in", "convt", "res_k7", "res_k1", "head", "import", "export", "res_fused",
@@ -80,6 +81,32 @@ class voc_profile_stat(ctypes.Structure):
     ]
 
 
+class voc_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("page_tokens", ctypes.c_int),
+        ("kv_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int),
+        ("n_pages", ctypes.c_int64),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+    ]
+
+
+class voc_kv_batch(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("tokens", ctypes.c_int64),
+        ("max_new", ctypes.c_int64),
+        ("max_total", ctypes.c_int64),
+        ("starts", ctypes.c_void_p),
+        ("past", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 # int (*voc_cancel_fn)(void *user)
@@ -100,7 +127,7 @@ def lib():
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python -m dac_vocoder_decoding_amd.build`")
         L = ctypes.CDLL(LIB_PATH)
-        P, I64, I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+        P, I64, I, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
         CFG = ctypes.POINTER(voc_config)
         sig = {
             "voc_config_default": (None, [CFG]),
@@ -131,6 +158,14 @@ def lib():
             "voc_dbg_run_stage": (I, [P, I, P, I64, I64, P, P]),
             "voc_dbg_copy": (I, [P, P, I64, P]),
             "voc_dbg_peak": (I, [I, I64, ctypes.POINTER(ctypes.c_double), P]),
+            "voc_ops_create": (I, [I, ctypes.POINTER(P)]),
+            "voc_ops_last_error": (ctypes.c_char_p, [P]),
+            "voc_ops_destroy": (None, [P]),
+            "vocoder_rms_norm": (I, [P, I, I64, I64, P, I64, P, I64, P, I64, P, F, P, I64, P, P]),
+            "vocoder_quantize_rows": (I, [P, I, I64, I64, P, I64, P, I64, P, P]),
+            "vocoder_matmul_int": (I, [P, I, I64, I64, I64, P, I64, P, P, I64, P, P, I, P, I64, P]),
+            "vocoder_cache_append": (I, [P, P, P, I, P, I64, I64, P, I64, I64, P]),
+            "vocoder_cache_attention": (I, [P, P, P, I, I, P, I64, I64, F, I, I64, P, I64, I64, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -461,4 +496,210 @@ def run_stage(ctx, stage: int, x, stream=None):
     expect_dim("stage input", x.shape, 1, c_in)
     out = torch.empty(b, c_out, t_out, device=x.device)
     check(voc_dbg_run_stage(ctx, stage, x, b, t, out, stream), ctx)
+    return out
+
+
+# ------------------------------------------ 8-bit transformer operators
+# The calls of vocoder.h take raw pointers and strides; the helpers below take
+# CUDA tensors, read the strides off them, check the shapes that the library
+# cannot see, and allocate what is not given.  All of them run on `stream`
+# (default: torch's current stream).
+
+def voc_ops_create(device: int = 0):
+    """Returns (status, ops)."""
+    ops = ctypes.c_void_p()
+    st = lib().voc_ops_create(device, ctypes.byref(ops))
+    return st, ops
+
+
+def voc_ops_last_error(ops) -> str:
+    r = lib().voc_ops_last_error(ops)
+    return r.decode() if r else ""
+
+
+def voc_ops_destroy(ops) -> None:
+    lib().voc_ops_destroy(ops)
+
+
+def open_ops(device: int = 0):
+    """A handle of the operators (voc_ops_create); raises VocError on failure."""
+    st, ops = voc_ops_create(device)
+    if st != VOC_OK:
+        raise VocError(st, voc_ops_last_error(None))
+    return ops
+
+
+_dtypes: dict = {}
+
+
+def _dtype(t) -> int:
+    """voc_dtype of a torch dtype."""
+    if not _dtypes:
+        import torch
+        _dtypes.update({torch.float32: VOC_F32, torch.bfloat16: VOC_BF16, torch.float16: VOC_F16})
+    d = _dtypes.get(t)
+    if d is None:
+        raise ValueError(f"dtype {t}: float32, bfloat16 or float16 is needed")
+    return d
+
+
+def _check_ops(st: int, ops) -> None:
+    if st != VOC_OK:
+        raise VocError(st, voc_ops_last_error(ops))
+
+
+def _rows(what: str, t, shape=None, dtype=None):
+    """Checks a CUDA matrix whose rows are contiguous; returns its row stride."""
+    if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: a CUDA matrix with contiguous rows is needed")
+    if (shape is not None and tuple(t.shape) != tuple(shape)) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what}: expected {tuple(shape or t.shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _vector(what: str, t, n: int):
+    import torch
+    if not t.is_cuda or t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what}: {n} contiguous CUDA float32 values are needed")
+    return t
+
+
+def rms_norm(ops, x, weight, eps: float = 1e-6, residual=None, h=None, q=None, scale=None, stream=None):
+    """(q int8 [rows, C], scale fp32 [rows], h) of the rows x [rows, C]
+    (vocoder_rms_norm).  h = x + residual is stored into `h` (which may be x
+    or residual itself), into a new tensor if that is None and there is a
+    residual, and is x itself without one."""
+    import torch
+    ldx = _rows("x", x)
+    rows, C = x.shape
+    ldr = _rows("residual", residual, x.shape, x.dtype) if residual is not None else 0
+    if h is None and residual is not None:
+        h = torch.empty_like(x, memory_format=torch.contiguous_format)
+    ldh = _rows("h", h, x.shape, x.dtype) if h is not None else 0
+    if q is None:
+        q = torch.empty(rows, C, dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _check_ops(lib().vocoder_rms_norm(
+        ops, _dtype(x.dtype), rows, C, x.data_ptr(), ldx, _ptr(residual), ldr, _ptr(h), ldh,
+        _vector("weight", weight, C).data_ptr(), eps, q.data_ptr(), _rows("q", q, x.shape, torch.int8),
+        _vector("scale", scale, rows).data_ptr(), _stream(stream)), ops)
+    return q, scale, x if h is None else h
+
+
+def quantize_rows(ops, x, q=None, scale=None, stream=None):
+    """(q int8 [rows, C], scale fp32 [rows]) of the rows x [rows, C]
+    (vocoder_quantize_rows)."""
+    import torch
+    ldx = _rows("x", x)
+    rows, C = x.shape
+    if q is None:
+        q = torch.empty(rows, C, dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _check_ops(lib().vocoder_quantize_rows(
+        ops, _dtype(x.dtype), rows, C, x.data_ptr(), ldx, q.data_ptr(), _rows("q", q, x.shape, torch.int8),
+        _vector("scale", scale, rows).data_ptr(), _stream(stream)), ops)
+    return q, scale
+
+
+def matmul_int(ops, a, a_scale, b, b_scale, bias=None, gelu: bool = False, dtype=None, out=None, stream=None):
+    """act((a b^T) * a_scale[:, None] * b_scale + bias) [M, N] for int8 a
+    [M, K] and b [N, K] (vocoder_matmul_int), in `dtype` (default float16) or
+    the dtype of `out`."""
+    import torch
+    lda, ldb = _rows("a", a, None, torch.int8), _rows("b", b, (b.shape[0], a.shape[1]), torch.int8)
+    (M, K), N = a.shape, b.shape[0]
+    if out is None:
+        out = torch.empty(M, N, dtype=dtype or torch.float16, device=a.device)
+    ldy = _rows("out", out, (M, N), dtype)
+    _check_ops(lib().vocoder_matmul_int(
+        ops, _dtype(out.dtype), M, N, K, a.data_ptr(), lda, _vector("a_scale", a_scale, M).data_ptr(), b.data_ptr(), ldb,
+        _vector("b_scale", b_scale, N).data_ptr(), _ptr(None if bias is None else _vector("bias", bias, N)),
+        VOC_ACT_GELU if gelu else VOC_ACT_NONE, out.data_ptr(), ldy, _stream(stream)), ops)
+    return out
+
+
+class KVCache:
+    """A paged 8-bit cache (voc_kv_cache): k int8 [pages, kv_heads,
+    page_tokens, head_dim], v int8 [pages, kv_heads, head_dim, page_tokens],
+    k_scale and v_scale fp32 [pages, kv_heads]."""
+
+    def __init__(self, pages: int, page_tokens: int, kv_heads: int, head_dim: int, device="cuda"):
+        import torch
+        self._set(torch.zeros(pages, kv_heads, page_tokens, head_dim, dtype=torch.int8, device=device),
+                  torch.zeros(pages, kv_heads, head_dim, page_tokens, dtype=torch.int8, device=device),
+                  torch.zeros(pages, kv_heads, device=device), torch.zeros(pages, kv_heads, device=device))
+
+    @classmethod
+    def from_tensors(cls, k, v, k_scale, v_scale):
+        """A cache over tensors that the caller allocated."""
+        c = cls.__new__(cls)
+        c._set(k, v, k_scale, v_scale)
+        return c
+
+    def _set(self, k, v, k_scale, v_scale):
+        import torch
+        n, h, p, d = k.shape
+        for t, shape, dt in ((k, (n, h, p, d), torch.int8), (v, (n, h, d, p), torch.int8),
+                             (k_scale, (n, h), torch.float32), (v_scale, (n, h), torch.float32)):
+            if tuple(t.shape) != shape or t.dtype != dt or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"cache: a contiguous CUDA {dt} tensor of shape {shape} is needed")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.kv_heads, self.page_tokens, self.head_dim = h, p, d
+        self.c = voc_kv_cache(p, h, d, n, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
+        self.ref = ctypes.byref(self.c)
+
+
+class KVBatch:
+    """The sequences of one step (voc_kv_batch): page_table int32 [B, pages],
+    past int32 [B], starts int32 [B + 1], and the host's bounds max_new (new
+    tokens of a sequence) and max_total (past + new)."""
+
+    def __init__(self, page_table, past, starts, max_new: int, max_total: int):
+        import torch
+        B = past.numel()
+        for what, t, shape in (("page_table", page_table, (B, page_table.shape[-1])), ("past", past, (B,)),
+                               ("starts", starts, (B + 1,))):
+            if t.dtype != torch.int32 or not t.is_cuda or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{what}: a contiguous CUDA int32 tensor of shape {shape} is needed")
+        self.page_table, self.past, self.starts = page_table, past, starts
+        self.c = voc_kv_batch(B, 0, max_new, max_total, starts.data_ptr(), past.data_ptr(), page_table.data_ptr(),
+                              page_table.shape[1])
+        self.ref = ctypes.byref(self.c)
+
+
+def _heads(what: str, t, tokens, heads, dim, dtype=None):
+    """Checks a CUDA tensor [tokens, heads, dim] with contiguous dim."""
+    if not t.is_cuda or t.dim() != 3 or t.shape[2] != dim or t.stride(2) != 1 or (tokens, heads) != tuple(t.shape[:2]):
+        raise ValueError(f"{what}: a CUDA tensor [{tokens}, {heads}, {dim}] with contiguous last dimension is needed")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    return t
+
+
+def cache_append(ops, cache: KVCache, batch: KVBatch, k, v, stream=None) -> None:
+    """Append k and v [tokens, kv_heads, head_dim] to the cache
+    (vocoder_cache_append)."""
+    _heads("k", k, k.shape[0], cache.kv_heads, cache.head_dim)
+    _heads("v", v, k.shape[0], cache.kv_heads, cache.head_dim, k.dtype)
+    batch.c.tokens = k.shape[0]
+    _check_ops(lib().vocoder_cache_append(ops, cache.ref, batch.ref, _dtype(k.dtype), k.data_ptr(), k.stride(0),
+                                          k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), _stream(stream)), ops)
+
+
+def cache_attention(ops, cache: KVCache, batch: KVBatch, q, scale: float | None = None, causal: bool = True,
+                    window: int = 0, out=None, stream=None):
+    """Attention of q [tokens, heads, head_dim] over the cache
+    (vocoder_cache_attention); scale defaults to head_dim ** -0.5."""
+    import torch
+    _heads("q", q, q.shape[0], q.shape[1], cache.head_dim)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _heads("out", out, q.shape[0], q.shape[1], cache.head_dim, q.dtype)
+    batch.c.tokens = q.shape[0]
+    _check_ops(lib().vocoder_cache_attention(
+        ops, cache.ref, batch.ref, _dtype(q.dtype), q.shape[1], q.data_ptr(), q.stride(0), q.stride(1),
+        cache.head_dim ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(), out.stride(0),
+        out.stride(1), _stream(stream)), ops)
     return out

@@ -83,9 +83,11 @@ typedef enum voc_status {
 
 typedef enum voc_dtype {
   VOC_F32 = 0,  /* fp32 weights and matrix-core operands, fp32 accumulate   */
-  VOC_BF16 = 1  /* bf16 weights (cast after the fold) and bf16 operands,    */
+  VOC_BF16 = 1, /* bf16 weights (cast after the fold) and bf16 operands,    */
                 /* fp32 accumulate and epilogues, fp16 residual stream       */
                 /* (operand_terms = 2: two bf16 terms per operand, below)    */
+  VOC_F16 = 2   /* fp16 activations of the 8-bit transformer operators (end  */
+                /* of this file); no decoder configuration has it            */
 } voc_dtype;
 
 typedef enum voc_act { VOC_SNAKE = 0, VOC_SNAKE_BETA = 1 } voc_act;
@@ -457,6 +459,176 @@ voc_status voc_dbg_copy(void *dst, const void *src, int64_t bytes, void *hip_str
  * measurement only, not for a decode loop.  Errors: VOC_INVALID_PARAMS
  * (NULL value, n <= 0, unknown `what`), VOC_DEVICE_ERROR. */
 voc_status voc_dbg_peak(int what, int64_t n, double *value, void *hip_stream);
+
+/* ------------------------------------- 8-bit transformer operators
+ * What a codec's transformer stage runs ahead of the causal decoder
+ * (qwentts.cpp ARCHITECTURE, "Audio tokenizer decoder": a pre-transformer
+ * with a sliding window and a key/value cache hands its frames to the DAC
+ * stage), with 8-bit weights, activations and cache:
+ *   vocoder_rms_norm         residual addition, RMS norm, 8-bit rows
+ *   vocoder_quantize_rows    8-bit rows of any matrix (weights, activations)
+ *   vocoder_matmul_int       8-bit integer product with row scales
+ *   vocoder_cache_append     keys and values into a paged 8-bit cache
+ *   vocoder_cache_attention  attention over that cache
+ *
+ * All of them work on device buffers of the caller, are asynchronous on
+ * hip_stream, allocate nothing and can be captured into a HIP graph.  They
+ * check their host arguments and return VOC_INVALID_PARAMS with a message
+ * (voc_ops_last_error) before any device call.  Activations are VOC_F32,
+ * VOC_BF16 or VOC_F16; strides count elements; arithmetic is fp32 (integer
+ * products: 32-bit integers, exact), each output rounded once.
+ *
+ * 8-bit rows: a group of values v (a row; a page of one cache head) is held
+ * as signed codes q with one fp32 scale s: s = max|v| / 127 (computed as
+ * max|v| times the fp32 value nearest 1/127), q = rint(v * (1 / s)), ties to
+ * even, |q| <= 127.  A group whose largest magnitude is below 2^-100 gets
+ * s = 0 and q = 0; a group with a NaN or an infinity gets s = NaN and q = 0,
+ * so that what is computed from it is NaN.
+ *
+ * Threading: as for voc_ctx, one handle per host thread and stream (the
+ * handle owns the workspace in which split attention joins its parts). */
+typedef struct voc_ops voc_ops;
+
+/* Create a handle on HIP device hip_device with its workspace (device
+ * memory, VOC_OPS_WORKSPACE_BYTES).  *out receives the handle or NULL. */
+#define VOC_OPS_WORKSPACE_BYTES 33554432
+voc_status voc_ops_create(int hip_device, voc_ops **out);
+
+/* Message of the last error on ops ("" if none); with ops == NULL, of the
+ * last failed voc_ops_create of this thread. */
+const char *voc_ops_last_error(const voc_ops *ops);
+
+/* Release the handle and its workspace.  NULL-safe.  The caller must have
+ * synchronized the streams it used the handle on. */
+void voc_ops_destroy(voc_ops *ops);
+
+/*
+ * For each of `rows` rows of C values (1 <= C <= 16384; rows may be 0):
+ *   h = round_to_dtype(x + residual)      (h = x without a residual)
+ *   y = h / sqrt(mean(h^2) + eps) * weight
+ *   q, scale = 8-bit row of y             (codes [rows][ldq], scale [rows])
+ * x, residual, h: dtype, row strides ldx, ldr, ldh >= C.  residual may be
+ * NULL; h_out may be NULL (not stored), or x or residual themselves (updated
+ * in place; any other overlap is an error of the caller).  weight: fp32 [C].
+ * A row whose sum of squares is not finite in fp32 gets scale NaN.
+ * Rows whose pointers and strides are 16-byte multiples run faster.
+ * Errors: VOC_INVALID_PARAMS (NULL pointer, unknown dtype, size or stride
+ * out of range, pointers not aligned to their elements, eps negative or not
+ * finite), VOC_DEVICE_ERROR.
+ */
+voc_status vocoder_rms_norm(voc_ops *ops, int dtype, int64_t rows, int64_t C, const void *x,
+                            int64_t ldx, const void *residual, int64_t ldr, void *h_out,
+                            int64_t ldh, const float *weight, float eps, int8_t *q, int64_t ldq,
+                            float *scale, void *hip_stream);
+
+/* q, scale = 8-bit rows of x (as above, without the norm): activations in
+ * front of a product, and its weights [N][K] (one scale per output
+ * channel).  1 <= C <= 16384. */
+voc_status vocoder_quantize_rows(voc_ops *ops, int dtype, int64_t rows, int64_t C, const void *x,
+                                 int64_t ldx, int8_t *q, int64_t ldq, float *scale,
+                                 void *hip_stream);
+
+/*
+ * y[m][n] = act((sum_k a[m][k] b[n][k]) * a_scale[m] * b_scale[n] + bias[n])
+ * a: int8 [M][lda], b: int8 [N][ldb] (a Linear's weight, (out, in)), scales
+ * fp32 [M] and [N], bias fp32 [N] or NULL, y: out_dtype [M][ldy].
+ * 1 <= K <= 131071 (the 32-bit sums are exact for any codes); M or N may be
+ * 0.  act: VOC_ACT_NONE, or VOC_ACT_GELU, x/2 (1 + erf(x / sqrt(2))).
+ * Any alignment and stride works; 16-byte multiples run faster.
+ * Errors: VOC_INVALID_PARAMS (NULL pointer, unknown dtype or act, size or
+ * stride out of range, y or the scales not aligned to their elements),
+ * VOC_DEVICE_ERROR.
+ */
+enum { VOC_ACT_NONE = 0, VOC_ACT_GELU = 1 };
+voc_status vocoder_matmul_int(voc_ops *ops, int out_dtype, int64_t M, int64_t N, int64_t K,
+                              const int8_t *a, int64_t lda, const float *a_scale, const int8_t *b,
+                              int64_t ldb, const float *b_scale, const float *bias, int act,
+                              void *y, int64_t ldy, void *hip_stream);
+
+/*
+ * A paged cache in 8 bits.  A page holds page_tokens consecutive tokens of
+ * one sequence for every cache head, with one key scale and one value scale
+ * per page and head:
+ *   k        int8  [n_pages][kv_heads][page_tokens][head_dim]
+ *   v        int8  [n_pages][kv_heads][head_dim][page_tokens]
+ *            (values are transposed inside a page: both matrix products of
+ *            the attention then read 16 codes of their reduction at a time)
+ *   k_scale, v_scale   fp32 [n_pages][kv_heads]
+ * page_tokens is 16, 32, 64 or 128; head_dim a multiple of 32 up to 256;
+ * k and v are 16-byte aligned.  Device memory of the caller; nothing in it
+ * has to be cleared: what no token was written to is never used.
+ */
+typedef struct voc_kv_cache {
+  int page_tokens, kv_heads, head_dim;
+  int64_t n_pages;
+  int8_t *k, *v;
+  float *k_scale, *v_scale;
+} voc_kv_cache;
+
+/*
+ * The sequences of one step, all arrays int32 on the device.  Sequence b
+ * holds past[b] tokens already; its new tokens are rows starts[b] ..
+ * starts[b + 1] - 1 of the packed inputs (starts has batch + 1 entries,
+ * starts[batch] <= tokens, the packed rows); position p of it lies in page
+ * page_table[b * table_stride + p / page_tokens].  Every layer of a model
+ * appends and attends with the same past; the caller advances it afterwards.
+ * max_new and max_total are the host's upper bounds for the new tokens of a
+ * sequence and for past + new (they size the launches).
+ * The device arrays cannot be checked on the host.  The kernels stay in
+ * bounds whatever they hold: page numbers outside [0, n_pages) and positions
+ * past table_stride pages hold no tokens (appends to them are dropped), past
+ * counts as 0 if negative, and a sequence whose rows do not lie in
+ * [0, tokens) or exceed max_new has no new tokens (its outputs, if any row
+ * of them exists, are not written).
+ * A page must belong to one sequence only while it is appended to.
+ */
+typedef struct voc_kv_batch {
+  int64_t batch, tokens, max_new, max_total;
+  const int32_t *starts, *past, *page_table;
+  int64_t table_stride;
+} voc_kv_batch;
+
+/*
+ * Append new keys and values (dtype, element [t][head][d] at
+ * t * token_stride + head * head_stride + d; rows as in `batch`) to the
+ * cache.  A page's scale covers its old and new tokens: the larger of the
+ * old scale and the new tokens' own; where it grows, the page's old codes
+ * are rounded again, rint(q * (s_old * (1 / s_new))).  The tokens of one
+ * page are best appended together: each growth of the scale costs the older
+ * ones up to half a step.  A NaN or infinity makes the page's scale of that
+ * head NaN, for its other tokens too.
+ * Errors: VOC_INVALID_PARAMS, VOC_DEVICE_ERROR.
+ */
+voc_status vocoder_cache_append(voc_ops *ops, const voc_kv_cache *cache, const voc_kv_batch *batch,
+                                int dtype, const void *k, int64_t k_token_stride,
+                                int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                                int64_t v_head_stride, void *hip_stream);
+
+/*
+ * Attention of the new tokens' queries over the cache (their own keys and
+ * values appended before): query row starts[b] + i of sequence b sits at
+ * position p = past[b] + i and sees the positions j of its past[b] + new
+ * tokens with j <= p (causal = 1) and j > p - window (window > 0):
+ *   o = sum_j softmax_j(softmax_scale q . k_j) v_j
+ * A query that sees no position gives zeros.  q and o: dtype, [t][head][d]
+ * with their strides, `heads` query heads; heads is a multiple of kv_heads
+ * and query head h reads cache head h / (heads / kv_heads).
+ * Keys and values enter the matrix cores as exact fp16 codes.  fp16 and bf16
+ * queries enter exactly (each row scaled by a power of two; what lies 2^24
+ * below a row's largest value may round), the probabilities in fp16; fp32
+ * queries and probabilities as two fp16 terms each, which hold about 22
+ * bits.  Scores, softmax statistics and sums are fp32.
+ * Results do not depend on what else runs; long caches are split over
+ * workgroups and the parts joined in a fixed order.
+ * q and o need 16-byte alignment and strides of 16-byte multiples.
+ * Errors: VOC_INVALID_PARAMS, VOC_DEVICE_ERROR.
+ */
+voc_status vocoder_cache_attention(voc_ops *ops, const voc_kv_cache *cache,
+                                   const voc_kv_batch *batch, int dtype, int heads, const void *q,
+                                   int64_t q_token_stride, int64_t q_head_stride,
+                                   float softmax_scale, int causal, int64_t window, void *o,
+                                   int64_t o_token_stride, int64_t o_head_stride,
+                                   void *hip_stream);
 
 #ifdef __cplusplus
 }
