@@ -5,9 +5,10 @@
 //
 // The matrix-core "A" operand is b (output features), "B" is a (tokens): a
 // lane then holds four consecutive features of one token, which it stores
-// together.
+// together.  Integer sums are exact, so every variant gives the same bits.
 #include <string.h>
 
+#include "gemm_common.h"
 #include "ops_device.h"
 
 namespace voc {
@@ -30,49 +31,336 @@ __device__ __forceinline__ float activate(float v, int act) {
   return act ? 0.5f * v * (1.0f + erff(v * 0.70710678118654752f)) : v;
 }
 
-// One wave per 16 tokens x 64 features, operands read straight from memory.
+// Four consecutive features n .. n + 3 of token m (n a multiple of 4).
 template <int T>
-__global__ __launch_bounds__(256) void int_matmul_kernel(const IntMatmulArgs a) {
+__device__ __forceinline__ void store4(const IntMatmulArgs& a, bool vec, int m, int n, float sa, const i32x4& acc) {
   typedef typename Elem<T>::type E;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int lr = lane & 15, lg = lane >> 4;
-  const int n0 = (blockIdx.x * 4 + wave) * 64;
-  const int m = blockIdx.y * 16 + lr;
-  if (n0 >= a.N) return;
-  i32x4 acc[4] = {{0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}};
-  const int8_t* arow = a.a + static_cast<int64_t>(min(m, a.M - 1)) * a.lda;
-  const int8_t* brow[4];
+  E* y = static_cast<E*>(a.y) + static_cast<int64_t>(m) * a.ldy + n;
+  E e[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) brow[j] = a.b + static_cast<int64_t>(min(n0 + j * 16 + lr, a.N - 1)) * a.ldb;
-  for (int k = lg * 16; k < a.K + lg * 16; k += 64) {
-    const i32x4 av = load_codes(arow, k, a.K);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(load_codes(brow[j], k, a.K), av, acc[j], 0, 0, 0);
+  for (int i = 0; i < 4; ++i) {
+    const int c = min(n + i, a.N - 1);
+    const float v = static_cast<float>(acc[i]) * sa * a.sb[c] + (a.bias ? a.bias[c] : 0.f);
+    e[i] = static_cast<E>(activate(v, a.act));
   }
-  if (m >= a.M) return;
-  const float sa = a.sa[m];
-  E* y = static_cast<E*>(a.y) + static_cast<int64_t>(m) * a.ldy;
+  if (vec && n + 4 <= a.N) {
+    __builtin_memcpy(__builtin_assume_aligned(y, 4 * sizeof(E)), e, 4 * sizeof(E));
+  } else {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+    for (int i = 0; i < 4; ++i)
+      if (n + i < a.N) y[i] = e[i];
+  }
+}
+
+// ------------------------------------------------------------- few tokens
+// One workgroup per 16 features: its eight waves split K and read the weights
+// once, straight into registers; the integer partial sums meet in LDS.
+// MB blocks of 16 tokens.
+template <int T, int MB>
+__global__ __launch_bounds__(512) void int_matmul_few_kernel(const IntMatmulArgs a, int vec) {
+  __shared__ i32x4 s_acc[8][MB][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, lg = lane >> 4;
+  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * MB * 16;
+  const int steps = (a.K + 63) / 64, per = (steps + 7) / 8;
+  const int k1 = min(a.K + 63, (wave + 1) * per * 64) & ~63;
+  const int8_t* brow = a.b + static_cast<int64_t>(min(n0 + lr, a.N - 1)) * a.ldb;
+  const int8_t* arow[MB];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = n0 + j * 16 + lg * 4 + i;
-      if (n < a.N) {
-        const float v = static_cast<float>(acc[j][i]) * sa * a.sb[n] + (a.bias ? a.bias[n] : 0.f);
-        y[n] = static_cast<E>(activate(v, a.act));
+  for (int j = 0; j < MB; ++j) arow[j] = a.a + static_cast<int64_t>(min(m0 + j * 16 + lr, a.M - 1)) * a.lda;
+  i32x4 acc[MB];
+#pragma unroll
+  for (int j = 0; j < MB; ++j) acc[j] = i32x4{0, 0, 0, 0};
+  // Four steps' loads are issued together; only the step that holds K's end
+  // needs the masked load.
+  for (int k0 = wave * per * 64; k0 < k1; k0 += 256) {
+    i32x4 w[4], x[4][MB];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = k0 + u * 64 + lg * 16;
+      if (k0 + u * 64 >= k1) continue;
+      if (k0 + u * 64 + 64 <= a.K) {
+        __builtin_memcpy(&w[u], brow + k, 16);
+#pragma unroll
+        for (int j = 0; j < MB; ++j) __builtin_memcpy(&x[u][j], arow[j] + k, 16);
+      } else {
+        w[u] = load_codes(brow, k, a.K);
+#pragma unroll
+        for (int j = 0; j < MB; ++j) x[u][j] = load_codes(arow[j], k, a.K);
       }
     }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (k0 + u * 64 >= k1) continue;
+#pragma unroll
+      for (int j = 0; j < MB; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u], x[u][j], acc[j], 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < MB; ++j) s_acc[wave][j][lane] = acc[j];
+  __syncthreads();
+  if (wave >= MB) return;  // wave j finishes token block j
+  i32x4 v = {0, 0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < 8; ++w) v += s_acc[w][wave][lane];
+  const int m = m0 + wave * 16 + lr, n = n0 + 4 * lg;
+  if (m < a.M && n < a.N) store4<T>(a, vec, m, n, a.sa[m], v);
+}
+
+// ------------------------------------------------------------- tiles
+// BF features x BT tokens per workgroup, WF x WT waves.  K passes in stages
+// of 128 codes (whole cache lines) through a ring of NS stages in LDS.  A
+// stage holds rows of 128 bytes, features first; the 16-byte unit u of row r
+// sits at unit u ^ (r / 2 % 8) of its row, which spreads the fragment reads
+// (16 rows, 4 units) over all banks.
+// DMA: global -> LDS copies through buffer resources, NS - 1 stages in
+// flight, out-of-range rows and codes read as zero (16-byte aligned rows, K
+// a multiple of 16).  Otherwise the rows go through registers, two stages
+// ahead, with their tails masked (any alignment).
+constexpr int kStageK = 128;
+
+template <int T, int BF, int BT, int WF, int WT, int NS, bool DMA>
+__global__ __launch_bounds__(WF * WT * 64) void int_matmul_tile_kernel(const IntMatmulArgs a, int tf, int tt, int vec) {
+  typedef typename Elem<T>::type E;
+  constexpr int NW = WF * WT;
+  constexpr int FF = BF / WF / 16, FT = BT / WT / 16;
+  constexpr int FB = BF / 8, TB = FB + BT / 8;  // 1 KB blocks of 8 rows in a stage
+  constexpr int LW = TB / NW;
+  constexpr int STAGE = TB * 1024;
+  static_assert(TB % NW == 0 && NW % 2 == 0 && (NS - 2) * LW <= 63, "whole blocks per wave");
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[NS * STAGE];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, lg = lane >> 4;
+  const int wf = wave % WF, wt = wave / WF;
+
+  // Each XCD takes a contiguous range of tiles, in bands of 8 token tiles, so
+  // that the tiles it runs together share feature and token rows in its L2.
+  const int L = xcd_remap(blockIdx.x, tf * tt);
+  const int band = L / (8 * tf), left = tt - band * 8;
+  const int bh = left < 8 ? left : 8;
+  const int in_band = L - band * 8 * tf;
+  const int n0 = (in_band / bh) * BF, m0 = (band * 8 + in_band % bh) * BT;
+  const int nstages = (a.K + kStageK - 1) / kStageK;
+
+  i32x4 acc[FF][FT];
+#pragma unroll
+  for (int i = 0; i < FF; ++i)
+#pragma unroll
+    for (int j = 0; j < FT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+
+  // This lane's part of a block copy: row 8 b + lane / 8, the unit that sits
+  // at position lane % 8 there (b has the parity of the wave).
+  const int crow = lane >> 3;
+  const int cunit = ((lane & 7) ^ ((crow >> 1) + 4 * (wave & 1))) * 16;
+  // Its fragment rows within 16 rows, for both halves of a stage.
+  const int frow = (lr >> 3) * 1024 + (lr & 7) * 128;
+  const int fu[2] = {frow + ((lg ^ (lr >> 1)) * 16), frow + (((lg + 4) ^ (lr >> 1)) * 16)};
+  auto stage_mma = [&](const unsigned char* s) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const unsigned char* pf = s + fu[h] + wf * FF * 2048;
+      const unsigned char* pt = s + fu[h] + FB * 1024 + wt * FT * 2048;
+      i32x4 xf[FF], xt[FT];
+#pragma unroll
+      for (int j = 0; j < FT; ++j) xt[j] = *reinterpret_cast<const i32x4*>(pt + j * 2048);
+#pragma unroll
+      for (int i = 0; i < FF; ++i) xf[i] = *reinterpret_cast<const i32x4*>(pf + i * 2048);
+#pragma unroll
+      for (int i = 0; i < FF; ++i)
+#pragma unroll
+        for (int j = 0; j < FT; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xf[i], xt[j], acc[i][j], 0, 0, 0);
+    }
+    // The second half's fragments are read between the first half's products.
+    __builtin_amdgcn_sched_group_barrier(0x100, FT + FF, 0);
+#pragma unroll
+    for (int q = 0; q < FF + FT; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, FF * FT / (FF + FT), 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+  };
+
+  if constexpr (DMA) {
+    const uint32_t lds = lds_addr(smem);
+    // The host keeps 256 rows below 2^31 bytes.
+    const int nf = min(a.N - n0, BF), nt = min(a.M - m0, BT);
+    const i4 fs = buf_rsrc(a.b + static_cast<int64_t>(n0) * a.ldb, static_cast<uint32_t>((nf - 1) * a.ldb + a.K));
+    const i4 ts = buf_rsrc(a.a + static_cast<int64_t>(m0) * a.lda, static_cast<uint32_t>((nt - 1) * a.lda + a.K));
+    uint32_t off[LW];
+#pragma unroll
+    for (int u = 0; u < LW; ++u) {
+      const int b = wave + NW * u;
+      const int row = (b < FB ? b : b - FB) * 8 + crow;
+      off[u] = row < (b < FB ? nf : nt) ? static_cast<uint32_t>(row) * static_cast<uint32_t>(b < FB ? a.ldb : a.lda) + cunit
+                                        : 0x80000000u;
+    }
+    auto issue = [&](int c, int slot) {
+      const int k = c * kStageK;
+      const bool past = k + cunit >= a.K;
+#pragma unroll
+      for (int u = 0; u < LW; ++u) {
+        const int b = wave + NW * u;
+        dma16(b < FB ? fs : ts, past ? 0x80000000u : off[u] + k, lds + slot * STAGE + b * 1024);
+      }
+    };
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s)
+      if (s < nstages) issue(s, s);
+    int slot = 0;
+    for (int c = 0; c < nstages; ++c) {
+      if (c + NS - 1 <= nstages)
+        wait_vm<(NS - 2) * LW>();
+      else
+        wait_vm<0>();
+      lds_barrier();  // stage c is in LDS; every wave has read stage c - 1
+      if (c + NS - 1 < nstages) issue(c + NS - 1, slot == 0 ? NS - 1 : slot - 1);
+      stage_mma(smem + slot * STAGE);
+      slot = slot + 1 == NS ? 0 : slot + 1;
+    }
+  } else {
+    const int8_t* row[LW];
+#pragma unroll
+    for (int u = 0; u < LW; ++u) {
+      const int b = wave + NW * u;
+      row[u] = b < FB ? a.b + static_cast<int64_t>(min(n0 + b * 8 + crow, a.N - 1)) * a.ldb
+                      : a.a + static_cast<int64_t>(min(m0 + (b - FB) * 8 + crow, a.M - 1)) * a.lda;
+    }
+    constexpr int AHEAD = 2;
+    i32x4 g[AHEAD][LW];
+#pragma unroll
+    for (int p = 0; p < AHEAD; ++p)
+#pragma unroll
+      for (int u = 0; u < LW; ++u) g[p][u] = load_codes(row[u], p * kStageK + cunit, a.K);
+    for (int c0 = 0; c0 < nstages; c0 += AHEAD) {
+#pragma unroll
+      for (int p = 0; p < AHEAD; ++p) {
+        const int c = c0 + p;
+        if (c >= nstages) break;
+        unsigned char* s = smem + (c & 1) * STAGE;
+#pragma unroll
+        for (int u = 0; u < LW; ++u) *reinterpret_cast<i32x4*>(s + (wave + NW * u) * 1024 + lane * 16) = g[p][u];
+        __syncthreads();
+        if ((c + AHEAD + 1) * kStageK <= a.K) {  // uniform: the whole stage lies inside the rows
+#pragma unroll
+          for (int u = 0; u < LW; ++u) __builtin_memcpy(&g[p][u], row[u] + (c + AHEAD) * kStageK + cunit, 16);
+        } else if (c + AHEAD < nstages) {
+#pragma unroll
+          for (int u = 0; u < LW; ++u) g[p][u] = load_codes(row[u], (c + AHEAD) * kStageK + cunit, a.K);
+        }
+        stage_mma(s);
+      }
+    }
+  }
+
+  // Epilogue: each wave turns its tile over in its own part of LDS, so that
+  // whole rows of features go out in 16-byte pieces.
+  constexpr int ES = sizeof(E);
+  constexpr int RC = FF * 16 * ES / 16;               // 16-byte pieces of a token's row
+  constexpr int ROOM = NS * STAGE / NW / (RC * 16);   // token rows that fit
+  constexpr int CT = ROOM >= FT * 16 ? FT : ROOM / 16;  // blocks of 16 tokens at a time
+  static_assert(CT >= 1 && FT % CT == 0 && (RC & (RC - 1)) == 0, "the epilogue's part of LDS");
+  __syncthreads();
+  unsigned char* part = smem + wave * (NS * STAGE / NW);
+  const int nw = n0 + wf * FF * 16, mw = m0 + wt * FT * 16;
+  f4 sb[FF], bi[FF];
+#pragma unroll
+  for (int i = 0; i < FF; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int n = min(nw + i * 16 + 4 * lg + e, a.N - 1);
+      sb[i][e] = a.sb[n];
+      bi[i][e] = a.bias ? a.bias[n] : 0.f;
+    }
+#pragma unroll
+  for (int j0 = 0; j0 < FT; j0 += CT) {
+#pragma unroll
+    for (int jj = 0; jj < CT; ++jj) {
+      const float sa = a.sa[min(mw + (j0 + jj) * 16 + lr, a.M - 1)];
+      unsigned char* pr = part + (jj * 16 + lr) * RC * 16;
+#pragma unroll
+      for (int i = 0; i < FF; ++i) {
+        E e[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) e[q] = static_cast<E>(activate(static_cast<float>(acc[i][j0 + jj][q]) * sa * sb[i][q] + bi[i][q], a.act));
+        const int byte = (i * 16 + 4 * lg) * ES;
+        __builtin_memcpy(__builtin_assume_aligned(pr + (((byte >> 4) ^ (lr & (RC - 1))) << 4) + (byte & 15), 4 * ES), e, 4 * ES);
+      }
+    }
+    // (The wave's own writes and reads of LDS stay in order.)
+#pragma unroll
+    for (int q = 0; q < CT * 16 * RC / 64; ++q) {
+      const int p = q * 64 + lane, t = p / RC, c = p % RC;
+      const int m = mw + j0 * 16 + t, n = nw + c * (16 / ES);
+      const uint4 v = *reinterpret_cast<const uint4*>(part + t * RC * 16 + ((c ^ (t & 15 & (RC - 1))) << 4));
+      if (m < a.M && n < a.N) {
+        E* y = static_cast<E*>(a.y) + static_cast<int64_t>(m) * a.ldy + n;
+        if (vec && n + 16 / ES <= a.N) {
+          *reinterpret_cast<uint4*>(y) = v;
+        } else {
+          const E* e = reinterpret_cast<const E*>(&v);
+#pragma unroll
+          for (int k = 0; k < 16 / ES; ++k)
+            if (n + k < a.N) y[k] = e[k];
+        }
+      }
+    }
+  }
+}
+
+template <int T, int BF, int BT, int WF, int WT, int NS, bool DMA>
+static void go_tile(const IntMatmulArgs& a, hipStream_t s) {
+  const int tf = (a.N + BF - 1) / BF, tt = (a.M + BT - 1) / BT;
+  const int vec = a.ldy * elem_size(T) % 16 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
+  int_matmul_tile_kernel<T, BF, BT, WF, WT, NS, DMA>
+      <<<dim3(static_cast<unsigned>(tf) * tt), WF * WT * 64, 0, s>>>(a, tf, tt, vec);
+}
+
+// Which kernel (times on MI355X, us, rotating inputs):
+//  * up to 64 tokens, or so few 64x64 tiles that most of the chip would idle:
+//    the K-splitting kernel (128x1024x4096: 7.9 against 12.9 for tiles;
+//    64x4096x1024: 5.7 against 6.9);
+//  * the largest tile that still gives the 256 CUs enough workgroups:
+//    256x256 from 192 tiles (8000x4096x1024: 56 against 60 for 128x128;
+//    8000x1024x4096, 128 tiles: 59 against 39), 128x128 from 384 (two
+//    workgroups a CU), 128x64 from 384 (1000x4096x1024: 11.0 against 13.7
+//    and 14.2), else 64x64 (2000x1024x1024: 7.9 against 8.3);
+//  * rows that are not 16-byte aligned go through registers in 64x64 tiles
+//    (689x1504x1504: 10.9 against 9.0 for aligned rows).
+template <int T>
+static void go_int_matmul(const IntMatmulArgs& a, hipStream_t s) {
+  auto tiles = [&](int f, int t) { return static_cast<int64_t>((a.N + f - 1) / f) * ((a.M + t - 1) / t); };
+  const bool dma = a.K % 16 == 0 && a.lda % 16 == 0 && a.ldb % 16 == 0 && a.lda < (1 << 22) && a.ldb < (1 << 22) &&
+                   (reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.b)) % 16 == 0;
+  if (a.M <= 64 || tiles(64, 64) <= 64) {
+    const int vec = a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % (4 * elem_size(T)) == 0;
+    const unsigned gx = (a.N + 15) / 16;
+    if (a.M <= 16)
+      int_matmul_few_kernel<T, 1><<<dim3(gx), 512, 0, s>>>(a, vec);
+    else if (a.M <= 32 || a.M > 64)
+      int_matmul_few_kernel<T, 2><<<dim3(gx, (a.M + 31) / 32), 512, 0, s>>>(a, vec);
+    else
+      int_matmul_few_kernel<T, 4><<<dim3(gx), 512, 0, s>>>(a, vec);
+  } else if (!dma) {
+    go_tile<T, 64, 64, 2, 2, 2, false>(a, s);
+  } else if (tiles(256, 256) >= 192) {
+    go_tile<T, 256, 256, 2, 4, 2, true>(a, s);
+  } else if (tiles(128, 128) >= 384) {
+    go_tile<T, 128, 128, 2, 2, 2, true>(a, s);
+  } else if (tiles(128, 64) >= 384) {
+    go_tile<T, 128, 64, 2, 2, 3, true>(a, s);
+  } else {
+    go_tile<T, 64, 64, 2, 2, 4, true>(a, s);
+  }
 }
 
 hipError_t launch_int_matmul(int dtype, const IntMatmulArgs& a, hipStream_t s) {
-  const dim3 grid((a.N + 255) / 256, (a.M + 15) / 16);
   if (dtype == EL_F32)
-    int_matmul_kernel<EL_F32><<<grid, 256, 0, s>>>(a);
+    go_int_matmul<EL_F32>(a, s);
   else if (dtype == EL_BF16)
-    int_matmul_kernel<EL_BF16><<<grid, 256, 0, s>>>(a);
+    go_int_matmul<EL_BF16>(a, s);
   else
-    int_matmul_kernel<EL_F16><<<grid, 256, 0, s>>>(a);
+    go_int_matmul<EL_F16>(a, s);
   return hipGetLastError();
 }
 

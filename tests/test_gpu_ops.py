@@ -169,6 +169,20 @@ def test_matmul_int(ops, dtype, M, N, K, pad, bias, gelu):
     assert torch.equal(y, V.matmul_int(ops, a, sa, b, sb, bias=bi, gelu=gelu, dtype=dtype))
 
 
+@pytest.mark.parametrize("M,N,K,dtype", [
+    (3331, 3900, 272, BF16), (3331, 3900, 144, F32), (2500, 2500, 400, F16), (2500, 2501, 128, F32),
+    (2000, 1600, 208, BF16), (2000, 1600, 1040, F32), (700, 640, 2064, F16), (1300, 1210, 77, BF16)])
+def test_matmul_int_many_tiles(ops, M, N, K, dtype):
+    """Sizes that fill the chip with every size of tile, with ragged edges."""
+    g = gen(M + N + K)
+    a = torch.randint(-127, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    b = torch.randint(-127, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    sa, sb = torch.rand(M, generator=g, device="cuda"), torch.rand(N, generator=g, device="cuda") / K
+    y = V.matmul_int(ops, a, sa, b, sb, dtype=dtype)
+    ref = (a.double() @ b.double().t()) * sa.double()[:, None] * sb.double()    # integers below 2^53
+    assert ((y.double() - ref).abs() <= (U[dtype] + 4 * E) * ref.abs() + SUB[dtype]).all()
+
+
 def test_matmul_int_misaligned_rows(ops):
     """Rows that start at any address, a row stride that is no multiple of 16."""
     g = gen(3)
