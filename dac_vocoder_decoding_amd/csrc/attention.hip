@@ -37,17 +37,6 @@ __device__ __forceinline__ f16x8 codes_to_f16(uint32_t a, uint32_t b) {
   return u.v;
 }
 
-// Eight consecutive elements as floats.
-template <int T>
-__device__ __forceinline__ void load8(const typename Elem<T>::type* p, float (&v)[8]) {
-  typedef typename Elem<T>::type E;
-  union { uint4 u[sizeof(E) / 2]; E e[8]; } x;
-#pragma unroll
-  for (unsigned i = 0; i < sizeof(E) / 2; ++i) x.u[i] = reinterpret_cast<const uint4*>(p)[i];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(x.e[i]);
-}
-
 // The probabilities enter the matrix cores as p * (page scale / largest page
 // scale so far) * kLift: at most kLift, and far above fp16's subnormals.
 constexpr float kLift = 4096.f;

@@ -7,30 +7,52 @@
 
 namespace voc {
 
-// Workgroup (j, 2 * head + is_value, sequence): the j-th page that the
+// What one workgroup appends to: the page that is its sequence's j-th among
+// those the new tokens touch; tokens [lo, hi) of it are new.
+struct PageShare {
+  int64_t slot;     // page * heads + head
+  int64_t token;    // packed row of token lo
+  int lo, hi;       // hi <= lo: nothing to do
+};
+__device__ __forceinline__ PageShare page_share(const CacheView& c, int b, int j, int head) {
+  PageShare s{0, 0, 0, 0};
+  const Seq q = load_seq(c, b);
+  const int P = 1 << c.page_log;
+  const int64_t column = (q.past >> c.page_log) + static_cast<int64_t>(j);
+  if (column >= c.stride) return s;
+  const int64_t first = column << c.page_log;  // position of the page's first token
+  const int64_t end = static_cast<int64_t>(q.past) + q.count;
+  const int page = c.table[b * c.stride + column];
+  if (end <= first || page < 0 || page >= c.n_pages) return s;
+  s.slot = static_cast<int64_t>(page) * c.heads + head;
+  s.lo = q.past > first ? static_cast<int>(q.past - first) : 0;
+  s.hi = end < first + P ? static_cast<int>(end - first) : P;
+  s.token = q.start + (first + s.lo - q.past);
+  return s;
+}
+
+// The scale that covers a page's older tokens (none: 0) and its new ones.
+__device__ __forceinline__ float joint_scale(float old, uint32_t top) {
+  const float own = scale_of_bits(top);
+  return !(old == old) ? old : !(own == own) ? own : fmaxf(old, own);
+}
+
+// Any alignment, and few new tokens.  Workgroup (j, 2 * head + is_value, sequence): the j-th page that the
 // sequence's new tokens touch.  Values are stored transposed inside a page.
 template <int T>
 __global__ __launch_bounds__(256) void append_kernel(const AppendArgs a) {
   typedef typename Elem<T>::type E;
   __shared__ uint32_t s_max[4];
   const int tid = threadIdx.x;
-  const Seq q = load_seq(a.c, blockIdx.z);
   const int head = blockIdx.y >> 1;
   const bool value = blockIdx.y & 1;
   const int P = 1 << a.c.page_log, D = a.D;
-  const int64_t column = (q.past >> a.c.page_log) + static_cast<int64_t>(blockIdx.x);
-  if (column >= a.c.stride) return;
-  const int64_t first = column << a.c.page_log;           // position of the page's first token
-  const int64_t end = static_cast<int64_t>(q.past) + q.count;
-  const int lo = q.past > first ? static_cast<int>(q.past - first) : 0;   // [lo, hi): new tokens
-  const int hi = end < first + P ? static_cast<int>(end - first) : P;
+  const PageShare sh = page_share(a.c, blockIdx.z, blockIdx.x, head);
+  const int lo = sh.lo, hi = sh.hi;
   if (hi <= lo) return;
-  const int page = a.c.table[blockIdx.z * a.c.stride + column];
-  if (page < 0 || page >= a.c.n_pages) return;
-  const int64_t slot = static_cast<int64_t>(page) * a.c.heads + head;
-  const E* src = value ? static_cast<const E*>(a.v) + head * a.v_h : static_cast<const E*>(a.k) + head * a.k_h;
+  const int64_t slot = sh.slot;
   const int64_t st = value ? a.v_t : a.k_t;
-  src += (q.start + (first + lo - q.past)) * st;
+  const E* src = (value ? static_cast<const E*>(a.v) + head * a.v_h : static_cast<const E*>(a.k) + head * a.k_h) + sh.token * st;
   int8_t* codes = (value ? a.c.v : a.c.k) + slot * P * D;
   float* scales = value ? a.c.vs : a.c.ks;
 
@@ -45,8 +67,7 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendArgs a) {
   const float old = lo ? scales[slot] : 0.f;
   __syncthreads();
   top = max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3]));
-  const float own = scale_of_bits(top);
-  const float scale = !(old == old) ? old : !(own == own) ? own : fmaxf(old, own);
+  const float scale = joint_scale(old, top);
   const float inv = inverse_of(scale);
   if (lo && scale != old) {
     const float ratio = inv > 0.f ? old * inv : 0.f;
@@ -63,15 +84,155 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendArgs a) {
   if (tid == 0) scales[slot] = scale;
 }
 
-hipError_t launch_append(int dtype, const AppendArgs& a, hipStream_t s) {
+// Many new tokens, rows of 16-byte multiples.  The page's image is built in
+// LDS and written whole, 16 bytes at a time: a value page is turned over
+// there, four tokens of one d to a 32-bit word.  The new rows stay in
+// registers between the maximum and the codes where a thread has up to four
+// units (4 tokens x 8 values); larger pages read the rest a second time.
+// LDS: a key page [token][D], a value page [d][token] with rows of P + 4
+// bytes (the writes of neighbouring d then fall on different banks).
+template <int T>
+__global__ __launch_bounds__(256) void append_page_kernel(const AppendArgs a) {
+  typedef typename Elem<T>::type E;
+  constexpr int KEEP = T == EL_F32 ? 1 : 2;
+  extern __shared__ __attribute__((aligned(16))) unsigned char s_page[];
+  __shared__ uint32_t s_max[4];
+  const int tid = threadIdx.x;
+  const int head = blockIdx.y >> 1;
+  const bool value = blockIdx.y & 1;
+  const int P = 1 << a.c.page_log, D = a.D;
+  const PageShare sh = page_share(a.c, blockIdx.z, blockIdx.x, head);
+  const int lo = sh.lo, hi = sh.hi;
+  if (hi <= lo) return;
+  const int64_t st = value ? a.v_t : a.k_t;
+  const E* src = (value ? static_cast<const E*>(a.v) + head * a.v_h : static_cast<const E*>(a.k) + head * a.k_h) +
+                 (sh.token - lo) * st;  // row t of the page (t >= lo)
+  int8_t* codes = (value ? a.c.v : a.c.k) + sh.slot * P * D;
+  float* scales = value ? a.c.vs : a.c.ks;
+  const float old = lo ? scales[sh.slot] : 0.f;
+
+  const int D8 = D >> 3, units = (P >> 2) * D8;
+  float keep[KEEP][4][8];
+  uint32_t top = 0;
+  auto load_unit = [&](int u, float (&v)[4][8]) {
+    const int t4 = u / D8 * 4, d8 = u % D8 * 8;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if (t4 + t >= lo && t4 + t < hi) {
+        load8<T>(src + (t4 + t) * st + d8, v[t]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[t][k] = 0.f;
+      }
+    }
+  };
+  auto raise = [&](const float (&v)[4][8]) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = max(top, abs_bits(v[t][k]));
+  };
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i)
+    if (tid + i * 256 < units) {
+      load_unit(tid + i * 256, keep[i]);
+      raise(keep[i]);
+    }
+  for (int u = tid + KEEP * 256; u < units; u += 256) {
+    float v[4][8];
+    load_unit(u, v);
+    raise(v);
+  }
+  top = wave_max(top);
+  if ((tid & 63) == 0) s_max[tid >> 6] = top;
+  // The page as it is, where some of it stays.
+  const int pitch = value ? P + 4 : D;  // bytes of a row of the image
+  const int words = value ? P >> 2 : D >> 2;
+  if (lo > 0 || hi < P) {
+    for (int w = tid; w < (P * D) >> 2; w += 256)
+      *reinterpret_cast<uint32_t*>(s_page + w / words * pitch + w % words * 4) = reinterpret_cast<const uint32_t*>(codes)[w];
+  }
+  __syncthreads();
+  top = max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3]));
+  const float scale = joint_scale(old, top), inv = inverse_of(scale);
+  if (lo && scale != old) {
+    const float ratio = inv > 0.f ? old * inv : 0.f;
+    for (int i = tid; i < lo * D; i += 256) {
+      const int t = value ? i % lo : i / D, d = value ? i / lo : i % D;
+      int8_t* p = reinterpret_cast<int8_t*>(s_page) + (value ? d * pitch + t : t * pitch + d);
+      *p = static_cast<int8_t>(__builtin_rintf(static_cast<float>(*p) * ratio));
+    }
+    __syncthreads();
+  }
+  auto put = [&](int u, const float (&v)[4][8]) {
+    const int t4 = u / D8 * 4, d8 = u % D8 * 8;
+    if (t4 + 4 <= lo || t4 >= hi) return;
+    uint2 c[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) c[t] = codes8(v[t], inv);
+    if (!value) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (t4 + t >= lo && t4 + t < hi) *reinterpret_cast<uint2*>(s_page + (t4 + t) * pitch + d8) = c[t];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) w |= (((k < 4 ? c[t].x : c[t].y) >> (8 * (k & 3))) & 0xffu) << (8 * t);
+        unsigned char* p = s_page + (d8 + k) * pitch + t4;
+        if (t4 >= lo && t4 + 4 <= hi) {
+          *reinterpret_cast<uint32_t*>(p) = w;
+        } else {
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            if (t4 + t >= lo && t4 + t < hi) p[t] = static_cast<unsigned char>(w >> (8 * t));
+        }
+      }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i)
+    if (tid + i * 256 < units) put(tid + i * 256, keep[i]);
+  for (int u = tid + KEEP * 256; u < units; u += 256) {
+    float v[4][8];
+    load_unit(u, v);
+    put(u, v);
+  }
+  __syncthreads();
+  for (int w = tid; w < (P * D) >> 4; w += 256) {
+    const int r = w / (words >> 2), c = w % (words >> 2) * 16;
+    uint4 v;
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(s_page + r * pitch + c);
+    v.x = p[0];
+    v.y = p[1];
+    v.z = p[2];
+    v.w = p[3];
+    reinterpret_cast<uint4*>(codes)[w] = v;
+  }
+  if (tid == 0) scales[sh.slot] = scale;
+}
+
+template <int T>
+static void go_append(const AppendArgs& a, hipStream_t s) {
   const int P = 1 << a.c.page_log;
   const dim3 grid((a.c.max_new + P - 1) / P + 1, 2 * a.c.heads, a.batch);
-  if (dtype == EL_F32)
-    append_kernel<EL_F32><<<grid, 256, 0, s>>>(a);
-  else if (dtype == EL_BF16)
-    append_kernel<EL_BF16><<<grid, 256, 0, s>>>(a);
+  constexpr int per16 = 16 / sizeof(typename Elem<T>::type);
+  const bool vec = (reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) % 16 == 0 &&
+                   (a.k_t | a.k_h | a.v_t | a.v_h) % per16 == 0;
+  if (vec && a.c.max_new > 4)
+    append_page_kernel<T><<<grid, 256, static_cast<size_t>(a.D) * (P + 4), s>>>(a);
   else
-    append_kernel<EL_F16><<<grid, 256, 0, s>>>(a);
+    append_kernel<T><<<grid, 256, 0, s>>>(a);
+}
+
+hipError_t launch_append(int dtype, const AppendArgs& a, hipStream_t s) {
+  if (dtype == EL_F32)
+    go_append<EL_F32>(a, s);
+  else if (dtype == EL_BF16)
+    go_append<EL_BF16>(a, s);
+  else
+    go_append<EL_F16>(a, s);
   return hipGetLastError();
 }
 

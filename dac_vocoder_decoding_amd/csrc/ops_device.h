@@ -15,6 +15,26 @@ template <> struct Elem<EL_F32> { typedef float type; };
 template <> struct Elem<EL_BF16> { typedef __bf16 type; };
 template <> struct Elem<EL_F16> { typedef _Float16 type; };
 
+// Eight consecutive elements (16-byte aligned) as floats, and back.
+template <int T>
+__device__ __forceinline__ void load8(const typename Elem<T>::type* p, float (&v)[8]) {
+  typedef typename Elem<T>::type E;
+  union { uint4 u[sizeof(E) / 2]; E e[8]; } x;
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(E) / 2; ++i) x.u[i] = reinterpret_cast<const uint4*>(p)[i];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(x.e[i]);
+}
+template <int T>
+__device__ __forceinline__ void store8(typename Elem<T>::type* p, const float (&v)[8]) {
+  typedef typename Elem<T>::type E;
+  union { uint4 u[sizeof(E) / 2]; E e[8]; } x;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x.e[i] = static_cast<E>(v[i]);
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(E) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = x.u[i];
+}
+
 // The scale of a group whose largest magnitude has the bit pattern `bits`
 // (magnitudes compare like their bits, with NaN above infinity above every
 // finite value, so an integer maximum carries a NaN along).
@@ -33,6 +53,18 @@ __device__ __forceinline__ int code_of(float v, float inv) {
   // inv is 0 where the group holds an infinity: 0 times it must not become a code.
   const float r = inv > 0.f ? __builtin_rintf(v * inv) : 0.f;
   return static_cast<int>(fminf(fmaxf(r, -127.f), 127.f));
+}
+
+// Eight codes in a row.
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    w[h] = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[h] |= (static_cast<uint32_t>(code_of(v[4 * h + i], inv)) & 0xffu) << (8 * i);
+  }
+  return make_uint2(w[0], w[1]);
 }
 
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {

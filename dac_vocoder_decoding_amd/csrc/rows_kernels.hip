@@ -7,71 +7,181 @@
 
 namespace voc {
 
-// One workgroup per row; NPT values of the row per thread stay in registers
-// between the sum of squares, the maximum and the codes.
-template <int T, int NPT>
+// Group g (eight values) of a row of C: 16-byte loads and stores where the
+// rows allow them (VEC), else whole groups at any alignment and the last,
+// partial one value by value (what is missing reads as zero).
+template <int T, bool VEC>
+__device__ __forceinline__ void load_group(const typename Elem<T>::type* row, int g, int C, float (&v)[8]) {
+  typedef typename Elem<T>::type E;
+  if constexpr (VEC) {
+    load8<T>(row + g * 8, v);
+  } else {
+    E e[8];
+    if (g * 8 + 8 <= C) {
+      __builtin_memcpy(e, row + g * 8, 8 * sizeof(E));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) e[k] = g * 8 + k < C ? row[g * 8 + k] : static_cast<E>(0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = static_cast<float>(e[k]);
+  }
+}
+template <int T, bool VEC>
+__device__ __forceinline__ void store_group(typename Elem<T>::type* row, int g, int C, const float (&v)[8]) {
+  typedef typename Elem<T>::type E;
+  if constexpr (VEC) {
+    store8<T>(row + g * 8, v);
+  } else {
+    E e[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] = static_cast<E>(v[k]);
+    if (g * 8 + 8 <= C) {
+      __builtin_memcpy(row + g * 8, e, 8 * sizeof(E));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (g * 8 + k < C) row[g * 8 + k] = e[k];
+    }
+  }
+}
+
+// NG groups of eight values per thread, all in registers, so that every row
+// is read once.  WPR waves per row: one (four
+// rows a workgroup, no barrier) up to 2048 values, four above.  A workgroup
+// goes on with the row that is a grid further, so that its weights are read
+// once.  The sums' order does not depend on the rows' alignment (VEC).
+template <int T, int NG, int WPR, bool VEC>
 __global__ __launch_bounds__(256) void rows_kernel(const RowsArgs a) {
   typedef typename Elem<T>::type E;
-  __shared__ float s_sum[4];
-  __shared__ uint32_t s_max[4];
+  __shared__ float s_sum[2][4];
+  __shared__ uint32_t s_max[2][4];
   const int tid = threadIdx.x, wave = tid >> 6;
-  const int64_t row = blockIdx.x;
-  const E* x = static_cast<const E*>(a.x) + row * a.ldx;
-  const E* r = a.r ? static_cast<const E*>(a.r) + row * a.ldr : nullptr;
-  E* h = a.h ? static_cast<E*>(a.h) + row * a.ldh : nullptr;
-  float v[NPT];
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < NPT; ++i) {
-    const int c = tid + i * 256;
-    v[i] = 0.f;
-    if (c < a.C) {
-      float f = static_cast<float>(x[c]);
-      if (r) f = static_cast<float>(static_cast<E>(f + static_cast<float>(r[c])));
-      if (h) h[c] = static_cast<E>(f);
-      v[i] = f;
-      sum += f * f;
-    }
-  }
-  uint32_t top = 0;
+  const int at = WPR == 1 ? tid & 63 : tid;    // this thread's first group
+  constexpr int STEP = WPR * 64;
+  const int groups = (a.C + 7) >> 3;
+  float w[NG][8];
   if (a.weight) {
-    sum = wave_sum(sum);
-    if ((tid & 63) == 0) s_sum[wave] = sum;
-    __syncthreads();
-    sum = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
-    const float rms = rsqrtf(sum / static_cast<float>(a.C) + a.eps);
-    if (abs_bits(sum) >= kInfBits) top = kInfBits;
 #pragma unroll
-    for (int i = 0; i < NPT; ++i) {
-      const int c = tid + i * 256;
-      if (c < a.C) v[i] = v[i] * rms * a.weight[c];
+    for (int i = 0; i < NG; ++i)
+      if (at + i * STEP < groups) load_group<EL_F32, VEC>(a.weight, at + i * STEP, a.C, w[i]);
+  }
+  int turn = 0;
+  for (int64_t row = WPR == 1 ? static_cast<int64_t>(blockIdx.x) * 4 + wave : blockIdx.x; row < a.rows;
+       row += WPR == 1 ? static_cast<int64_t>(gridDim.x) * 4 : gridDim.x, turn ^= 1) {
+    const E* x = static_cast<const E*>(a.x) + row * a.ldx;
+    float v[NG][8];
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      if (at + i * STEP < groups) {
+        load_group<T, VEC>(x, at + i * STEP, a.C, v[i]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+      }
     }
-  }
+    if (a.r) {
+      const E* r = static_cast<const E*>(a.r) + row * a.ldr;
 #pragma unroll
-  for (int i = 0; i < NPT; ++i) top = max(top, abs_bits(v[i]));
-  top = wave_max(top);
-  if ((tid & 63) == 0) s_max[wave] = top;
-  __syncthreads();
-  top = max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3]));
-  const float scale = scale_of_bits(top), inv = inverse_of(scale);
-  if (tid == 0) a.scale[row] = scale;
-  int8_t* q = a.q + row * a.ldq;
+      for (int i = 0; i < NG; ++i) {
+        if (at + i * STEP < groups) {
+          float f[8];
+          load_group<T, VEC>(r, at + i * STEP, a.C, f);
 #pragma unroll
-  for (int i = 0; i < NPT; ++i) {
-    const int c = tid + i * 256;
-    if (c < a.C) q[c] = static_cast<int8_t>(code_of(v[i], inv));
+          for (int k = 0; k < 8; ++k) v[i][k] = static_cast<float>(static_cast<E>(v[i][k] + f[k]));
+        }
+      }
+    }
+    if (a.h) {
+      E* h = static_cast<E*>(a.h) + row * a.ldh;
+#pragma unroll
+      for (int i = 0; i < NG; ++i)
+        if (at + i * STEP < groups) store_group<T, VEC>(h, at + i * STEP, a.C, v[i]);
+    }
+    uint32_t top = 0;
+    if (a.weight) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NG; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum += v[i][k] * v[i][k];
+      sum = wave_sum(sum);
+      if constexpr (WPR > 1) {
+        if ((tid & 63) == 0) s_sum[turn][wave] = sum;
+        __syncthreads();
+        sum = (s_sum[turn][0] + s_sum[turn][1]) + (s_sum[turn][2] + s_sum[turn][3]);
+      }
+      const float rms = rsqrtf(sum / static_cast<float>(a.C) + a.eps);
+      if (abs_bits(sum) >= kInfBits) top = kInfBits;
+#pragma unroll
+      for (int i = 0; i < NG; ++i)
+        if (at + i * STEP < groups) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[i][k] = v[i][k] * rms * w[i][k];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = max(top, abs_bits(v[i][k]));
+    top = wave_max(top);
+    if constexpr (WPR > 1) {
+      if ((tid & 63) == 0) s_max[turn][wave] = top;
+      __syncthreads();
+      top = max(max(s_max[turn][0], s_max[turn][1]), max(s_max[turn][2], s_max[turn][3]));
+    }
+    const float scale = scale_of_bits(top), inv = inverse_of(scale);
+    if (at == 0) a.scale[row] = scale;
+    int8_t* q = a.q + row * a.ldq;
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+      if (at + i * STEP < groups) {
+        const int c = (at + i * STEP) * 8;
+        const uint2 u = codes8(v[i], inv);
+        if (VEC) {
+          *reinterpret_cast<uint2*>(q + c) = u;
+        } else if (c + 8 <= a.C) {
+          __builtin_memcpy(q + c, &u, 8);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (c + k < a.C) q[c + k] = static_cast<int8_t>((k < 4 ? u.x : u.y) >> (8 * (k & 3)));
+        }
+      }
   }
+}
+
+template <int T, bool VEC>
+static void pick_rows(const RowsArgs& a, hipStream_t s) {
+  // Enough workgroups to fill every CU eight times over.
+  const int64_t most = 2048;
+  const dim3 one(static_cast<unsigned>(a.rows < most ? a.rows : most));
+  const dim3 four(static_cast<unsigned>((a.rows + 3) / 4 < most ? (a.rows + 3) / 4 : most));
+  if (a.C <= 512)
+    rows_kernel<T, 1, 1, VEC><<<four, 256, 0, s>>>(a);
+  else if (a.C <= 1024)
+    rows_kernel<T, 2, 1, VEC><<<four, 256, 0, s>>>(a);
+  else if (a.C <= 2048)
+    rows_kernel<T, 4, 1, VEC><<<four, 256, 0, s>>>(a);
+  else if (a.C <= 4096)
+    rows_kernel<T, 2, 4, VEC><<<one, 256, 0, s>>>(a);
+  else if (a.C <= 8192)
+    rows_kernel<T, 4, 4, VEC><<<one, 256, 0, s>>>(a);
+  else
+    rows_kernel<T, 8, 4, VEC><<<one, 256, 0, s>>>(a);
 }
 
 template <int T>
 static void go_rows(const RowsArgs& a, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(a.rows));
-  if (a.C <= 1024)
-    rows_kernel<T, 4><<<grid, 256, 0, s>>>(a);
-  else if (a.C <= 4096)
-    rows_kernel<T, 16><<<grid, 256, 0, s>>>(a);
+  auto on16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  constexpr int per16 = 16 / sizeof(typename Elem<T>::type);
+  const bool vec = a.C % 8 == 0 && on16(a.x) && on16(a.r) && on16(a.h) && on16(a.weight) &&
+                   reinterpret_cast<uintptr_t>(a.q) % 8 == 0 && a.ldx % per16 == 0 && a.ldr % per16 == 0 &&
+                   a.ldh % per16 == 0 && a.ldq % 8 == 0;
+  if (vec)
+    pick_rows<T, true>(a, s);
   else
-    rows_kernel<T, 64><<<grid, 256, 0, s>>>(a);
+    pick_rows<T, false>(a, s);
 }
 
 hipError_t launch_rows(int dtype, const RowsArgs& a, hipStream_t s) {
