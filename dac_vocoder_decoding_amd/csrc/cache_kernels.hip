@@ -89,18 +89,22 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendArgs a) {
 // there, four tokens of one d to a 32-bit word.  The new rows stay in
 // registers between the maximum and the codes where a thread has up to four
 // units (4 tokens x 8 values); larger pages read the rest a second time.
+// A page of 32 x 128 is 128 units: two waves a workgroup.
 // LDS: a key page [token][D], a value page [d][token] with rows of P + 4
 // bytes (the writes of neighbouring d then fall on different banks).
-template <int T>
-__global__ __launch_bounds__(256) void append_page_kernel(const AppendArgs a) {
+constexpr int kPageThreads = 128;
+
+template <int T, int D>
+__global__ __launch_bounds__(kPageThreads) void append_page_kernel(const AppendArgs a) {
   typedef typename Elem<T>::type E;
-  constexpr int KEEP = T == EL_F32 ? 1 : 2;
+  constexpr int KEEP = 2, NT = kPageThreads;
+  constexpr int D8 = D >> 3;
   extern __shared__ __attribute__((aligned(16))) unsigned char s_page[];
-  __shared__ uint32_t s_max[4];
+  __shared__ uint32_t s_max[NT / 64];
   const int tid = threadIdx.x;
   const int head = blockIdx.y >> 1;
   const bool value = blockIdx.y & 1;
-  const int P = 1 << a.c.page_log, D = a.D;
+  const int P = 1 << a.c.page_log;
   const PageShare sh = page_share(a.c, blockIdx.z, blockIdx.x, head);
   const int lo = sh.lo, hi = sh.hi;
   if (hi <= lo) return;
@@ -111,7 +115,7 @@ __global__ __launch_bounds__(256) void append_page_kernel(const AppendArgs a) {
   float* scales = value ? a.c.vs : a.c.ks;
   const float old = lo ? scales[sh.slot] : 0.f;
 
-  const int D8 = D >> 3, units = (P >> 2) * D8;
+  const int units = (P >> 2) * D8;
   float keep[KEEP][4][8];
   uint32_t top = 0;
   auto load_unit = [&](int u, float (&v)[4][8]) {
@@ -134,11 +138,11 @@ __global__ __launch_bounds__(256) void append_page_kernel(const AppendArgs a) {
   };
 #pragma unroll
   for (int i = 0; i < KEEP; ++i)
-    if (tid + i * 256 < units) {
-      load_unit(tid + i * 256, keep[i]);
+    if (tid + i * NT < units) {
+      load_unit(tid + i * NT, keep[i]);
       raise(keep[i]);
     }
-  for (int u = tid + KEEP * 256; u < units; u += 256) {
+  for (int u = tid + KEEP * NT; u < units; u += NT) {
     float v[4][8];
     load_unit(u, v);
     raise(v);
@@ -147,17 +151,18 @@ __global__ __launch_bounds__(256) void append_page_kernel(const AppendArgs a) {
   if ((tid & 63) == 0) s_max[tid >> 6] = top;
   // The page as it is, where some of it stays.
   const int pitch = value ? P + 4 : D;  // bytes of a row of the image
-  const int words = value ? P >> 2 : D >> 2;
+  // Words of a row, as a shift (a key page is one long row: its image is the page).
+  const int row_log = a.c.page_log - 2;
   if (lo > 0 || hi < P) {
-    for (int w = tid; w < (P * D) >> 2; w += 256)
-      *reinterpret_cast<uint32_t*>(s_page + w / words * pitch + w % words * 4) = reinterpret_cast<const uint32_t*>(codes)[w];
+    for (int w = tid; w < (P * D) >> 2; w += NT)
+      *reinterpret_cast<uint32_t*>(s_page + w * 4 + (value ? (w >> row_log) * 4 : 0)) = reinterpret_cast<const uint32_t*>(codes)[w];
   }
   __syncthreads();
-  top = max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3]));
+  top = max(s_max[0], s_max[1]);
   const float scale = joint_scale(old, top), inv = inverse_of(scale);
   if (lo && scale != old) {
     const float ratio = inv > 0.f ? old * inv : 0.f;
-    for (int i = tid; i < lo * D; i += 256) {
+    for (int i = tid; i < lo * D; i += NT) {
       const int t = value ? i % lo : i / D, d = value ? i / lo : i % D;
       int8_t* p = reinterpret_cast<int8_t*>(s_page) + (value ? d * pitch + t : t * pitch + d);
       *p = static_cast<int8_t>(__builtin_rintf(static_cast<float>(*p) * ratio));
@@ -193,17 +198,16 @@ __global__ __launch_bounds__(256) void append_page_kernel(const AppendArgs a) {
   };
 #pragma unroll
   for (int i = 0; i < KEEP; ++i)
-    if (tid + i * 256 < units) put(tid + i * 256, keep[i]);
-  for (int u = tid + KEEP * 256; u < units; u += 256) {
+    if (tid + i * NT < units) put(tid + i * NT, keep[i]);
+  for (int u = tid + KEEP * NT; u < units; u += NT) {
     float v[4][8];
     load_unit(u, v);
     put(u, v);
   }
   __syncthreads();
-  for (int w = tid; w < (P * D) >> 4; w += 256) {
-    const int r = w / (words >> 2), c = w % (words >> 2) * 16;
+  for (int w = tid; w < (P * D) >> 4; w += NT) {
     uint4 v;
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(s_page + r * pitch + c);
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(s_page + w * 16 + (value ? (w >> (row_log - 2)) * 4 : 0));
     v.x = p[0];
     v.y = p[1];
     v.z = p[2];
@@ -220,10 +224,21 @@ static void go_append(const AppendArgs& a, hipStream_t s) {
   constexpr int per16 = 16 / sizeof(typename Elem<T>::type);
   const bool vec = (reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) % 16 == 0 &&
                    (a.k_t | a.k_h | a.v_t | a.v_h) % per16 == 0;
-  if (vec && a.c.max_new > 4)
-    append_page_kernel<T><<<grid, 256, static_cast<size_t>(a.D) * (P + 4), s>>>(a);
-  else
+  if (!vec || a.c.max_new <= 4) {
     append_kernel<T><<<grid, 256, 0, s>>>(a);
+    return;
+  }
+  const size_t lds = static_cast<size_t>(a.D) * (P + 4);
+  switch (a.D / 32) {
+    case 1: append_page_kernel<T, 32><<<grid, kPageThreads, lds, s>>>(a); break;
+    case 2: append_page_kernel<T, 64><<<grid, kPageThreads, lds, s>>>(a); break;
+    case 3: append_page_kernel<T, 96><<<grid, kPageThreads, lds, s>>>(a); break;
+    case 4: append_page_kernel<T, 128><<<grid, kPageThreads, lds, s>>>(a); break;
+    case 5: append_page_kernel<T, 160><<<grid, kPageThreads, lds, s>>>(a); break;
+    case 6: append_page_kernel<T, 192><<<grid, kPageThreads, lds, s>>>(a); break;
+    case 7: append_page_kernel<T, 224><<<grid, kPageThreads, lds, s>>>(a); break;
+    default: append_page_kernel<T, 256><<<grid, kPageThreads, lds, s>>>(a); break;
+  }
 }
 
 hipError_t launch_append(int dtype, const AppendArgs& a, hipStream_t s) {
