@@ -20,6 +20,7 @@
 //
 // Codes become fp16 exactly: the byte, its sign bit flipped, as the low
 // mantissa byte of 1024 + u, minus 1152.
+#include "gemm_common.h"
 #include "ops_device.h"
 
 namespace voc {
@@ -38,17 +39,20 @@ __device__ __forceinline__ f16x8 codes_to_f16(uint32_t a, uint32_t b) {
 }
 
 // The probabilities enter the matrix cores as p * (page scale / largest page
-// scale so far) * kLift: at most kLift, and far above fp16's subnormals.
-constexpr float kLift = 4096.f;
+// scale so far) * kLift with p = 2^(s - m).  m follows the row's maximum
+// only when that has moved past it by more than kSlack (a factor of 8), so
+// p reaches at most 2^kSlack; both keep the products inside fp16 and far
+// above its subnormals.
+constexpr float kLift = 4096.f, kSlack = 3.f;
 
-constexpr int kTileRows = 16, kBlockKeys = 64;
+constexpr int kBlockKeys = 64;
 
 // The share of one workgroup: rows r0 .. r0 + nrows - 1 of (sequence, cache
 // head), keys of [lo, hi) in blocks of 64 from kb0.
 struct Share {
-  int r0, nrows, total, kb0, lo, hi;
+  int r0, nrows, total, kb0, lo, hi, blk0, blk1;
 };
-__device__ __forceinline__ Share share_of(const AttendArgs& a, const Seq& s, int tile, int tile_rows) {
+__device__ __forceinline__ Share share_of(const AttendArgs& a, const Seq& s, int tile, int tile_rows, int part, int parts) {
   Share h;
   const int rows = s.count * a.group;
   h.r0 = tile * tile_rows;
@@ -63,22 +67,132 @@ __device__ __forceinline__ Share share_of(const AttendArgs& a, const Seq& s, int
     if (a.causal) h.hi = min(h.total, s.past + i_hi + 1);
   }
   h.kb0 = h.lo & ~(kBlockKeys - 1);
+  const int nblk = h.hi > h.lo ? (h.hi - h.kb0 + kBlockKeys - 1) / kBlockKeys : 0;
+  const int per = (nblk + parts - 1) / parts;
+  h.blk0 = min(nblk, part * per);
+  h.blk1 = min(nblk, h.blk0 + per);
   return h;
 }
 
-// Workgroup: 16 rows, one part of the keys; its four waves take every fourth
-// block of 64 keys and are joined in order at the end.  parts > 1: the
-// results go to the workspace (unnormalised, with their maxima and sums) for
-// join_kernel.
+// The keys [lo, hi) that query row r of a share sees.
+struct Sight {
+  int lo, hi;
+};
+__device__ __forceinline__ Sight sight_of(const AttendArgs& a, const Seq& s, int total, int row) {
+  const int pos = s.past + row / a.group;
+  return Sight{a.window ? max(0, pos - a.window + 1) : 0, a.causal ? min(pos + 1, total) : total};
+}
+
+// One query row as matrix-core operands: the row times a power of two that
+// brings its largest value to [2^14, 2^15), in NT fp16 terms.  Returns the
+// factor of its scores.  DOF(c): this lane's first d of fragment c.
+template <int T, int DC, int NT, typename FD>
+__device__ __forceinline__ float load_query(const typename Elem<T>::type* qp, float scale, f16x8 (&qf)[NT][DC], FD dof) {
+  float v[DC][8];
+  uint32_t top = 0;
+#pragma unroll
+  for (int c = 0; c < DC; ++c) {
+    load8<T>(qp + dof(c), v[c]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, abs_bits(v[c][i]));
+  }
+  top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
+  top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
+  const uint32_t e = max(top >> 23, 15u);
+  // A negative softmax scale goes into the query: the factor stays positive.
+  const float up = copysignf(__uint_as_float((268u - e) << 23), scale), down = __uint_as_float((e - 14u) << 23);
+#pragma unroll
+  for (int c = 0; c < DC; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float f = v[c][i] * up;
+      const _Float16 hi = static_cast<_Float16>(f);
+      qf[0][c][i] = hi;
+      if constexpr (NT > 1) qf[1][c][i] = static_cast<_Float16>(f - static_cast<float>(hi));
+    }
+  return fabsf(scale) * down;
+}
+
+// What a wave carries along for 16 query rows (a lane: row lr, the sum over
+// its own keys only).  vref is the largest page scale so far.
+struct RowState {
+  float m = -INFINITY, l = 0.f, vref = 0.f;
+};
+
+// The probabilities of 16 keys (this lane's, of one page group with scales
+// ks, vs) as operands of the second product; rescales what was summed when m
+// or vref has to move.  all: every key is visible; else keys key0 .. key0+15
+// count where `in` and inside the row's sight.
+template <int NT, int NA>
+__device__ __forceinline__ void probabilities(const f32x4 (&st)[4], float ks, float vs, float cq, bool all, bool in,
+                                              int key0, const Sight& see, RowState& r, f32x4 (&acc)[NA],
+                                              f16x8 (&pf)[NT][2]) {
+  const float sc = ks * cq;
+  uint32_t seen = 0xffffu;
+  float top = -INFINITY;
+  if (all) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) top = fmaxf(top, st[j >> 2][j & 3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const bool s = in && key0 + j >= see.lo && key0 + j < see.hi;
+      if (!s) seen &= ~(1u << j);
+      top = s ? fmaxf(top, st[j >> 2][j & 3]) : top;
+    }
+  }
+  top *= sc;  // NaN where nothing is seen and sc is 0: no comparison holds
+  if (__any(top > r.m + kSlack || vs > r.vref)) {
+    float t = fmaxf(top, __shfl_xor(top, 16));
+    t = fmaxf(t, __shfl_xor(t, 32));
+    float v = fmaxf(vs, __shfl_xor(vs, 16));
+    v = fmaxf(v, __shfl_xor(v, 32));
+    const float m = t > r.m + kSlack ? t : r.m;
+    const float vref = fmaxf(r.vref, v);
+    const float alpha = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(r.m - m);
+    const float beta = vref > 0.f ? alpha * (r.vref / vref) : alpha;
+    r.m = m;
+    r.vref = vref;
+    r.l *= alpha;
+#pragma unroll
+    for (int i = 0; i < NA; ++i) acc[i] *= beta;
+  }
+  const float vf = r.vref > 0.f ? vs * (kLift / r.vref) : vs;
+  float w[16], sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    float p = __builtin_amdgcn_exp2f(fmaf(st[j >> 2][j & 3], sc, -r.m));
+    w[j] = p * vf;
+    if (!all) {
+      const bool s = (seen >> j) & 1u;
+      p = s ? p : 0.f;
+      w[j] = s ? w[j] : 0.f;
+    }
+    sum[j & 3] += p;
+  }
+  r.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const _Float16 hi = static_cast<_Float16>(w[j]);
+    pf[0][j >> 3][j & 7] = hi;
+    if constexpr (NT > 1) pf[1][j >> 3][j & 7] = static_cast<_Float16>(w[j] - static_cast<float>(hi));
+  }
+}
+
+// Few query rows.  Workgroup: 16 rows, one part of the keys; its four waves
+// take every fourth block of 64 keys, operands straight from memory, and are
+// joined in order at the end.  parts > 1: the results go to the workspace
+// (unnormalised, with their maxima and sums) for join_kernel.
+constexpr int kFewRows = 16;
+
 template <int T, int DC>
-__global__ __launch_bounds__(256) void attend_kernel(const AttendArgs a, int tiles, int parts) {
+__global__ __launch_bounds__(256) void attend_few_kernel(const AttendArgs a, int tiles, int parts) {
   typedef typename Elem<T>::type E;
   constexpr int D = DC * 32, NC = DC / 2, REM = DC & 1;
-  constexpr bool TWO = T == EL_F32;
-  constexpr int NT = TWO ? 2 : 1;
+  constexpr int NT = T == EL_F32 ? 2 : 1;
   constexpr int PITCH = D + 4;
-  __shared__ float s_o[kTileRows * PITCH];
-  __shared__ float s_m[4][kTileRows], s_l[4][kTileRows];
+  __shared__ float s_o[kFewRows * PITCH];
+  __shared__ float s_m[4][kFewRows], s_l[4][kFewRows];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -89,61 +203,30 @@ __global__ __launch_bounds__(256) void attend_kernel(const AttendArgs a, int til
   const int tile = id % tiles;
   const int head = id / tiles % a.c.heads, b = id / tiles / a.c.heads;
   const Seq sq = load_seq(a.c, b);
-  const Share sh = share_of(a, sq, tile, kTileRows);
+  const Share sh = share_of(a, sq, tile, kFewRows, part, parts);
   if (sh.nrows <= 0) return;
 
-  // This lane's query row.
+  // This lane's query row (past the last one: the last one again).  A lane's
+  // operands are 16 consecutive d of 64, then 8 of the last 32.
   const int row = sh.r0 + min(lr, sh.nrows - 1);
-  const int qi = row / a.group, qh = head * a.group + row % a.group;
-  const int pos = sq.past + qi;
-  const int row_hi = a.causal ? min(pos + 1, sh.total) : sh.total;
-  const int row_lo = a.window ? max(0, pos - a.window + 1) : 0;
-  const E* qp = static_cast<const E*>(a.q) + (sq.start + qi) * a.q_t + qh * a.q_h;
+  const Sight see = sight_of(a, sq, sh.total, row);
   f16x8 qf[NT][DC];
-  float cq;
-  {
-    float v[DC][8];
-    uint32_t top = 0;
-#pragma unroll
-    for (int c = 0; c < DC; ++c) {
-      const int d = c < 2 * NC ? 64 * (c / 2) + 16 * lg + 8 * (c & 1) : 64 * NC + 8 * lg;
-      load8<T>(qp + d, v[c]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = max(top, abs_bits(v[c][i]));
-    }
-    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
-    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
-    // The row times a power of two that brings its largest value to [2^14, 2^15).
-    const uint32_t e = max(top >> 23, 15u);
-    const float up = __uint_as_float((268u - e) << 23), down = __uint_as_float((e - 14u) << 23);
-    cq = a.scale * down;
-#pragma unroll
-    for (int c = 0; c < DC; ++c)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float f = v[c][i] * up;
-        const _Float16 hi = static_cast<_Float16>(f);
-        qf[0][c][i] = hi;
-        if constexpr (TWO) qf[1][c][i] = static_cast<_Float16>(f - static_cast<float>(hi));
-      }
-  }
+  const float cq = load_query<T, DC, NT>(
+      static_cast<const E*>(a.q) + (sq.start + row / a.group) * a.q_t + (head * a.group + row % a.group) * a.q_h, a.scale,
+      qf, [&](int c) { return c < 2 * NC ? 64 * (c / 2) + 16 * lg + 8 * (c & 1) : 64 * NC + 8 * lg; });
 
   f32x4 acc[D / 16];
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, l = 0.f, vref = 0.f;
+  RowState rs;
 
-  const int nblk = sh.hi > sh.lo ? (sh.hi - sh.kb0 + kBlockKeys - 1) / kBlockKeys : 0;
-  const int per = (nblk + parts - 1) / parts;
-  const int blk_end = min(nblk, (part + 1) * per);
   const int P = 1 << a.c.page_log;
   const int32_t* table = a.c.table + b * a.c.stride;
   // Every row of the tile sees all keys of [full_lo, full_hi).
-  const int i_lo = sh.r0 / a.group, i_hi = (sh.r0 + sh.nrows - 1) / a.group;
-  const int full_lo = a.window ? max(0, sq.past + i_hi - a.window + 1) : 0;
-  const int full_hi = a.causal ? min(sq.past + i_lo + 1, sh.total) : sh.total;
+  const int full_lo = sight_of(a, sq, sh.total, sh.r0 + sh.nrows - 1).lo;
+  const int full_hi = sight_of(a, sq, sh.total, sh.r0).hi;
 
-  for (int blk = part * per + wave; blk < blk_end; blk += 4) {
+  for (int blk = sh.blk0 + wave; blk < sh.blk1; blk += 4) {
     const int kb = sh.kb0 + blk * kBlockKeys;
     // Pages of the 16-key groups lr / 4 (keys) and lg (values, scales).
     const int gk = kb + 16 * (lr >> 2), gv = kb + 16 * lg;
@@ -179,50 +262,8 @@ __global__ __launch_bounds__(256) void attend_kernel(const AttendArgs a, int til
         for (int n = 0; n < NT; ++n) st[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[n][2 * NC], st[t], 0, 0, 0);
       }
     }
-
-    const float sc = ks * cq;
-    float s[16], top = -INFINITY;
-    uint32_t seen = 0xffffu;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) s[j] = st[j >> 2][j & 3] * sc;
-    if (!(kb >= full_lo && kb + kBlockKeys <= full_hi && __all(ok_v))) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int key = gv + j;
-        const bool in = ok_v && key >= row_lo && key < row_hi;
-        if (!in) seen &= ~(1u << j);
-        s[j] = in ? s[j] : -INFINITY;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) top = fmaxf(top, s[j]);
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const float m_new = fmaxf(m, top), m_use = m_new == -INFINITY ? 0.f : m_new;
-    float vtop = fmaxf(vs, __shfl_xor(vs, 16));
-    vtop = fmaxf(vtop, __shfl_xor(vtop, 32));
-    const float vref_new = fmaxf(vref, vtop);
-    const float vinv = vref_new > 0.f ? kLift / vref_new : 0.f;
-    const float alpha = __builtin_amdgcn_exp2f(m - m_use);
-    const float beta = vref_new > 0.f ? alpha * (vref / vref_new) : alpha;
-    const float vf = vs * vinv;
-    l *= alpha;
     f16x8 pf[NT][2];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float p = __builtin_amdgcn_exp2f(s[j] - m_use);
-      l += p;
-      const float w = (seen >> j) & 1u ? p * vf : 0.f;
-      const _Float16 hi = static_cast<_Float16>(w);
-      pf[0][j >> 3][j & 7] = hi;
-      if constexpr (TWO) pf[1][j >> 3][j & 7] = static_cast<_Float16>(w - static_cast<float>(hi));
-    }
-    m = m_new;
-    vref = vref_new;
-    if (!__all(beta == 1.f)) {
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) acc[i] *= beta;
-    }
+    probabilities<NT>(st, ks, vs, cq, kb >= full_lo && kb + kBlockKeys <= full_hi && __all(ok_v), ok_v, gv, see, rs, acc, pf);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       const uint4 u = *reinterpret_cast<const uint4*>(vp + static_cast<int64_t>(16 * i) * P);
@@ -237,16 +278,17 @@ __global__ __launch_bounds__(256) void attend_kernel(const AttendArgs a, int til
 
   // Join the four waves.  (m is -inf where a wave saw no key; a NaN sum stays
   // NaN whatever its factor.)
+  float l = rs.l;
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
   if (lg == 0) {
-    s_m[wave][lr] = m;
+    s_m[wave][lr] = rs.m;
     s_l[wave][lr] = l;
   }
   __syncthreads();
   const float mj = fmaxf(fmaxf(s_m[0][lr], s_m[1][lr]), fmaxf(s_m[2][lr], s_m[3][lr]));
   const float m_use = mj == -INFINITY ? 0.f : mj;
-  const float f = __builtin_amdgcn_exp2f(m - m_use) * (vref / kLift);
+  const float f = __builtin_amdgcn_exp2f(rs.m - m_use) * (rs.vref > 0.f ? rs.vref / kLift : 1.f);
   for (int w = 0; w < 4; ++w) {
     if (w == wave && lr < sh.nrows) {
 #pragma unroll
@@ -260,7 +302,7 @@ __global__ __launch_bounds__(256) void attend_kernel(const AttendArgs a, int til
   }
   for (int k = tid; k < sh.nrows * D; k += 256) {
     const int r = k / D, d = k - r * D;
-    float mm = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
+    const float mm = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
     const float mu = mm == -INFINITY ? 0.f : mm;
     float lt = 0.f;
 #pragma unroll
@@ -271,76 +313,303 @@ __global__ __launch_bounds__(256) void attend_kernel(const AttendArgs a, int til
       E* o = static_cast<E*>(a.o) + (sq.start + rr / a.group) * a.o_t + (head * a.group + rr % a.group) * a.o_h;
       o[d] = static_cast<E>(lt == 0.f ? 0.f : v / lt);
     } else {
-      float* ws = static_cast<float*>(a.ws) + static_cast<int64_t>(blockIdx.x) * kTileRows * (D + 2);
+      float* ws = static_cast<float*>(a.ws) + static_cast<int64_t>(blockIdx.x) * kFewRows * (D + 2);
       ws[r * D + d] = v;
       if (d == 0) {
-        ws[kTileRows * D + r] = mm;
-        ws[kTileRows * D + kTileRows + r] = lt;
+        ws[kFewRows * D + r] = mm;
+        ws[kFewRows * D + kFewRows + r] = lt;
       }
     }
   }
 }
 
-// Joins the parts of each tile of 16 rows, in order.
+// Many query rows.  Workgroup: 4 waves of RT tiles of 16 rows.  Blocks of 64 keys
+// and values are brought to LDS as fp16 once for all four waves, two buffers
+// in turn: while one is worked on, the next block's codes are on their way
+// into registers and are converted at the end of the step.  The page numbers
+// run two blocks ahead, the scales one (threads 0 .. 3, one to a group of 16
+// keys), so that no step waits for a chain of loads.
+// LDS rows have an odd number of 16-byte units, so that 16 neighbouring rows
+// fall on different banks; key 16 g + 4 t + i is row 16 t + 4 g + i, which
+// puts the rows of one fragment side by side.
+// RT is 2 while a wave's registers hold it (fp32 queries above 128 d: 1);
+// up to 128 d of 16-bit queries two workgroups share a CU, so that one's
+// products run under the other's exponentials.
+constexpr int many_rt(int t, int dc) { return t == EL_F32 && dc > 4 ? 1 : 2; }
+constexpr int many_waves(int t, int dc) { return t == EL_F32 ? (dc <= 2 ? 2 : 1) : dc <= 4 ? 2 : 1; }
+
+template <int T, int DC>
+__global__ __launch_bounds__(256, many_waves(T, DC)) void attend_many_kernel(const AttendArgs a, int tiles, int parts) {
+  typedef typename Elem<T>::type E;
+  constexpr int D = DC * 32;
+  constexpr int NT = T == EL_F32 ? 2 : 1;
+  constexpr int RT = many_rt(T, DC), ROWS = 64 * RT;
+  constexpr int KPITCH = 2 * D + 16, VPITCH = 2 * kBlockKeys + 16;
+  constexpr int KBYTES = kBlockKeys * KPITCH, BUF = KBYTES + D * VPITCH;
+  constexpr int KU = kBlockKeys * D / 16, CU = (KU + 255) / 256;  // 16-code units of a block (keys; values have as many)
+  __shared__ __attribute__((aligned(16))) unsigned char s_kv[2 * BUF];
+  __shared__ int64_t s_slot[4][4];
+  __shared__ float s_ks[4][4], s_vs[4][4];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, lg = lane >> 4;
+  // An XCD takes a contiguous range: whole (sequence, head) pairs share their
+  // keys and values in its L2.  The longest causal rows come first.
+  int id = xcd_remap(blockIdx.x, gridDim.x);
+  const int part = id % parts;
+  id /= parts;
+  const int tile = tiles - 1 - id % tiles;
+  const int head = id / tiles % a.c.heads, b = id / tiles / a.c.heads;
+  const Seq sq = load_seq(a.c, b);
+  const Share sh = share_of(a, sq, tile, ROWS, part, parts);
+  if (sh.nrows <= 0) return;
+
+  f16x8 qf[RT][NT][DC];
+  float cq[RT];
+  Sight see[RT];
+  RowState rs[RT];
+  f32x4 acc[RT][D / 16];
+  const int w0 = wave * 16 * RT;                                 // the wave's first row
+  const bool work = w0 < sh.nrows;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int row = sh.r0 + min(w0 + 16 * r + lr, sh.nrows - 1);
+    see[r] = sight_of(a, sq, sh.total, row);
+    cq[r] = load_query<T, DC, NT>(
+        static_cast<const E*>(a.q) + (sq.start + row / a.group) * a.q_t + (head * a.group + row % a.group) * a.q_h,
+        a.scale, qf[r], [&](int c) { return 32 * c + 8 * lg; });
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) acc[r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  // What the wave's rows see together, and what each of them sees.
+  const int wl = sh.r0 + min(w0, sh.nrows - 1), wh = sh.r0 + min(w0 + 16 * RT - 1, sh.nrows - 1);
+  const Sight first = sight_of(a, sq, sh.total, wl), last = sight_of(a, sq, sh.total, wh);
+
+  const int P = 1 << a.c.page_log;
+  const int32_t* table = a.c.table + b * a.c.stride;
+  const int nblk = sh.blk1 - sh.blk0;
+  const int kb0 = sh.kb0 + sh.blk0 * kBlockKeys;
+
+  // Threads 0 .. 3: page number, then slot and scales, of group tid of block n.
+  auto page_of = [&](int n) {
+    const int key = kb0 + n * kBlockKeys + 16 * tid;
+    return n < nblk && key < sh.hi ? table[key >> a.c.page_log] : -1;
+  };
+  auto slot_of = [&](int page) {
+    return page >= 0 && page < a.c.n_pages ? static_cast<int64_t>(page) * a.c.heads + head : int64_t(-1);
+  };
+  uint4 ck[CU], cv[CU];
+  auto fetch = [&](int n) {
+    const int kb = kb0 + n * kBlockKeys;
+#pragma unroll
+    for (int u = 0; u < CU; ++u) {
+      const int i = tid + u * 256;
+      if (KU % 256 && i >= KU) continue;
+      const int key = i / (D / 16), d = i % (D / 16) * 16;
+      const int64_t sk = max(s_slot[n & 3][key >> 4], int64_t(0));
+      ck[u] = *reinterpret_cast<const uint4*>(a.c.k + (sk * P + ((kb + key) & (P - 1))) * D + d);
+      const int64_t sv = max(s_slot[n & 3][i & 3], int64_t(0));
+      cv[u] = *reinterpret_cast<const uint4*>(a.c.v + (sv * D + (i >> 2)) * P + ((kb + 16 * (i & 3)) & (P - 1)));
+    }
+  };
+  auto convert = [&](int n) {
+    unsigned char* buf = s_kv + (n & 1) * BUF;
+#pragma unroll
+    for (int u = 0; u < CU; ++u) {
+      const int i = tid + u * 256;
+      if (KU % 256 && i >= KU) continue;
+      const int key = i / (D / 16), d = i % (D / 16) * 16;
+      const int krow = ((key >> 2) & 3) * 16 + (key >> 4) * 4 + (key & 3);
+      f16x8* pk = reinterpret_cast<f16x8*>(buf + krow * KPITCH + 2 * d);
+      pk[0] = codes_to_f16(ck[u].x, ck[u].y);
+      pk[1] = codes_to_f16(ck[u].z, ck[u].w);
+      f16x8* pv = reinterpret_cast<f16x8*>(buf + KBYTES + (i >> 2) * VPITCH + 32 * (i & 3));
+      pv[0] = codes_to_f16(cv[u].x, cv[u].y);
+      pv[1] = codes_to_f16(cv[u].z, cv[u].w);
+    }
+  };
+
+  int page2 = -1;                    // page number of block n + 2
+  float ks1 = 0.f, vs1 = 0.f;        // scales of block n + 1
+  if (tid < 4) {
+    const int64_t s0 = slot_of(page_of(0)), s1 = slot_of(page_of(1));
+    page2 = page_of(2);
+    s_slot[0][tid] = s0;
+    s_slot[1][tid] = s1;
+    s_ks[0][tid] = s0 >= 0 ? a.c.ks[s0] : 0.f;
+    s_vs[0][tid] = s0 >= 0 ? a.c.vs[s0] : 0.f;
+    ks1 = s1 >= 0 ? a.c.ks[s1] : 0.f;
+    vs1 = s1 >= 0 ? a.c.vs[s1] : 0.f;
+  }
+  __syncthreads();
+  if (nblk > 0) {
+    fetch(0);
+    convert(0);
+  }
+  __syncthreads();
+
+  for (int n = 0; n < nblk; ++n) {
+    if (n + 1 < nblk) fetch(n + 1);
+    if (tid < 4) {
+      s_ks[(n + 1) & 3][tid] = ks1;
+      s_vs[(n + 1) & 3][tid] = vs1;
+      const int64_t s2 = slot_of(page2);
+      s_slot[(n + 2) & 3][tid] = s2;
+      ks1 = s2 >= 0 ? a.c.ks[s2] : 0.f;
+      vs1 = s2 >= 0 ? a.c.vs[s2] : 0.f;
+      page2 = page_of(n + 3);
+    }
+    const int kb = kb0 + n * kBlockKeys;
+    // Blocks that none of the wave's rows sees are left out.
+    if (work && kb < last.hi && kb + kBlockKeys > first.lo) {
+      const unsigned char* kt = s_kv + (n & 1) * BUF + lr * KPITCH + 16 * lg;
+      f32x4 st[RT][4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) st[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < DC; ++c) {
+          const f16x8 k = *reinterpret_cast<const f16x8*>(kt + 16 * t * KPITCH + 64 * c);
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int x = 0; x < NT; ++x) st[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qf[r][x][c], st[r][t], 0, 0, 0);
+        }
+      }
+      const bool in = s_slot[n & 3][lg] >= 0;
+      const float ks = s_ks[n & 3][lg], vs = s_vs[n & 3][lg];
+      const bool all = kb >= last.lo && kb + kBlockKeys <= first.hi && __all(in);
+      f16x8 pf[RT][NT][2];
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        probabilities<NT>(st[r], ks, vs, cq[r], all, in, kb + 16 * lg, see[r], rs[r], acc[r], pf[r]);
+      const unsigned char* vt = s_kv + (n & 1) * BUF + KBYTES + lr * VPITCH + 32 * lg;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const f16x8 v = *reinterpret_cast<const f16x8*>(vt + 16 * i * VPITCH + 16 * h);
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int x = 0; x < NT; ++x) acc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pf[r][x][h], acc[r][i], 0, 0, 0);
+        }
+    }
+    if (n + 1 < nblk) convert(n + 1);
+    __syncthreads();
+  }
+
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    float l = rs[r].l;
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    const int k = w0 + 16 * r + lr;
+    if (k >= sh.nrows) continue;
+    const float lift = rs[r].vref > 0.f ? rs[r].vref / kLift : 1.f;
+    if (parts == 1) {
+      const int rr = sh.r0 + k;
+      E* o = static_cast<E*>(a.o) + (sq.start + rr / a.group) * a.o_t + (head * a.group + rr % a.group) * a.o_h;
+      const float f = l == 0.f ? 0.f : lift / l;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        E e[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) e[q] = static_cast<E>(l == 0.f ? 0.f : acc[r][i][q] * f);
+        __builtin_memcpy(__builtin_assume_aligned(o + 16 * i + 4 * lg, 4 * sizeof(E)), e, 4 * sizeof(E));
+      }
+    } else {
+      // The workgroup's place in the workspace goes by its share, not its number.
+      const int64_t at = ((static_cast<int64_t>(b) * a.c.heads + head) * tiles + tile) * parts + part;
+      float* ws = static_cast<float*>(a.ws) + at * ROWS * (D + 2);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) *reinterpret_cast<f32x4*>(ws + k * D + 16 * i + 4 * lg) = acc[r][i] * lift;
+      if (lg == 0) {
+        ws[ROWS * D + k] = rs[r].m;
+        ws[ROWS * D + ROWS + k] = l;
+      }
+    }
+  }
+}
+
+// Joins the parts of each tile of tile_rows rows, in order.  Workgroup: 16
+// rows of a tile.
 template <int T>
-__global__ __launch_bounds__(256) void join_kernel(const AttendArgs a, int tiles, int parts) {
+__global__ __launch_bounds__(256) void join_kernel(const AttendArgs a, int tiles, int tile_rows, int parts) {
   typedef typename Elem<T>::type E;
   const int D = a.D;
-  const int id = blockIdx.x;
+  const int slices = tile_rows / 16;
+  const int k0 = static_cast<int>(blockIdx.x) % slices * 16, id = static_cast<int>(blockIdx.x) / slices;
   const int tile = id % tiles, head = id / tiles % a.c.heads, b = id / tiles / a.c.heads;
   const Seq sq = load_seq(a.c, b);
-  const int r0 = tile * kTileRows, nrows = min(kTileRows, sq.count * a.group - r0);
-  const int64_t size = kTileRows * (D + 2);
+  const int r0 = tile * tile_rows + k0, nrows = min(16, sq.count * a.group - r0);
+  const int64_t size = static_cast<int64_t>(tile_rows) * (D + 2);
   const float* ws = static_cast<const float*>(a.ws) + static_cast<int64_t>(id) * parts * size;
   for (int k = threadIdx.x; k < nrows * D; k += 256) {
-    const int r = k / D, d = k - r * D;
+    const int r = k0 + k / D, d = k % D;
     float m = -INFINITY;
-    for (int p = 0; p < parts; ++p) m = fmaxf(m, ws[p * size + kTileRows * D + r]);
+    for (int p = 0; p < parts; ++p) m = fmaxf(m, ws[p * size + tile_rows * D + r]);
     m = m == -INFINITY ? 0.f : m;
     float l = 0.f, v = 0.f;
     for (int p = 0; p < parts; ++p) {
-      const float f = __builtin_amdgcn_exp2f(ws[p * size + kTileRows * D + r] - m);
-      l += f * ws[p * size + kTileRows * D + kTileRows + r];
+      const float f = __builtin_amdgcn_exp2f(ws[p * size + tile_rows * D + r] - m);
+      l += f * ws[p * size + tile_rows * D + tile_rows + r];
       v += f * ws[p * size + r * D + d];
     }
-    const int rr = r0 + r;
+    const int rr = r0 + k / D;
     E* o = static_cast<E*>(a.o) + (sq.start + rr / a.group) * a.o_t + (head * a.group + rr % a.group) * a.o_h;
     o[d] = static_cast<E>(l == 0.f ? 0.f : v / l);
   }
 }
 
-template <int T>
+template <int T, int DC>
 static void go_attend(const AttendArgs& a, hipStream_t s) {
-  const int tiles = static_cast<int>((static_cast<int64_t>(a.c.max_new) * a.group + kTileRows - 1) / kTileRows);
-  const int64_t wgs = static_cast<int64_t>(a.batch) * a.c.heads * tiles;
-  const int64_t part_bytes = static_cast<int64_t>(kTileRows) * (a.D + 2) * 4;
-  int64_t parts = 1024 / wgs;
-  parts = parts < (a.max_total + 255) / 256 ? parts : (a.max_total + 255) / 256;
-  const int64_t room = static_cast<int64_t>(a.ws_bytes) / (part_bytes * wgs);
+  const int64_t rows = static_cast<int64_t>(a.c.max_new) * a.group, pairs = static_cast<int64_t>(a.batch) * a.c.heads;
+  const bool many = rows > 32;
+  const int tile_rows = many ? 64 * many_rt(T, DC) : kFewRows;
+  const int64_t tiles = (rows + tile_rows - 1) / tile_rows, wgs = pairs * tiles;
+  // Parts of the keys where the rows alone do not fill the chip, each at
+  // least one round of the workgroup's waves long, as the workspace allows.
+  int64_t keys = a.max_total;
+  if (a.window && keys > static_cast<int64_t>(a.window) + a.c.max_new) keys = static_cast<int64_t>(a.window) + a.c.max_new;
+  const int64_t most = (keys + 255) / 256, room = static_cast<int64_t>(a.ws_bytes) / (tile_rows * (a.D + 2) * 4 * wgs);
+  int64_t parts = (many ? 512 : 1024) / wgs;
+  parts = parts < most ? parts : most;
   parts = parts < room ? parts : room;
   if (parts < 1) parts = 1;
+  const int nt = static_cast<int>(tiles), np = static_cast<int>(parts);
   const dim3 grid(static_cast<unsigned>(wgs * parts));
-  const int np = static_cast<int>(parts);
+  if (many)
+    attend_many_kernel<T, DC><<<grid, 256, 0, s>>>(a, nt, np);
+  else
+    attend_few_kernel<T, DC><<<grid, 256, 0, s>>>(a, nt, np);
+  if (np > 1)
+    join_kernel<T><<<dim3(static_cast<unsigned>(wgs * (tile_rows / 16))), 256, 0, s>>>(a, nt, tile_rows, np);
+}
+
+template <int T>
+static void go_dim(const AttendArgs& a, hipStream_t s) {
   switch (a.D / 32) {
-    case 1: attend_kernel<T, 1><<<grid, 256, 0, s>>>(a, tiles, np); break;
-    case 2: attend_kernel<T, 2><<<grid, 256, 0, s>>>(a, tiles, np); break;
-    case 3: attend_kernel<T, 3><<<grid, 256, 0, s>>>(a, tiles, np); break;
-    case 4: attend_kernel<T, 4><<<grid, 256, 0, s>>>(a, tiles, np); break;
-    case 5: attend_kernel<T, 5><<<grid, 256, 0, s>>>(a, tiles, np); break;
-    case 6: attend_kernel<T, 6><<<grid, 256, 0, s>>>(a, tiles, np); break;
-    case 7: attend_kernel<T, 7><<<grid, 256, 0, s>>>(a, tiles, np); break;
-    default: attend_kernel<T, 8><<<grid, 256, 0, s>>>(a, tiles, np); break;
+    case 1: go_attend<T, 1>(a, s); break;
+    case 2: go_attend<T, 2>(a, s); break;
+    case 3: go_attend<T, 3>(a, s); break;
+    case 4: go_attend<T, 4>(a, s); break;
+    case 5: go_attend<T, 5>(a, s); break;
+    case 6: go_attend<T, 6>(a, s); break;
+    case 7: go_attend<T, 7>(a, s); break;
+    default: go_attend<T, 8>(a, s); break;
   }
-  if (np > 1) join_kernel<T><<<dim3(static_cast<unsigned>(wgs)), 256, 0, s>>>(a, tiles, np);
 }
 
 hipError_t launch_attend(int dtype, const AttendArgs& a, hipStream_t s) {
   if (dtype == EL_F32)
-    go_attend<EL_F32>(a, s);
+    go_dim<EL_F32>(a, s);
   else if (dtype == EL_BF16)
-    go_attend<EL_BF16>(a, s);
+    go_dim<EL_BF16>(a, s);
   else
-    go_attend<EL_F16>(a, s);
+    go_dim<EL_F16>(a, s);
   return hipGetLastError();
 }
 
