@@ -66,7 +66,7 @@ __device__ __forceinline__ Share share_of(const AttendArgs& a, const Seq& s, int
     if (a.window) h.lo = max(0, s.past + i_lo - a.window + 1);
     if (a.causal) h.hi = min(h.total, s.past + i_hi + 1);
   }
-  h.kb0 = h.lo & ~(kBlockKeys - 1);
+  h.kb0 = h.lo & ~15;
   const int nblk = h.hi > h.lo ? (h.hi - h.kb0 + kBlockKeys - 1) / kBlockKeys : 0;
   const int per = (nblk + parts - 1) / parts;
   h.blk0 = min(nblk, part * per);
@@ -116,32 +116,35 @@ __device__ __forceinline__ float load_query(const typename Elem<T>::type* qp, fl
 // What a wave carries along for 16 query rows (a lane: row lr, the sum over
 // its own keys only).  vref is the largest page scale so far.
 struct RowState {
-  float m = -INFINITY, l = 0.f, vref = 0.f;
+  float m = -INFINITY, l = 0.f, vref = 0.f, lift = 1.f;  // lift: kLift / vref
 };
 
-// The probabilities of 16 keys (this lane's, of one page group with scales
-// ks, vs) as operands of the second product; rescales what was summed when m
-// or vref has to move.  all: every key is visible; else keys key0 .. key0+15
-// count where `in` and inside the row's sight.
-template <int NT, int NA>
-__device__ __forceinline__ void probabilities(const f32x4 (&st)[4], float ks, float vs, float cq, bool all, bool in,
-                                              int key0, const Sight& see, RowState& r, f32x4 (&acc)[NA],
-                                              f16x8 (&pf)[NT][2]) {
-  const float sc = ks * cq;
-  uint32_t seen = 0xffffu;
-  float top = -INFINITY;
-  if (all) {
+// Hides what a row does not see: this lane's keys key0 .. key0 + 15 count
+// where `in` and inside the row's sight.  Scores become final (their factor
+// sc 1) with -inf in hidden places, and the scale of values of which the row
+// sees none becomes 0, so that a hidden page's NaN scale stays out.
+__device__ __forceinline__ void hide(f32x4 (&st)[4], float& sc, float& vs, bool in, int key0, const Sight& see) {
+  bool any = false;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) top = fmaxf(top, st[j >> 2][j & 3]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const bool s = in && key0 + j >= see.lo && key0 + j < see.hi;
-      if (!s) seen &= ~(1u << j);
-      top = s ? fmaxf(top, st[j >> 2][j & 3]) : top;
-    }
+  for (int j = 0; j < 16; ++j) {
+    const bool s = in && key0 + j >= see.lo && key0 + j < see.hi;
+    any |= s;
+    st[j >> 2][j & 3] = s ? st[j >> 2][j & 3] * sc : -INFINITY;
   }
-  top *= sc;  // NaN where nothing is seen and sc is 0: no comparison holds
+  sc = 1.f;
+  vs = any ? vs : 0.f;
+}
+
+// The probabilities of 16 keys (this lane's, of one page group: scores st
+// times sc, value scale vs) as operands of the second product; rescales what
+// was summed when m or vref has to move.
+template <int NT, int NA>
+__device__ __forceinline__ void probabilities(const f32x4 (&st)[4], float sc, float vs, RowState& r, f32x4 (&acc)[NA],
+                                              f16x8 (&pf)[NT][2]) {
+  float top = st[0][0];
+#pragma unroll
+  for (int j = 1; j < 16; ++j) top = fmaxf(top, st[j >> 2][j & 3]);
+  top *= sc;
   if (__any(top > r.m + kSlack || vs > r.vref)) {
     float t = fmaxf(top, __shfl_xor(top, 16));
     t = fmaxf(t, __shfl_xor(t, 32));
@@ -153,30 +156,25 @@ __device__ __forceinline__ void probabilities(const f32x4 (&st)[4], float ks, fl
     const float beta = vref > 0.f ? alpha * (r.vref / vref) : alpha;
     r.m = m;
     r.vref = vref;
+    r.lift = vref > 0.f ? kLift / vref : 1.f;
     r.l *= alpha;
 #pragma unroll
     for (int i = 0; i < NA; ++i) acc[i] *= beta;
   }
-  const float vf = r.vref > 0.f ? vs * (kLift / r.vref) : vs;
-  float w[16], sum[4] = {0.f, 0.f, 0.f, 0.f};
+  const float vf = vs * r.lift;
+  // A row that has seen nothing yet has only -inf here: any finite m will do.
+  const float neg = r.m == -INFINITY ? 0.f : -r.m;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    float p = __builtin_amdgcn_exp2f(fmaf(st[j >> 2][j & 3], sc, -r.m));
-    w[j] = p * vf;
-    if (!all) {
-      const bool s = (seen >> j) & 1u;
-      p = s ? p : 0.f;
-      w[j] = s ? w[j] : 0.f;
-    }
+    const float p = __builtin_amdgcn_exp2f(fmaf(st[j >> 2][j & 3], sc, neg));
     sum[j & 3] += p;
+    const float w = p * vf;
+    const _Float16 hi = static_cast<_Float16>(w);
+    pf[0][j >> 3][j & 7] = hi;
+    if constexpr (NT > 1) pf[1][j >> 3][j & 7] = static_cast<_Float16>(w - static_cast<float>(hi));
   }
   r.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const _Float16 hi = static_cast<_Float16>(w[j]);
-    pf[0][j >> 3][j & 7] = hi;
-    if constexpr (NT > 1) pf[1][j >> 3][j & 7] = static_cast<_Float16>(w[j] - static_cast<float>(hi));
-  }
 }
 
 // Few query rows.  Workgroup: 16 rows, one part of the keys; its four waves
@@ -184,9 +182,10 @@ __device__ __forceinline__ void probabilities(const f32x4 (&st)[4], float ks, fl
 // joined in order at the end.  parts > 1: the results go to the workspace
 // (unnormalised, with their maxima and sums) for join_kernel.
 constexpr int kFewRows = 16;
+constexpr int few_waves(int t, int dc) { return t == EL_F32 ? (dc <= 2 ? 3 : dc <= 4 ? 2 : 1) : dc <= 2 ? 4 : dc <= 4 ? 3 : dc <= 6 ? 2 : 1; }
 
 template <int T, int DC>
-__global__ __launch_bounds__(256) void attend_few_kernel(const AttendArgs a, int tiles, int parts) {
+__global__ __launch_bounds__(256, few_waves(T, DC)) void attend_few_kernel(const AttendArgs a, int tiles, int parts) {
   typedef typename Elem<T>::type E;
   constexpr int D = DC * 32, NC = DC / 2, REM = DC & 1;
   constexpr int NT = T == EL_F32 ? 2 : 1;
@@ -238,8 +237,21 @@ __global__ __launch_bounds__(256) void attend_few_kernel(const AttendArgs a, int
     const int64_t slot_v = (ok_v ? static_cast<int64_t>(pv) : 0) * a.c.heads + head;
     const int8_t* kp = a.c.k + (slot_k * P + (gk & (P - 1)) + (lr & 3)) * D;
     const int8_t* vp = a.c.v + (slot_v * D + lr) * P + (gv & (P - 1));
+    // The whole block's loads first: keys, scales, then the values that are
+    // needed last.
+    uint4 kc[4][NC ? NC : 1];
+    uint2 kr[4];
+    uint4 vc[D / 16];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) kc[t][c] = *reinterpret_cast<const uint4*>(kp + 4 * t * D + 64 * c + 16 * lg);
+      if constexpr (REM) kr[t] = *reinterpret_cast<const uint2*>(kp + 4 * t * D + 64 * NC + 8 * lg);
+    }
     const float ks = ok_v ? a.c.ks[slot_v] : 0.f;
     const float vs = ok_v ? a.c.vs[slot_v] : 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) vc[i] = *reinterpret_cast<const uint4*>(vp + static_cast<int64_t>(16 * i) * P);
 
     f32x4 st[4];
 #pragma unroll
@@ -247,8 +259,7 @@ __global__ __launch_bounds__(256) void attend_few_kernel(const AttendArgs a, int
       st[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const uint4 u = *reinterpret_cast<const uint4*>(kp + 4 * t * D + 64 * c + 16 * lg);
-        const f16x8 k0 = codes_to_f16(u.x, u.y), k1 = codes_to_f16(u.z, u.w);
+        const f16x8 k0 = codes_to_f16(kc[t][c].x, kc[t][c].y), k1 = codes_to_f16(kc[t][c].z, kc[t][c].w);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           st[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[n][2 * c], st[t], 0, 0, 0);
@@ -256,18 +267,18 @@ __global__ __launch_bounds__(256) void attend_few_kernel(const AttendArgs a, int
         }
       }
       if constexpr (REM) {
-        const uint2 u = *reinterpret_cast<const uint2*>(kp + 4 * t * D + 64 * NC + 8 * lg);
-        const f16x8 k0 = codes_to_f16(u.x, u.y);
+        const f16x8 k0 = codes_to_f16(kr[t].x, kr[t].y);
 #pragma unroll
         for (int n = 0; n < NT; ++n) st[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[n][2 * NC], st[t], 0, 0, 0);
       }
     }
     f16x8 pf[NT][2];
-    probabilities<NT>(st, ks, vs, cq, kb >= full_lo && kb + kBlockKeys <= full_hi && __all(ok_v), ok_v, gv, see, rs, acc, pf);
+    float sc = ks * cq, vsc = vs;
+    if (!(kb >= full_lo && kb + kBlockKeys <= full_hi && __all(ok_v))) hide(st, sc, vsc, ok_v, gv, see);
+    probabilities<NT>(st, sc, vsc, rs, acc, pf);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
-      const uint4 u = *reinterpret_cast<const uint4*>(vp + static_cast<int64_t>(16 * i) * P);
-      const f16x8 v0 = codes_to_f16(u.x, u.y), v1 = codes_to_f16(u.z, u.w);
+      const f16x8 v0 = codes_to_f16(vc[i].x, vc[i].y), v1 = codes_to_f16(vc[i].z, vc[i].w);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[n][0], acc[i], 0, 0, 0);
@@ -288,7 +299,7 @@ __global__ __launch_bounds__(256) void attend_few_kernel(const AttendArgs a, int
   __syncthreads();
   const float mj = fmaxf(fmaxf(s_m[0][lr], s_m[1][lr]), fmaxf(s_m[2][lr], s_m[3][lr]));
   const float m_use = mj == -INFINITY ? 0.f : mj;
-  const float f = __builtin_amdgcn_exp2f(rs.m - m_use) * (rs.vref > 0.f ? rs.vref / kLift : 1.f);
+  const float f = __builtin_amdgcn_exp2f(rs.m - m_use) * (1.f / rs.lift);
   for (int w = 0; w < 4; ++w) {
     if (w == wave && lr < sh.nrows) {
 #pragma unroll
@@ -482,9 +493,18 @@ __global__ __launch_bounds__(256, many_waves(T, DC)) void attend_many_kernel(con
       const float ks = s_ks[n & 3][lg], vs = s_vs[n & 3][lg];
       const bool all = kb >= last.lo && kb + kBlockKeys <= first.hi && __all(in);
       f16x8 pf[RT][NT][2];
+      float sc[RT], vsc[RT];
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-        probabilities<NT>(st[r], ks, vs, cq[r], all, in, kb + 16 * lg, see[r], rs[r], acc[r], pf[r]);
+      for (int r = 0; r < RT; ++r) {
+        sc[r] = ks * cq[r];
+        vsc[r] = vs;
+      }
+      if (!all) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) hide(st[r], sc[r], vsc[r], in, kb + 16 * lg, see[r]);
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) probabilities<NT>(st[r], sc[r], vsc[r], rs[r], acc[r], pf[r]);
       const unsigned char* vt = s_kv + (n & 1) * BUF + KBYTES + lr * VPITCH + 32 * lg;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
@@ -508,7 +528,7 @@ __global__ __launch_bounds__(256, many_waves(T, DC)) void attend_many_kernel(con
     l += __shfl_xor(l, 32);
     const int k = w0 + 16 * r + lr;
     if (k >= sh.nrows) continue;
-    const float lift = rs[r].vref > 0.f ? rs[r].vref / kLift : 1.f;
+    const float lift = 1.f / rs[r].lift;
     if (parts == 1) {
       const int rr = sh.r0 + k;
       E* o = static_cast<E*>(a.o) + (sq.start + rr / a.group) * a.o_t + (head * a.group + rr % a.group) * a.o_h;
@@ -534,32 +554,42 @@ __global__ __launch_bounds__(256, many_waves(T, DC)) void attend_many_kernel(con
   }
 }
 
-// Joins the parts of each tile of tile_rows rows, in order.  Workgroup: 16
-// rows of a tile.
+// Joins the parts of the tiles, in order.  Workgroup: one row.
+constexpr int kMaxParts = 256;
+
 template <int T>
-__global__ __launch_bounds__(256) void join_kernel(const AttendArgs a, int tiles, int tile_rows, int parts) {
+__global__ __launch_bounds__(128) void join_kernel(const AttendArgs a, int tiles, int tile_rows, int parts) {
   typedef typename Elem<T>::type E;
-  const int D = a.D;
-  const int slices = tile_rows / 16;
-  const int k0 = static_cast<int>(blockIdx.x) % slices * 16, id = static_cast<int>(blockIdx.x) / slices;
+  __shared__ float s_f[kMaxParts], s_l[kMaxParts], s_m[2];
+  const int D = a.D, tid = threadIdx.x;
+  const int k = static_cast<int>(blockIdx.x) % tile_rows, id = static_cast<int>(blockIdx.x) / tile_rows;
   const int tile = id % tiles, head = id / tiles % a.c.heads, b = id / tiles / a.c.heads;
   const Seq sq = load_seq(a.c, b);
-  const int r0 = tile * tile_rows + k0, nrows = min(16, sq.count * a.group - r0);
+  const int row = tile * tile_rows + k;
+  if (row >= sq.count * a.group) return;
   const int64_t size = static_cast<int64_t>(tile_rows) * (D + 2);
   const float* ws = static_cast<const float*>(a.ws) + static_cast<int64_t>(id) * parts * size;
-  for (int k = threadIdx.x; k < nrows * D; k += 256) {
-    const int r = k0 + k / D, d = k % D;
-    float m = -INFINITY;
-    for (int p = 0; p < parts; ++p) m = fmaxf(m, ws[p * size + tile_rows * D + r]);
-    m = m == -INFINITY ? 0.f : m;
-    float l = 0.f, v = 0.f;
-    for (int p = 0; p < parts; ++p) {
-      const float f = __builtin_amdgcn_exp2f(ws[p * size + tile_rows * D + r] - m);
-      l += f * ws[p * size + tile_rows * D + tile_rows + r];
-      v += f * ws[p * size + r * D + d];
-    }
-    const int rr = r0 + k / D;
-    E* o = static_cast<E*>(a.o) + (sq.start + rr / a.group) * a.o_t + (head * a.group + rr % a.group) * a.o_h;
+  float m = -INFINITY;
+  for (int p = tid; p < parts; p += 128) {
+    s_f[p] = ws[p * size + tile_rows * D + k];
+    s_l[p] = ws[p * size + tile_rows * D + tile_rows + k];
+    m = fmaxf(m, s_f[p]);
+  }
+#pragma unroll
+  for (int x = 32; x; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
+  if ((tid & 63) == 0) s_m[tid >> 6] = m;
+  __syncthreads();
+  m = fmaxf(s_m[0], s_m[1]);
+  m = m == -INFINITY ? 0.f : m;
+  for (int p = tid; p < parts; p += 128) s_f[p] = __builtin_amdgcn_exp2f(s_f[p] - m);
+  __syncthreads();
+  float l = 0.f;
+  for (int p = 0; p < parts; ++p) l += s_f[p] * s_l[p];
+  E* o = static_cast<E*>(a.o) + (sq.start + row / a.group) * a.o_t + (head * a.group + row % a.group) * a.o_h;
+  for (int d = tid; d < D; d += 128) {
+    float v = 0.f;
+#pragma unroll 8
+    for (int p = 0; p < parts; ++p) v += s_f[p] * ws[p * size + k * D + d];
     o[d] = static_cast<E>(l == 0.f ? 0.f : v / l);
   }
 }
@@ -575,7 +605,8 @@ static void go_attend(const AttendArgs& a, hipStream_t s) {
   int64_t keys = a.max_total;
   if (a.window && keys > static_cast<int64_t>(a.window) + a.c.max_new) keys = static_cast<int64_t>(a.window) + a.c.max_new;
   const int64_t most = (keys + 255) / 256, room = static_cast<int64_t>(a.ws_bytes) / (tile_rows * (a.D + 2) * 4 * wgs);
-  int64_t parts = (many ? 512 : 1024) / wgs;
+  int64_t parts = 256 * (many ? many_waves(T, DC) : few_waves(T, DC)) / wgs;
+  parts = parts < kMaxParts ? parts : kMaxParts;
   parts = parts < most ? parts : most;
   parts = parts < room ? parts : room;
   if (parts < 1) parts = 1;
@@ -586,7 +617,7 @@ static void go_attend(const AttendArgs& a, hipStream_t s) {
   else
     attend_few_kernel<T, DC><<<grid, 256, 0, s>>>(a, nt, np);
   if (np > 1)
-    join_kernel<T><<<dim3(static_cast<unsigned>(wgs * (tile_rows / 16))), 256, 0, s>>>(a, nt, tile_rows, np);
+    join_kernel<T><<<dim3(static_cast<unsigned>(wgs * tile_rows)), 128, 0, s>>>(a, nt, tile_rows, np);
 }
 
 template <int T>
