@@ -509,6 +509,8 @@ def voc_ops_create(device: int = 0):
     """Returns (status, ops)."""
     ops = ctypes.c_void_p()
     st = lib().voc_ops_create(device, ctypes.byref(ops))
+    if st == VOC_OK:
+        _use_torch()
     return st, ops
 
 
@@ -529,14 +531,33 @@ def open_ops(device: int = 0):
     return ops
 
 
+# voc_dtype of torch dtypes, and the function that reads a device's current
+# stream, filled in with the first handle (torch is imported only then).  A
+# call takes about 5 us in the library; the checks here are written to cost
+# little beside that.
 _dtypes: dict = {}
+_int8 = _float32 = _empty = _raw_stream = None
+
+
+def _use_torch() -> None:
+    global _int8, _float32, _empty, _raw_stream
+    import torch
+    _int8, _float32, _empty = torch.int8, torch.float32, torch.empty
+    # The public torch.cuda.current_stream() builds a Stream object (3 us).
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _dtypes.update({torch.float32: VOC_F32, torch.bfloat16: VOC_BF16, torch.float16: VOC_F16})
+
+
+def _stream_of(stream, t):
+    """`stream`, or the current stream of t's device."""
+    if stream is None:
+        return _raw_stream(t.get_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _dtype(t) -> int:
     """voc_dtype of a torch dtype."""
-    if not _dtypes:
-        import torch
-        _dtypes.update({torch.float32: VOC_F32, torch.bfloat16: VOC_BF16, torch.float16: VOC_F16})
     d = _dtypes.get(t)
     if d is None:
         raise ValueError(f"dtype {t}: float32, bfloat16 or float16 is needed")
@@ -548,20 +569,21 @@ def _check_ops(st: int, ops) -> None:
         raise VocError(st, voc_ops_last_error(ops))
 
 
-def _rows(what: str, t, shape=None, dtype=None):
+def _rows(what: str, t, shape, dtype) -> int:
     """Checks a CUDA matrix whose rows are contiguous; returns its row stride."""
-    if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: a CUDA matrix with contiguous rows is needed")
-    if (shape is not None and tuple(t.shape) != tuple(shape)) or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{what}: expected {tuple(shape or t.shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    if t.shape != shape or len(shape) != 2 or t.dtype is not dtype or not t.is_cuda:
+        raise ValueError(f"{what}: a CUDA matrix {tuple(shape)} {dtype} is needed, got {tuple(t.shape)} {t.dtype}")
+    step, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        raise ValueError(f"{what}: rows have to be contiguous")
+    return step if shape[0] > 1 else max(step, shape[1])
 
 
-def _vector(what: str, t, n: int):
-    import torch
-    if not t.is_cuda or t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+def _vector(what: str, t, n: int) -> int:
+    """Checks n contiguous CUDA float32 values; returns their address."""
+    if t.dtype is not _float32 or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{what}: {n} contiguous CUDA float32 values are needed")
-    return t
+    return t.data_ptr()
 
 
 def rms_norm(ops, x, weight, eps: float = 1e-6, residual=None, h=None, q=None, scale=None, stream=None):
@@ -569,37 +591,48 @@ def rms_norm(ops, x, weight, eps: float = 1e-6, residual=None, h=None, q=None, s
     (vocoder_rms_norm).  h = x + residual is stored into `h` (which may be x
     or residual itself), into a new tensor if that is None and there is a
     residual, and is x itself without one."""
-    import torch
-    ldx = _rows("x", x)
-    rows, C = x.shape
-    ldr = _rows("residual", residual, x.shape, x.dtype) if residual is not None else 0
-    if h is None and residual is not None:
-        h = torch.empty_like(x, memory_format=torch.contiguous_format)
-    ldh = _rows("h", h, x.shape, x.dtype) if h is not None else 0
+    shape, dtype, device = x.shape, x.dtype, x.device
+    ldx = _rows("x", x, shape, dtype)
+    rows, C = shape
+    r = hp = None
+    ldr = ldh = 0
+    if residual is not None:
+        ldr, r = _rows("residual", residual, shape, dtype), residual.data_ptr()
+        if h is None:
+            h, ldh = _empty(shape, dtype=dtype, device=device), C
+            hp = h.data_ptr()
+    if h is not None and hp is None:
+        ldh, hp = _rows("h", h, shape, dtype), h.data_ptr()
     if q is None:
-        q = torch.empty(rows, C, dtype=torch.int8, device=x.device)
+        q, ldq = _empty(shape, dtype=_int8, device=device), C
+    else:
+        ldq = _rows("q", q, shape, _int8)
     if scale is None:
-        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-    _check_ops(lib().vocoder_rms_norm(
-        ops, _dtype(x.dtype), rows, C, x.data_ptr(), ldx, _ptr(residual), ldr, _ptr(h), ldh,
-        _vector("weight", weight, C).data_ptr(), eps, q.data_ptr(), _rows("q", q, x.shape, torch.int8),
-        _vector("scale", scale, rows).data_ptr(), _stream(stream)), ops)
+        scale = _empty(rows, dtype=_float32, device=device)
+    st = lib().vocoder_rms_norm(ops, _dtype(dtype), rows, C, x.data_ptr(), ldx, r, ldr, hp, ldh,
+                                _vector("weight", weight, C), eps, q.data_ptr(), ldq, _vector("scale", scale, rows),
+                                _stream_of(stream, x))
+    if st:
+        _check_ops(st, ops)
     return q, scale, x if h is None else h
 
 
 def quantize_rows(ops, x, q=None, scale=None, stream=None):
     """(q int8 [rows, C], scale fp32 [rows]) of the rows x [rows, C]
     (vocoder_quantize_rows)."""
-    import torch
-    ldx = _rows("x", x)
-    rows, C = x.shape
+    shape, dtype, device = x.shape, x.dtype, x.device
+    ldx = _rows("x", x, shape, dtype)
+    rows, C = shape
     if q is None:
-        q = torch.empty(rows, C, dtype=torch.int8, device=x.device)
+        q, ldq = _empty(shape, dtype=_int8, device=device), C
+    else:
+        ldq = _rows("q", q, shape, _int8)
     if scale is None:
-        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-    _check_ops(lib().vocoder_quantize_rows(
-        ops, _dtype(x.dtype), rows, C, x.data_ptr(), ldx, q.data_ptr(), _rows("q", q, x.shape, torch.int8),
-        _vector("scale", scale, rows).data_ptr(), _stream(stream)), ops)
+        scale = _empty(rows, dtype=_float32, device=device)
+    st = lib().vocoder_quantize_rows(ops, _dtype(dtype), rows, C, x.data_ptr(), ldx, q.data_ptr(), ldq,
+                                     _vector("scale", scale, rows), _stream_of(stream, x))
+    if st:
+        _check_ops(st, ops)
     return q, scale
 
 
@@ -607,16 +640,25 @@ def matmul_int(ops, a, a_scale, b, b_scale, bias=None, gelu: bool = False, dtype
     """act((a b^T) * a_scale[:, None] * b_scale + bias) [M, N] for int8 a
     [M, K] and b [N, K] (vocoder_matmul_int), in `dtype` (default float16) or
     the dtype of `out`."""
-    import torch
-    lda, ldb = _rows("a", a, None, torch.int8), _rows("b", b, (b.shape[0], a.shape[1]), torch.int8)
-    (M, K), N = a.shape, b.shape[0]
+    lda = _rows("a", a, a.shape, _int8)
+    M, K = a.shape
+    N = b.shape[0]
+    ldb = _rows("b", b, (N, K), _int8)
     if out is None:
-        out = torch.empty(M, N, dtype=dtype or torch.float16, device=a.device)
-    ldy = _rows("out", out, (M, N), dtype)
-    _check_ops(lib().vocoder_matmul_int(
-        ops, _dtype(out.dtype), M, N, K, a.data_ptr(), lda, _vector("a_scale", a_scale, M).data_ptr(), b.data_ptr(), ldb,
-        _vector("b_scale", b_scale, N).data_ptr(), _ptr(None if bias is None else _vector("bias", bias, N)),
-        VOC_ACT_GELU if gelu else VOC_ACT_NONE, out.data_ptr(), ldy, _stream(stream)), ops)
+        if dtype is None:
+            import torch
+            dtype = torch.float16
+        out, ldy = _empty((M, N), dtype=dtype, device=a.device), N
+    else:
+        if dtype is None:
+            dtype = out.dtype
+        ldy = _rows("out", out, (M, N), dtype)
+    st = lib().vocoder_matmul_int(
+        ops, _dtype(dtype), M, N, K, a.data_ptr(), lda, _vector("a_scale", a_scale, M), b.data_ptr(), ldb,
+        _vector("b_scale", b_scale, N), None if bias is None else _vector("bias", bias, N),
+        VOC_ACT_GELU if gelu else VOC_ACT_NONE, out.data_ptr(), ldy, _stream_of(stream, a))
+    if st:
+        _check_ops(st, ops)
     return out
 
 
@@ -669,37 +711,46 @@ class KVBatch:
         self.ref = ctypes.byref(self.c)
 
 
-def _heads(what: str, t, tokens, heads, dim, dtype=None):
-    """Checks a CUDA tensor [tokens, heads, dim] with contiguous dim."""
-    if not t.is_cuda or t.dim() != 3 or t.shape[2] != dim or t.stride(2) != 1 or (tokens, heads) != tuple(t.shape[:2]):
-        raise ValueError(f"{what}: a CUDA tensor [{tokens}, {heads}, {dim}] with contiguous last dimension is needed")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
-    return t
+def _heads(what: str, t, shape, dtype):
+    """Checks a CUDA tensor [tokens, heads, dim] with contiguous dim; returns
+    its token and head strides."""
+    if t.shape != shape or len(shape) != 3 or t.dtype is not dtype or not t.is_cuda:
+        raise ValueError(f"{what}: a CUDA tensor {tuple(shape)} {dtype} is needed, got {tuple(t.shape)} {t.dtype}")
+    step, head, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{what}: the last dimension has to be contiguous")
+    return step, head
 
 
 def cache_append(ops, cache: KVCache, batch: KVBatch, k, v, stream=None) -> None:
     """Append k and v [tokens, kv_heads, head_dim] to the cache
     (vocoder_cache_append)."""
-    _heads("k", k, k.shape[0], cache.kv_heads, cache.head_dim)
-    _heads("v", v, k.shape[0], cache.kv_heads, cache.head_dim, k.dtype)
-    batch.c.tokens = k.shape[0]
-    _check_ops(lib().vocoder_cache_append(ops, cache.ref, batch.ref, _dtype(k.dtype), k.data_ptr(), k.stride(0),
-                                          k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), _stream(stream)), ops)
+    dtype, tokens = k.dtype, k.shape[0]
+    shape = (tokens, cache.kv_heads, cache.head_dim)
+    kt, kh = _heads("k", k, shape, dtype)
+    vt, vh = _heads("v", v, shape, dtype)
+    batch.c.tokens = tokens
+    st = lib().vocoder_cache_append(ops, cache.ref, batch.ref, _dtype(dtype), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+                                    _stream_of(stream, k))
+    if st:
+        _check_ops(st, ops)
 
 
 def cache_attention(ops, cache: KVCache, batch: KVBatch, q, scale: float | None = None, causal: bool = True,
                     window: int = 0, out=None, stream=None):
     """Attention of q [tokens, heads, head_dim] over the cache
     (vocoder_cache_attention); scale defaults to head_dim ** -0.5."""
-    import torch
-    _heads("q", q, q.shape[0], q.shape[1], cache.head_dim)
+    shape, dtype, dim = q.shape, q.dtype, cache.head_dim
+    qt, qh = _heads("q", q, shape, dtype)
+    if shape[2] != dim:
+        raise ValueError(f"q: head_dim {dim} is needed, got {shape[2]}")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _heads("out", out, q.shape[0], q.shape[1], cache.head_dim, q.dtype)
-    batch.c.tokens = q.shape[0]
-    _check_ops(lib().vocoder_cache_attention(
-        ops, cache.ref, batch.ref, _dtype(q.dtype), q.shape[1], q.data_ptr(), q.stride(0), q.stride(1),
-        cache.head_dim ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(), out.stride(0),
-        out.stride(1), _stream(stream)), ops)
+        out = _empty(shape, dtype=dtype, device=q.device)
+    ot, oh = _heads("out", out, shape, dtype)
+    batch.c.tokens = shape[0]
+    st = lib().vocoder_cache_attention(ops, cache.ref, batch.ref, _dtype(dtype), shape[1], q.data_ptr(), qt, qh,
+                                       dim ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(), ot, oh,
+                                       _stream_of(stream, q))
+    if st:
+        _check_ops(st, ops)
     return out
