@@ -135,12 +135,10 @@ __device__ __forceinline__ void hide(f32x4 (&st)[4], float& sc, float& vs, bool 
   vs = any ? vs : 0.f;
 }
 
-// The probabilities of 16 keys (this lane's, of one page group: scores st
-// times sc, value scale vs) as operands of the second product; rescales what
-// was summed when m or vref has to move.
-template <int NT, int NA>
-__device__ __forceinline__ void probabilities(const f32x4 (&st)[4], float sc, float vs, RowState& r, f32x4 (&acc)[NA],
-                                              f16x8 (&pf)[NT][2]) {
+// Rescales what was summed when the scores of 16 more keys (this lane's, of
+// one page group: st times sc, value scale vs) make m or vref move.
+template <int NA>
+__device__ __forceinline__ void follow_maximum(const f32x4 (&st)[4], float sc, float vs, RowState& r, f32x4 (&acc)[NA]) {
   float top = st[0][0];
 #pragma unroll
   for (int j = 1; j < 16; ++j) top = fmaxf(top, st[j >> 2][j & 3]);
@@ -161,6 +159,11 @@ __device__ __forceinline__ void probabilities(const f32x4 (&st)[4], float sc, fl
 #pragma unroll
     for (int i = 0; i < NA; ++i) acc[i] *= beta;
   }
+}
+
+// The probabilities of those keys as operands of the second product.
+template <int NT>
+__device__ __forceinline__ void probabilities(const f32x4 (&st)[4], float sc, float vs, RowState& r, f16x8 (&pf)[NT][2]) {
   const float vf = vs * r.lift;
   // A row that has seen nothing yet has only -inf here: any finite m will do.
   const float neg = r.m == -INFINITY ? 0.f : -r.m;
@@ -275,7 +278,8 @@ __global__ __launch_bounds__(256, few_waves(T, DC)) void attend_few_kernel(const
     f16x8 pf[NT][2];
     float sc = ks * cq, vsc = vs;
     if (!(kb >= full_lo && kb + kBlockKeys <= full_hi && __all(ok_v))) hide(st, sc, vsc, ok_v, gv, see);
-    probabilities<NT>(st, sc, vsc, rs, acc, pf);
+    follow_maximum(st, sc, vsc, rs, acc);
+    probabilities<NT>(st, sc, vsc, rs, pf);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       const f16x8 v0 = codes_to_f16(vc[i].x, vc[i].y), v1 = codes_to_f16(vc[i].z, vc[i].w);
@@ -334,44 +338,58 @@ __global__ __launch_bounds__(256, few_waves(T, DC)) void attend_few_kernel(const
   }
 }
 
-// Many query rows.  Workgroup: 4 waves of RT tiles of 16 rows.  Blocks of 64 keys
-// and values are brought to LDS as fp16 once for all four waves, two buffers
-// in turn: while one is worked on, the next block's codes are on their way
-// into registers and are converted at the end of the step.  The page numbers
-// run two blocks ahead, the scales one (threads 0 .. 3, one to a group of 16
-// keys), so that no step waits for a chain of loads.
-// LDS rows have an odd number of 16-byte units, so that 16 neighbouring rows
-// fall on different banks; key 16 g + 4 t + i is row 16 t + 4 g + i, which
-// puts the rows of one fragment side by side.
-// RT is 2 while a wave's registers hold it (fp32 queries above 128 d: 1);
-// up to 128 d of 16-bit queries two workgroups share a CU, so that one's
-// products run under the other's exponentials.
+// Keeps DEPTH operand fragments (one LDS read each) on their way ahead of the
+// matrix-core instructions that use them, PER to a fragment, N fragments in
+// all.  (Left alone, the compiler waits for every read right after it.)
+template <int N, int DEPTH, int PER>
+__device__ __forceinline__ void read_ahead() {
+  __builtin_amdgcn_sched_group_barrier(0x100, DEPTH, 0);
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);
+    if (q + DEPTH < N) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+}
+
+// Many query rows.  Workgroup: 8 waves (4 above 128 d and for fp32 queries)
+// of RT tiles of 16 rows.  Blocks of 64 keys and values are brought to LDS as
+// fp16 once for all waves, two buffers in turn: while one is worked on, the
+// next block's codes are on their way into registers and are converted at
+// the end of the step.  Page numbers run two blocks ahead, scales one
+// (threads 0 .. 3, one to a group of 16 keys), so that no step waits for a
+// chain of loads.
+// LDS holds the operands fragment by fragment, 1 KB each, in the order in
+// which the lanes read them; key fragment (t, c): keys 16 g + 4 t + i at row
+// 4 g + i, d 32 c .., value fragment (i, h): d 16 i .., keys 16 g + 8 h ...
+// A wave's copies take 64 bytes of each of 16 rows, which spreads its writes
+// over all banks.
+constexpr int many_waves(int t, int dc) { return t == EL_F32 || dc > 4 ? 4 : 8; }
 constexpr int many_rt(int t, int dc) { return t == EL_F32 && dc > 4 ? 1 : 2; }
-constexpr int many_waves(int t, int dc) { return t == EL_F32 ? (dc <= 2 ? 2 : 1) : dc <= 4 ? 2 : 1; }
 
 template <int T, int DC>
-__global__ __launch_bounds__(256, many_waves(T, DC)) void attend_many_kernel(const AttendArgs a, int tiles, int parts) {
+__global__ __launch_bounds__(64 * many_waves(T, DC)) void attend_many_kernel(const AttendArgs a, int tiles, int parts) {
   typedef typename Elem<T>::type E;
   constexpr int D = DC * 32;
   constexpr int NT = T == EL_F32 ? 2 : 1;
-  constexpr int RT = many_rt(T, DC), ROWS = 64 * RT;
-  constexpr int KPITCH = 2 * D + 16, VPITCH = 2 * kBlockKeys + 16;
-  constexpr int KBYTES = kBlockKeys * KPITCH, BUF = KBYTES + D * VPITCH;
-  constexpr int KU = kBlockKeys * D / 16, CU = (KU + 255) / 256;  // 16-code units of a block (keys; values have as many)
-  __shared__ __attribute__((aligned(16))) unsigned char s_kv[2 * BUF];
-  __shared__ int64_t s_slot[4][4];
+  constexpr int RT = many_rt(T, DC), NW = many_waves(T, DC), ROWS = NW * 16 * RT;
+  constexpr int TILE = kBlockKeys * D * 2;                         // bytes of a key or value tile
+  constexpr int CK = ((D + 63) / 64 + NW / 4 - 1) / (NW / 4);      // 16-code units of a key tile per thread
+  constexpr int CV = (D / 16 + NW - 1) / NW;                       // and of a value tile
+  __shared__ __attribute__((aligned(16))) unsigned char s_k[2 * TILE], s_v[2 * TILE];
+  __shared__ int64_t s_koff[4][4], s_voff[4][4];  // byte offsets of a block's groups; -1: no tokens
   __shared__ float s_ks[4][4], s_vs[4][4];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lg = lane >> 4;
-  // An XCD takes a contiguous range: whole (sequence, head) pairs share their
-  // keys and values in its L2.  The longest causal rows come first.
+  // An XCD takes a contiguous range: whole (head, sequence) pairs share their
+  // keys and values in its L2, and sequences of different lengths meet on
+  // every XCD.  The longest causal rows come first.
   int id = xcd_remap(blockIdx.x, gridDim.x);
   const int part = id % parts;
   id /= parts;
   const int tile = tiles - 1 - id % tiles;
-  const int head = id / tiles % a.c.heads, b = id / tiles / a.c.heads;
+  const int b = id / tiles % a.batch, head = id / tiles / a.batch;
   const Seq sq = load_seq(a.c, b);
   const Share sh = share_of(a, sq, tile, ROWS, part, parts);
   if (sh.nrows <= 0) return;
@@ -381,8 +399,7 @@ __global__ __launch_bounds__(256, many_waves(T, DC)) void attend_many_kernel(con
   Sight see[RT];
   RowState rs[RT];
   f32x4 acc[RT][D / 16];
-  const int w0 = wave * 16 * RT;                                 // the wave's first row
-  const bool work = w0 < sh.nrows;
+  const int w0 = wave * 16 * RT;                                   // the wave's first row
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     const int row = sh.r0 + min(w0 + 16 * r + lr, sh.nrows - 1);
@@ -393,61 +410,95 @@ __global__ __launch_bounds__(256, many_waves(T, DC)) void attend_many_kernel(con
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) acc[r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  // What the wave's rows see together, and what each of them sees.
-  const int wl = sh.r0 + min(w0, sh.nrows - 1), wh = sh.r0 + min(w0 + 16 * RT - 1, sh.nrows - 1);
-  const Sight first = sight_of(a, sq, sh.total, wl), last = sight_of(a, sq, sh.total, wh);
 
   const int P = 1 << a.c.page_log;
   const int32_t* table = a.c.table + b * a.c.stride;
   const int nblk = sh.blk1 - sh.blk0;
   const int kb0 = sh.kb0 + sh.blk0 * kBlockKeys;
+  // Blocks [na, nb) are seen by some row of the wave; every row of it sees
+  // all keys of [last.lo, first.hi).
+  const Sight first = sight_of(a, sq, sh.total, sh.r0 + min(w0, sh.nrows - 1));
+  const Sight last = sight_of(a, sq, sh.total, sh.r0 + min(w0 + 16 * RT - 1, sh.nrows - 1));
+  const int na = max(0, first.lo - kb0) / kBlockKeys;
+  const int nb = w0 < sh.nrows ? min(nblk, (max(0, last.hi - kb0) + kBlockKeys - 1) / kBlockKeys) : 0;
 
-  // Threads 0 .. 3: page number, then slot and scales, of group tid of block n.
+  // Threads 0 .. 3: page number, then offsets and scales, of group tid of block n.
   auto page_of = [&](int n) {
     const int key = kb0 + n * kBlockKeys + 16 * tid;
     return n < nblk && key < sh.hi ? table[key >> a.c.page_log] : -1;
   };
-  auto slot_of = [&](int page) {
-    return page >= 0 && page < a.c.n_pages ? static_cast<int64_t>(page) * a.c.heads + head : int64_t(-1);
+  auto place = [&](int n, int page) {
+    const bool ok = page >= 0 && page < a.c.n_pages;
+    const int64_t slot = ok ? static_cast<int64_t>(page) * a.c.heads + head : 0;
+    const int64_t at = (slot * D) << a.c.page_log;
+    const int token = (kb0 + n * kBlockKeys + 16 * tid) & (P - 1);
+    s_koff[n & 3][tid] = ok ? at + token * D : -1;
+    s_voff[n & 3][tid] = ok ? at + token : -1;
+    return ok ? slot : int64_t(-1);
   };
-  uint4 ck[CU], cv[CU];
-  auto fetch = [&](int n) {
-    const int kb = kb0 + n * kBlockKeys;
+  // This thread's units: keys 16 g + 4 (wave % 4) + i (g = lane / 4 % 4, i = lane % 4)
+  // and d 64 dq + 16 (lane / 16), dq = wave / 4 + NW / 4 u; values d 16 (wave + NW u) + lane % 16,
+  // keys 16 (lane / 16).
+  const int kg = (lane >> 2) & 3, dq0 = wave >> 2;
+  const int kin = (4 * (wave & 3) + (lane & 3)) * D + 64 * dq0 + 16 * lg;
+  const int vin = (16 * wave + lr) << a.c.page_log;
+  uint4 ck[CK], cv[CV];
+  auto has_k = [&](int u) { return D % (16 * NW) == 0 || 64 * (dq0 + NW / 4 * u) + 16 * lg < D; };
+  auto has_v = [&](int u) { return D % (16 * NW) == 0 || 16 * (wave + NW * u) < D; };
+  auto fetch_k = [&](int n) {
+    const int8_t* p = a.c.k + max(s_koff[n & 3][kg], int64_t(0)) + kin;
 #pragma unroll
-    for (int u = 0; u < CU; ++u) {
-      const int i = tid + u * 256;
-      if (KU % 256 && i >= KU) continue;
-      const int key = i / (D / 16), d = i % (D / 16) * 16;
-      const int64_t sk = max(s_slot[n & 3][key >> 4], int64_t(0));
-      ck[u] = *reinterpret_cast<const uint4*>(a.c.k + (sk * P + ((kb + key) & (P - 1))) * D + d);
-      const int64_t sv = max(s_slot[n & 3][i & 3], int64_t(0));
-      cv[u] = *reinterpret_cast<const uint4*>(a.c.v + (sv * D + (i >> 2)) * P + ((kb + 16 * (i & 3)) & (P - 1)));
-    }
+    for (int u = 0; u < CK; ++u)
+      if (has_k(u)) ck[u] = *reinterpret_cast<const uint4*>(p + 16 * NW * u);
   };
-  auto convert = [&](int n) {
-    unsigned char* buf = s_kv + (n & 1) * BUF;
+  auto fetch_v = [&](int n) {
+    const int8_t* p = a.c.v + max(s_voff[n & 3][lg], int64_t(0)) + vin;
 #pragma unroll
-    for (int u = 0; u < CU; ++u) {
-      const int i = tid + u * 256;
-      if (KU % 256 && i >= KU) continue;
-      const int key = i / (D / 16), d = i % (D / 16) * 16;
-      const int krow = ((key >> 2) & 3) * 16 + (key >> 4) * 4 + (key & 3);
-      f16x8* pk = reinterpret_cast<f16x8*>(buf + krow * KPITCH + 2 * d);
-      pk[0] = codes_to_f16(ck[u].x, ck[u].y);
-      pk[1] = codes_to_f16(ck[u].z, ck[u].w);
-      f16x8* pv = reinterpret_cast<f16x8*>(buf + KBYTES + (i >> 2) * VPITCH + 32 * (i & 3));
-      pv[0] = codes_to_f16(cv[u].x, cv[u].y);
-      pv[1] = codes_to_f16(cv[u].z, cv[u].w);
+    for (int u = 0; u < CV; ++u)
+      if (has_v(u)) cv[u] = *reinterpret_cast<const uint4*>(p + (static_cast<int64_t>(16 * NW * u) << a.c.page_log));
+  };
+  auto store_k = [&](int n) {
+    unsigned char* p = s_k + (n & 1) * TILE + ((wave & 3) * DC + 2 * dq0 + (lg >> 1)) * 1024 + (lg & 1) * 512 + lr * 16;
+#pragma unroll
+    for (int u = 0; u < CK; ++u)
+      if (has_k(u)) {
+        *reinterpret_cast<f16x8*>(p + 512 * NW * u) = codes_to_f16(ck[u].x, ck[u].y);
+        *reinterpret_cast<f16x8*>(p + 512 * NW * u + 256) = codes_to_f16(ck[u].z, ck[u].w);
+      }
+  };
+  auto store_v = [&](int n) {
+    unsigned char* p = s_v + (n & 1) * TILE + wave * 2048 + lane * 16;
+#pragma unroll
+    for (int u = 0; u < CV; ++u)
+      if (has_v(u)) {
+        *reinterpret_cast<f16x8*>(p + 2048 * NW * u) = codes_to_f16(cv[u].x, cv[u].y);
+        *reinterpret_cast<f16x8*>(p + 2048 * NW * u + 1024) = codes_to_f16(cv[u].z, cv[u].w);
+      }
+  };
+  auto scores = [&](int n, f32x4 (&st)[RT][4]) {
+    const unsigned char* kt = s_k + (n & 1) * TILE + lane * 16;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) st[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < DC; ++c) {
+        const f16x8 k = *reinterpret_cast<const f16x8*>(kt + (t * DC + c) * 1024);
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int x = 0; x < NT; ++x) st[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qf[r][x][c], st[r][t], 0, 0, 0);
+      }
     }
   };
 
-  int page2 = -1;                    // page number of block n + 2
+  int page3 = -1;                    // page number of block n + 3
   float ks1 = 0.f, vs1 = 0.f;        // scales of block n + 1
+  int64_t slot2 = -1;                // slot of block n + 2
   if (tid < 4) {
-    const int64_t s0 = slot_of(page_of(0)), s1 = slot_of(page_of(1));
-    page2 = page_of(2);
-    s_slot[0][tid] = s0;
-    s_slot[1][tid] = s1;
+    const int64_t s0 = place(0, page_of(0)), s1 = place(1, page_of(1));
+    slot2 = place(2, page_of(2));
+    page3 = page_of(3);
     s_ks[0][tid] = s0 >= 0 ? a.c.ks[s0] : 0.f;
     s_vs[0][tid] = s0 >= 0 ? a.c.vs[s0] : 0.f;
     ks1 = s1 >= 0 ? a.c.ks[s1] : 0.f;
@@ -455,69 +506,65 @@ __global__ __launch_bounds__(256, many_waves(T, DC)) void attend_many_kernel(con
   }
   __syncthreads();
   if (nblk > 0) {
-    fetch(0);
-    convert(0);
+    fetch_k(0);
+    fetch_v(0);
+    store_k(0);
+    store_v(0);
   }
   __syncthreads();
 
   for (int n = 0; n < nblk; ++n) {
-    if (n + 1 < nblk) fetch(n + 1);
+    if (n + 1 < nblk) {
+      fetch_k(n + 1);
+      fetch_v(n + 1);
+    }
     if (tid < 4) {
       s_ks[(n + 1) & 3][tid] = ks1;
       s_vs[(n + 1) & 3][tid] = vs1;
-      const int64_t s2 = slot_of(page2);
-      s_slot[(n + 2) & 3][tid] = s2;
-      ks1 = s2 >= 0 ? a.c.ks[s2] : 0.f;
-      vs1 = s2 >= 0 ? a.c.vs[s2] : 0.f;
-      page2 = page_of(n + 3);
+      ks1 = slot2 >= 0 ? a.c.ks[slot2] : 0.f;
+      vs1 = slot2 >= 0 ? a.c.vs[slot2] : 0.f;
+      slot2 = place(n + 3, page3);
+      page3 = page_of(n + 4);
     }
-    const int kb = kb0 + n * kBlockKeys;
-    // Blocks that none of the wave's rows sees are left out.
-    if (work && kb < last.hi && kb + kBlockKeys > first.lo) {
-      const unsigned char* kt = s_kv + (n & 1) * BUF + lr * KPITCH + 16 * lg;
+    if (n >= na && n < nb) {
+      const int kb = kb0 + n * kBlockKeys;
       f32x4 st[RT][4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r) st[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < DC; ++c) {
-          const f16x8 k = *reinterpret_cast<const f16x8*>(kt + 16 * t * KPITCH + 64 * c);
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int x = 0; x < NT; ++x) st[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qf[r][x][c], st[r][t], 0, 0, 0);
-        }
-      }
-      const bool in = s_slot[n & 3][lg] >= 0;
+      scores(n, st);
+      read_ahead<4 * DC, 4, RT * NT>();
+      const bool in = s_koff[n & 3][lg] >= 0;
       const float ks = s_ks[n & 3][lg], vs = s_vs[n & 3][lg];
-      const bool all = kb >= last.lo && kb + kBlockKeys <= first.hi && __all(in);
-      f16x8 pf[RT][NT][2];
       float sc[RT], vsc[RT];
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         sc[r] = ks * cq[r];
         vsc[r] = vs;
       }
-      if (!all) {
+      if (!(kb >= last.lo && kb + kBlockKeys <= first.hi && __all(in))) {
 #pragma unroll
         for (int r = 0; r < RT; ++r) hide(st[r], sc[r], vsc[r], in, kb + 16 * lg, see[r]);
       }
 #pragma unroll
-      for (int r = 0; r < RT; ++r) probabilities<NT>(st[r], sc[r], vsc[r], rs[r], acc[r], pf[r]);
-      const unsigned char* vt = s_kv + (n & 1) * BUF + KBYTES + lr * VPITCH + 32 * lg;
+      for (int r = 0; r < RT; ++r) follow_maximum(st[r], sc[r], vsc[r], rs[r], acc[r]);
+      f16x8 pf[RT][NT][2];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) probabilities<NT>(st[r], sc[r], vsc[r], rs[r], pf[r]);
+      const unsigned char* vt = s_v + (n & 1) * TILE + lane * 16;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const f16x8 v = *reinterpret_cast<const f16x8*>(vt + 16 * i * VPITCH + 16 * h);
+          const f16x8 v = *reinterpret_cast<const f16x8*>(vt + (2 * i + h) * 1024);
 #pragma unroll
           for (int r = 0; r < RT; ++r)
 #pragma unroll
             for (int x = 0; x < NT; ++x) acc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pf[r][x][h], acc[r][i], 0, 0, 0);
         }
+      read_ahead<D / 8, 4, RT * NT>();
     }
-    if (n + 1 < nblk) convert(n + 1);
+    if (n + 1 < nblk) {
+      store_k(n + 1);
+      store_v(n + 1);
+    }
     __syncthreads();
   }
 
@@ -598,14 +645,14 @@ template <int T, int DC>
 static void go_attend(const AttendArgs& a, hipStream_t s) {
   const int64_t rows = static_cast<int64_t>(a.c.max_new) * a.group, pairs = static_cast<int64_t>(a.batch) * a.c.heads;
   const bool many = rows > 32;
-  const int tile_rows = many ? 64 * many_rt(T, DC) : kFewRows;
+  const int tile_rows = many ? 16 * many_waves(T, DC) * many_rt(T, DC) : kFewRows;
   const int64_t tiles = (rows + tile_rows - 1) / tile_rows, wgs = pairs * tiles;
   // Parts of the keys where the rows alone do not fill the chip, each at
   // least one round of the workgroup's waves long, as the workspace allows.
   int64_t keys = a.max_total;
   if (a.window && keys > static_cast<int64_t>(a.window) + a.c.max_new) keys = static_cast<int64_t>(a.window) + a.c.max_new;
   const int64_t most = (keys + 255) / 256, room = static_cast<int64_t>(a.ws_bytes) / (tile_rows * (a.D + 2) * 4 * wgs);
-  int64_t parts = 256 * (many ? many_waves(T, DC) : few_waves(T, DC)) / wgs;
+  int64_t parts = 256 * (many ? 1 : few_waves(T, DC)) / wgs;
   parts = parts < kMaxParts ? parts : kMaxParts;
   parts = parts < most ? parts : most;
   parts = parts < room ? parts : room;
@@ -613,7 +660,7 @@ static void go_attend(const AttendArgs& a, hipStream_t s) {
   const int nt = static_cast<int>(tiles), np = static_cast<int>(parts);
   const dim3 grid(static_cast<unsigned>(wgs * parts));
   if (many)
-    attend_many_kernel<T, DC><<<grid, 256, 0, s>>>(a, nt, np);
+    attend_many_kernel<T, DC><<<grid, 64 * many_waves(T, DC), 0, s>>>(a, nt, np);
   else
     attend_few_kernel<T, DC><<<grid, 256, 0, s>>>(a, nt, np);
   if (np > 1)
