@@ -172,7 +172,12 @@ __device__ __forceinline__ void probabilities(const f32x4 (&st)[4], float sc, fl
   for (int j = 0; j < 16; ++j) {
     const float p = __builtin_amdgcn_exp2f(fmaf(st[j >> 2][j & 3], sc, neg));
     sum[j & 3] += p;
-    const float w = p * vf;
+    float w = p * vf;
+    // Both terms start from the rounded product: the compiler would otherwise
+    // take the first from the exact one (a fused multiply and conversion) for
+    // one of its two uses, and near a tie the second term would belong to
+    // another first one (seen: 2^-10 of a probability).
+    if constexpr (NT > 1) asm volatile("" : "+v"(w));
     const _Float16 hi = static_cast<_Float16>(w);
     pf[0][j >> 3][j & 7] = hi;
     if constexpr (NT > 1) pf[1][j >> 3][j & 7] = static_cast<_Float16>(w - static_cast<float>(hi));
@@ -478,11 +483,14 @@ __global__ __launch_bounds__(64 * many_waves(T, DC)) void attend_many_kernel(con
   auto scores = [&](int n, f32x4 (&st)[RT][4]) {
     const unsigned char* kt = s_k + (n & 1) * TILE + lane * 16;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int r = 0; r < RT; ++r) st[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // (Products into the same accumulator are kept apart, here and below.)
 #pragma unroll
-      for (int c = 0; c < DC; ++c) {
+    for (int c = 0; c < DC; ++c) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
         const f16x8 k = *reinterpret_cast<const f16x8*>(kt + (t * DC + c) * 1024);
 #pragma unroll
         for (int r = 0; r < RT; ++r)
@@ -550,9 +558,9 @@ __global__ __launch_bounds__(64 * many_waves(T, DC)) void attend_many_kernel(con
       for (int r = 0; r < RT; ++r) probabilities<NT>(st[r], sc[r], vsc[r], rs[r], pf[r]);
       const unsigned char* vt = s_v + (n & 1) * TILE + lane * 16;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int i = 0; i < D / 16; ++i) {
           const f16x8 v = *reinterpret_cast<const f16x8*>(vt + (2 * i + h) * 1024);
 #pragma unroll
           for (int r = 0; r < RT; ++r)
@@ -641,16 +649,56 @@ __global__ __launch_bounds__(128) void join_kernel(const AttendArgs a, int tiles
   }
 }
 
+// The same for tiles of many rows in a few parts: 16 rows a workgroup, 16
+// threads a row (2 parts of 128 x 256 rows: 29 us for 42 with a workgroup a
+// row; 32 parts: 52 for 36).
+template <int T>
+__global__ __launch_bounds__(256) void join_many_kernel(const AttendArgs a, int tiles, int tile_rows, int parts) {
+  typedef typename Elem<T>::type E;
+  const int D = a.D, tid = threadIdx.x;
+  const int slices = tile_rows / 16;
+  const int k = static_cast<int>(blockIdx.x) % slices * 16 + (tid >> 4), id = static_cast<int>(blockIdx.x) / slices;
+  const int tile = id % tiles, head = id / tiles % a.c.heads, b = id / tiles / a.c.heads;
+  const Seq sq = load_seq(a.c, b);
+  const int row = tile * tile_rows + k;
+  if (row >= sq.count * a.group) return;
+  const int64_t size = static_cast<int64_t>(tile_rows) * (D + 2);
+  const float* ws = static_cast<const float*>(a.ws) + static_cast<int64_t>(id) * parts * size;
+  const float* wm = ws + tile_rows * D + k;
+  float m = -INFINITY;
+  for (int p = 0; p < parts; ++p) m = fmaxf(m, wm[p * size]);
+  m = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  for (int p = 0; p < parts; ++p) l += __builtin_amdgcn_exp2f(wm[p * size] - m) * wm[p * size + tile_rows];
+  E* o = static_cast<E*>(a.o) + (sq.start + row / a.group) * a.o_t + (head * a.group + row % a.group) * a.o_h;
+  for (int d = (tid & 15) * 4; d < D; d += 64) {
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p)
+      v += *reinterpret_cast<const f32x4*>(ws + p * size + static_cast<int64_t>(k) * D + d) *
+           __builtin_amdgcn_exp2f(wm[p * size] - m);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[d + i] = static_cast<E>(l == 0.f ? 0.f : v[i] / l);
+  }
+}
+
 template <int T, int DC>
 static void go_attend(const AttendArgs& a, hipStream_t s) {
   const int64_t rows = static_cast<int64_t>(a.c.max_new) * a.group, pairs = static_cast<int64_t>(a.batch) * a.c.heads;
-  const bool many = rows > 32;
+  int64_t keys = a.max_total;
+  if (a.window && keys > static_cast<int64_t>(a.window) + a.c.max_new) keys = static_cast<int64_t>(a.window) + a.c.max_new;
+  // The kernel for many rows pays where its tiles are filled and the chip is:
+  // from about 80 rows (128 up to 64 d) a sequence and cache head, and enough
+  // units of 16 rows x 64 keys over all of them (us, few / many: 100 rows of
+  // 128 d, 20000 units 44 / 33; 256 rows, 16000 units 39 / 36; 100 rows, 2500
+  // units 21 / 25; 2000 rows of 64 d, 32000 units 44 / 51).
+  const int64_t seen = a.causal && !a.window ? keys - a.c.max_new / 2 : keys;
+  const int64_t units = pairs * ((rows + 15) / 16) * ((seen + kBlockKeys - 1) / kBlockKeys);
+  const bool many = rows > (DC <= 2 ? 128 : 80) && units >= (DC <= 2 ? 40000 : 16000);
   const int tile_rows = many ? 16 * many_waves(T, DC) * many_rt(T, DC) : kFewRows;
   const int64_t tiles = (rows + tile_rows - 1) / tile_rows, wgs = pairs * tiles;
   // Parts of the keys where the rows alone do not fill the chip, each at
   // least one round of the workgroup's waves long, as the workspace allows.
-  int64_t keys = a.max_total;
-  if (a.window && keys > static_cast<int64_t>(a.window) + a.c.max_new) keys = static_cast<int64_t>(a.window) + a.c.max_new;
   const int64_t most = (keys + 255) / 256, room = static_cast<int64_t>(a.ws_bytes) / (tile_rows * (a.D + 2) * 4 * wgs);
   int64_t parts = 256 * (many ? 1 : few_waves(T, DC)) / wgs;
   parts = parts < kMaxParts ? parts : kMaxParts;
@@ -663,7 +711,9 @@ static void go_attend(const AttendArgs& a, hipStream_t s) {
     attend_many_kernel<T, DC><<<grid, 64 * many_waves(T, DC), 0, s>>>(a, nt, np);
   else
     attend_few_kernel<T, DC><<<grid, 256, 0, s>>>(a, nt, np);
-  if (np > 1)
+  if (np > 1 && np <= 4 && many)
+    join_many_kernel<T><<<dim3(static_cast<unsigned>(wgs * (tile_rows / 16))), 256, 0, s>>>(a, nt, tile_rows, np);
+  else if (np > 1)
     join_kernel<T><<<dim3(static_cast<unsigned>(wgs * tile_rows)), 128, 0, s>>>(a, nt, tile_rows, np);
 }
 

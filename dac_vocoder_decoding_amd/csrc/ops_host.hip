@@ -102,7 +102,7 @@ voc_status check_cache(voc_ops* o, const voc_kv_cache* c, const voc_kv_batch* b,
   if (b->batch < 0 || b->batch > 65535) return fail(o, VOC_INVALID_PARAMS, "batch must be 0 .. 65535");
   if (b->tokens < 0 || b->tokens > kMaxInt || b->max_new < 0 || b->max_new > (1 << 24))
     return fail(o, VOC_INVALID_PARAMS, "tokens or max_new out of range");
-  if (b->table_stride < 1 || (b->table_stride << log) > kMaxInt - (1 << 25) || b->table_stride > kMaxInt)
+  if (b->table_stride < 1 || b->table_stride > (kMaxInt - (1 << 25)) >> log)
     return fail(o, VOC_INVALID_PARAMS, "table_stride out of range");
   if (b->max_total < 0 || b->max_total > kMaxInt) return fail(o, VOC_INVALID_PARAMS, "max_total out of range");
   if (b->batch && (!b->starts || !b->past || !b->page_table)) return fail(o, VOC_INVALID_PARAMS, "NULL batch pointer");

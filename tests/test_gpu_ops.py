@@ -454,6 +454,19 @@ ATTEND = [
     (32, 1, 64, 40, [90], [2], True, 0),
     (64, 1, 64, 1, [5000], [1], True, 0),
     (64, 2, 64, 1, [130], [130], False, 0),
+    # Enough rows and keys for the kernel of many rows (whole, then in parts),
+    # every size of head, windows, ragged tiles and pages.
+    (64, 8, 128, 2, [0, 37], [1300, 1111], True, 0),
+    (32, 2, 96, 1, [1], [2500], True, 0),
+    (16, 16, 64, 1, [0, 3], [2049, 1900], True, 0),
+    (128, 16, 32, 1, [0], [2900], False, 0),
+    (64, 2, 256, 1, [0], [2300], True, 0),
+    (32, 2, 224, 1, [9], [2301], True, 0),
+    (16, 2, 160, 1, [2000], [1500], True, 0),
+    (64, 4, 192, 1, [100], [1500], False, 0),
+    (64, 4, 128, 8, [9000], [40], True, 0),
+    (16, 8, 128, 4, [5], [1700], True, 700),
+    (64, 8, 64, 2, [6000, 100, 5000], [300, 0, 299], True, 0),
 ]
 
 
@@ -593,6 +606,28 @@ def test_append_then_attend_by_chunks(ops):
     # In the mean they are far closer: a few per cent.
     assert (outs[1] - outs[0]).norm() <= 0.1 * outs[0].norm()
     assert (outs[2] - outs[0]).norm() <= 0.1 * outs[0].norm()
+
+
+def test_cache_beyond_4_gib(ops):
+    """Pages whose codes lie past 32-bit byte offsets, for both attention kernels."""
+    g = gen(85)
+    P, H, D = 128, 8, 256
+    pages = 17000                                  # 4.4 GB of key codes
+    cache = V.KVCache.from_tensors(
+        torch.empty(pages, H, P, D, dtype=torch.int8, device="cuda"),
+        torch.empty(pages, H, D, P, dtype=torch.int8, device="cuda"),
+        torch.full((pages, H), float("nan"), device="cuda"), torch.full((pages, H), float("nan"), device="cuda"))
+    for n in (200, 1500):
+        used = -(-n // P)
+        table = torch.arange(pages - used, pages, device="cuda", dtype=torch.int32).flip(0)[None].contiguous()
+        k, v, q = (randn(g, n, H, D, dtype=F16) for _ in range(3))
+        b = batch_of(table, [0], [n])
+        V.cache_append(ops, cache, b, k, v)
+        o = V.cache_attention(ops, cache, b, q)
+        ref, tol = attend64(cache, table, [0], [n], q, 1 / 16, True, 0)
+        assert ((o.double() - ref).abs() <= tol).all()
+        got = values_of(cache, table, 0, n, "v").transpose(0, 1)
+        assert ((got - v.double()).abs() <= page_scales(cache, table, 0, n, "v").t()[..., None] * (0.5 + 127 * 6 * E)).all()
 
 
 # ------------------------------------------------- streams, graphs, errors

@@ -17,3 +17,9 @@ def test_null_handles_are_refused():
     assert L.voc_ops_create(0, None) == V.VOC_INVALID_PARAMS
     assert "NULL" in V.voc_ops_last_error(None)
     V.voc_ops_destroy(None)
+
+
+def test_half_precision_is_no_decoder_dtype():
+    cfg = V.voc_config_default()
+    cfg.dtype = V.VOC_F16
+    assert V.voc_config_validate(cfg) == V.VOC_INVALID_PARAMS
