@@ -173,11 +173,13 @@ __global__ __launch_bounds__(WF * WT * 64) void int_matmul_tile_kernel(const Int
         for (int j = 0; j < FT; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xf[i], xt[j], acc[i][j], 0, 0, 0);
     }
     // The second half's fragments are read between the first half's products.
-    __builtin_amdgcn_sched_group_barrier(0x100, FT + FF, 0);
+    if constexpr (FF * FT >= FF + FT) {
+      __builtin_amdgcn_sched_group_barrier(0x100, FT + FF, 0);
 #pragma unroll
-    for (int q = 0; q < FF + FT; ++q) {
-      __builtin_amdgcn_sched_group_barrier(0x008, FF * FT / (FF + FT), 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      for (int q = 0; q < FF + FT; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x008, FF * FT / (FF + FT), 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
     }
   };
 
@@ -324,9 +326,10 @@ static void go_tile(const IntMatmulArgs& a, hipStream_t s) {
 //    256x256 from 192 tiles (8000x4096x1024: 56 against 60 for 128x128;
 //    8000x1024x4096, 128 tiles: 59 against 39), 128x128 from 384 (two
 //    workgroups a CU), 128x64 from 384 (1000x4096x1024: 11.0 against 13.7
-//    and 14.2), else 64x64 (2000x1024x1024: 7.9 against 8.3);
+//    and 14.2), else 64x64 (2000x1024x1024: 7.9 against 8.3) with eight
+//    waves (500x1024x4096: 11.9 against 12.4 with four);
 //  * rows that are not 16-byte aligned go through registers in 64x64 tiles
-//    (689x1504x1504: 10.9 against 9.0 for aligned rows).
+//    (689x1000x1501: 11.0; four waves 12.5, 128x64 17.4).
 template <int T>
 static void go_int_matmul(const IntMatmulArgs& a, hipStream_t s) {
   auto tiles = [&](int f, int t) { return static_cast<int64_t>((a.N + f - 1) / f) * ((a.M + t - 1) / t); };
@@ -342,7 +345,7 @@ static void go_int_matmul(const IntMatmulArgs& a, hipStream_t s) {
     else
       int_matmul_few_kernel<T, 4><<<dim3(gx), 512, 0, s>>>(a, vec);
   } else if (!dma) {
-    go_tile<T, 64, 64, 2, 2, 2, false>(a, s);
+    go_tile<T, 64, 64, 4, 2, 2, false>(a, s);
   } else if (tiles(256, 256) >= 192) {
     go_tile<T, 256, 256, 2, 4, 2, true>(a, s);
   } else if (tiles(128, 128) >= 384) {
@@ -350,7 +353,7 @@ static void go_int_matmul(const IntMatmulArgs& a, hipStream_t s) {
   } else if (tiles(128, 64) >= 384) {
     go_tile<T, 128, 64, 2, 2, 3, true>(a, s);
   } else {
-    go_tile<T, 64, 64, 2, 2, 4, true>(a, s);
+    go_tile<T, 64, 64, 4, 2, 4, true>(a, s);
   }
 }
 
