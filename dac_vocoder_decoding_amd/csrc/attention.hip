@@ -609,49 +609,69 @@ __global__ __launch_bounds__(64 * many_waves(T, DC)) void attend_many_kernel(con
   }
 }
 
-// Joins the parts of the tiles, in order.  Workgroup: one row.
-constexpr int kMaxParts = 256;
+// Joins the parts of the tiles.  Workgroup: one row (of the first `live` rows
+// of a tile).  The factors of all parts first, then four d a thread, the parts
+// split over the threads that are left; every order of summation follows from
+// the sizes alone.  Bound by the latency of three dependent steps: 256 parts of
+// 16 rows x 64 d take 5.6 us (16.5 when a row's threads go over all the parts),
+// 24 parts of 32 x 4 rows x 128 d 5.3.
+constexpr int kMaxParts = 256, kJoinThreads = 256;
 
 template <int T>
-__global__ __launch_bounds__(128) void join_kernel(const AttendArgs a, int tiles, int tile_rows, int parts) {
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(const AttendArgs a, int tiles, int tile_rows, int live,
+                                                            int parts) {
   typedef typename Elem<T>::type E;
-  __shared__ float s_f[kMaxParts], s_l[kMaxParts], s_m[2];
+  __shared__ float s_f[kMaxParts], s_m[4], s_l[4];
+  __shared__ __attribute__((aligned(16))) float s_part[4 * kJoinThreads];
   const int D = a.D, tid = threadIdx.x;
-  const int k = static_cast<int>(blockIdx.x) % tile_rows, id = static_cast<int>(blockIdx.x) / tile_rows;
+  const int k = static_cast<int>(blockIdx.x) % live, id = static_cast<int>(blockIdx.x) / live;
   const int tile = id % tiles, head = id / tiles % a.c.heads, b = id / tiles / a.c.heads;
   const Seq sq = load_seq(a.c, b);
   const int row = tile * tile_rows + k;
   if (row >= sq.count * a.group) return;
   const int64_t size = static_cast<int64_t>(tile_rows) * (D + 2);
   const float* ws = static_cast<const float*>(a.ws) + static_cast<int64_t>(id) * parts * size;
-  float m = -INFINITY;
-  for (int p = tid; p < parts; p += 128) {
-    s_f[p] = ws[p * size + tile_rows * D + k];
-    s_l[p] = ws[p * size + tile_rows * D + tile_rows + k];
-    m = fmaxf(m, s_f[p]);
+  // Thread p: the maximum and the sum of part p.
+  float mp = -INFINITY, l = 0.f;
+  if (tid < parts) {
+    mp = ws[tid * size + tile_rows * D + k];
+    l = ws[tid * size + tile_rows * D + tile_rows + k];
   }
+  float m = mp;
 #pragma unroll
   for (int x = 32; x; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
   if ((tid & 63) == 0) s_m[tid >> 6] = m;
   __syncthreads();
-  m = fmaxf(s_m[0], s_m[1]);
+  m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
   m = m == -INFINITY ? 0.f : m;
-  for (int p = tid; p < parts; p += 128) s_f[p] = __builtin_amdgcn_exp2f(s_f[p] - m);
+  const float f = __builtin_amdgcn_exp2f(mp - m);
+  s_f[tid] = f;
+  l *= f;
+#pragma unroll
+  for (int x = 32; x; x >>= 1) l += __shfl_xor(l, x);
+  if ((tid & 63) == 0) s_l[tid >> 6] = l;
   __syncthreads();
-  float l = 0.f;
-  for (int p = 0; p < parts; ++p) l += s_f[p] * s_l[p];
-  E* o = static_cast<E*>(a.o) + (sq.start + row / a.group) * a.o_t + (head * a.group + row % a.group) * a.o_h;
-  for (int d = tid; d < D; d += 128) {
-    float v = 0.f;
+  const int d4 = D >> 2, slices = kJoinThreads / d4, slice = tid / d4, d = 4 * (tid - slice * d4);
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if (slice < slices) {
+    const float* p = ws + static_cast<int64_t>(k) * D + d;
 #pragma unroll 8
-    for (int p = 0; p < parts; ++p) v += s_f[p] * ws[p * size + k * D + d];
-    o[d] = static_cast<E>(l == 0.f ? 0.f : v / l);
+    for (int j = slice; j < parts; j += slices) v += *reinterpret_cast<const f32x4*>(p + j * size) * s_f[j];
+    *reinterpret_cast<f32x4*>(s_part + 4 * tid) = v;
   }
+  __syncthreads();
+  if (slice) return;
+  for (int j = 1; j < min(slices, parts); ++j) v += *reinterpret_cast<const f32x4*>(s_part + 4 * (tid + j * d4));
+  l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+  E* o = static_cast<E*>(a.o) + (sq.start + row / a.group) * a.o_t + (head * a.group + row % a.group) * a.o_h + d;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = static_cast<E>(l == 0.f ? 0.f : v[i] / l);
 }
 
-// The same for tiles of many rows in a few parts: 16 rows a workgroup, 16
-// threads a row (2 parts of 128 x 256 rows: 29 us for 42 with a workgroup a
-// row; 32 parts: 52 for 36).
+// The same for 16 rows a workgroup, 16 threads a row: for tiles whose rows are
+// all there and in up to four parts (us, against a workgroup a row: 2 parts of
+// 512 x 16 rows of 64 d 4.6 / 14.0, 2 parts of 128 x 256 rows of 128 d 29 /
+// 42; 32 parts 52 / 36, 4 parts of one row of 256 d 6.1 / 4.0).
 template <int T>
 __global__ __launch_bounds__(256) void join_many_kernel(const AttendArgs a, int tiles, int tile_rows, int parts) {
   typedef typename Elem<T>::type E;
@@ -707,14 +727,15 @@ static void go_attend(const AttendArgs& a, hipStream_t s) {
   if (parts < 1) parts = 1;
   const int nt = static_cast<int>(tiles), np = static_cast<int>(parts);
   const dim3 grid(static_cast<unsigned>(wgs * parts));
+  const int live = static_cast<int>(rows < tile_rows ? rows : tile_rows);
   if (many)
     attend_many_kernel<T, DC><<<grid, 64 * many_waves(T, DC), 0, s>>>(a, nt, np);
   else
     attend_few_kernel<T, DC><<<grid, 256, 0, s>>>(a, nt, np);
-  if (np > 1 && np <= 4 && many)
+  if (np > 1 && np <= 4 && live >= 16)
     join_many_kernel<T><<<dim3(static_cast<unsigned>(wgs * (tile_rows / 16))), 256, 0, s>>>(a, nt, tile_rows, np);
   else if (np > 1)
-    join_kernel<T><<<dim3(static_cast<unsigned>(wgs * tile_rows)), 128, 0, s>>>(a, nt, tile_rows, np);
+    join_kernel<T><<<dim3(static_cast<unsigned>(wgs * live)), kJoinThreads, 0, s>>>(a, nt, tile_rows, live, np);
 }
 
 template <int T>

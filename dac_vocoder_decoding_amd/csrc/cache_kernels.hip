@@ -224,7 +224,11 @@ static void go_append(const AppendArgs& a, hipStream_t s) {
   constexpr int per16 = 16 / sizeof(typename Elem<T>::type);
   const bool vec = (reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) % 16 == 0 &&
                    (a.k_t | a.k_h | a.v_t | a.v_h) % per16 == 0;
-  if (!vec || a.c.max_new <= 4) {
+  // A few tokens leave most of a page as it is, and only a scale that grew makes
+  // the small kernel touch it (us, small / page kernel, 32 x 8 heads x 128 d,
+  // pages of 64: 1 token 5.2 / 12.0, 8 tokens 9.0 / 12.8, 25 tokens 19.6 / 14.6;
+  // 32 x 16 x 64, pages of 32: 5.5 / 7.8, 7.2 / 9.0, 10.8 / 9.0).
+  if (!vec || a.c.max_new <= 12) {
     append_kernel<T><<<grid, 256, 0, s>>>(a);
     return;
   }

@@ -199,6 +199,8 @@ VOC_API voc_status vocoder_matmul_int(voc_ops* o, int out_dtype, int64_t M, int6
   if (M < 0 || M > (1 << 24) || N < 0 || N > (1 << 24)) return fail(o, VOC_INVALID_PARAMS, "M or N out of range");
   if (K < 1 || K > 131071) return fail(o, VOC_INVALID_PARAMS, "K must be 1 .. 131071");
   if (M == 0 || N == 0) return VOC_OK;
+  // A launch holds fewer than 2^32 threads (the smallest tiles: 64 x 64 in 512).
+  if (((M + 63) / 64) * ((N + 63) / 64) >= 1 << 23) return fail(o, VOC_INVALID_PARAMS, "too many outputs for one call");
   if (!a || !a_scale || !b || !b_scale || !y) return fail(o, VOC_INVALID_PARAMS, "NULL pointer");
   if (!stride_ok(lda, K) || !stride_ok(ldb, K) || !stride_ok(ldy, N))
     return fail(o, VOC_INVALID_PARAMS, "row strides must be at least the row's length");
@@ -274,7 +276,8 @@ VOC_API voc_status vocoder_cache_attention(voc_ops* o, const voc_kv_cache* cache
   a.max_total = static_cast<int>(batch->max_total);
   a.ws = o->ws;
   a.ws_bytes = VOC_OPS_WORKSPACE_BYTES;
-  if (static_cast<int64_t>(a.batch) * heads * ((batch->max_new + 15) / 16 + 1) > kMaxInt / 64)
+  // A launch holds fewer than 2^32 threads (16 query rows in 256).
+  if (static_cast<int64_t>(a.batch) * heads * ((batch->max_new + 15) / 16 + 1) >= 1 << 24)
     return fail(o, VOC_INVALID_PARAMS, "too many query rows for one call");
   return on_device(o, "cache_attention", [&] { return launch_attend(dtype, a, static_cast<hipStream_t>(hip_stream)); });
 }

@@ -483,7 +483,7 @@ voc_status voc_dbg_peak(int what, int64_t n, double *value, void *hip_stream);
  * max|v| times the fp32 value nearest 1/127), q = rint(v * (1 / s)), ties to
  * even, |q| <= 127.  A group whose largest magnitude is below 2^-100 gets
  * s = 0 and q = 0; a group with a NaN or an infinity gets s = NaN and q = 0,
- * so that what is computed from it is NaN.
+ * so that what is computed from it is NaN.  Scales are never negative.
  *
  * Threading: as for voc_ctx, one handle per host thread and stream (the
  * handle owns the workspace in which split attention joins its parts). */
@@ -533,7 +533,7 @@ voc_status vocoder_quantize_rows(voc_ops *ops, int dtype, int64_t rows, int64_t 
  * a: int8 [M][lda], b: int8 [N][ldb] (a Linear's weight, (out, in)), scales
  * fp32 [M] and [N], bias fp32 [N] or NULL, y: out_dtype [M][ldy].
  * 1 <= K <= 131071 (the 32-bit sums are exact for any codes); M or N may be
- * 0.  act: VOC_ACT_NONE, or VOC_ACT_GELU, x/2 (1 + erf(x / sqrt(2))).
+ * 0; fewer than 2^23 blocks of 64 x 64 outputs.  act: VOC_ACT_NONE, or VOC_ACT_GELU, x/2 (1 + erf(x / sqrt(2))).
  * Any alignment and stride works; 16-byte multiples run faster.
  * Errors: VOC_INVALID_PARAMS (NULL pointer, unknown dtype or act, size or
  * stride out of range, y or the scales not aligned to their elements),
@@ -621,6 +621,8 @@ voc_status vocoder_cache_append(voc_ops *ops, const voc_kv_cache *cache, const v
  * Results do not depend on what else runs; long caches are split over
  * workgroups and the parts joined in a fixed order.
  * q and o need 16-byte alignment and strides of 16-byte multiples.
+ * batch * heads * (max_new / 16 + 1, rounded up) stays below 2^24.
+ * Rows of o that belong to no sequence are not written.
  * Errors: VOC_INVALID_PARAMS, VOC_DEVICE_ERROR.
  */
 voc_status vocoder_cache_attention(voc_ops *ops, const voc_kv_cache *cache,

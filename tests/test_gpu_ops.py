@@ -805,3 +805,43 @@ def test_binding_refuses_what_the_library_cannot_see(ops):
         V.KVBatch(i32([[0]]), i32([0]), i32([0]), 1, 1)
     with pytest.raises(ValueError):
         V.KVCache.from_tensors(cache.k, cache.k, cache.k_scale, cache.v_scale)
+
+
+def test_calls_too_large_for_one_launch_are_refused(ops):
+    L = V.lib()
+    q, s = torch.zeros(4, 64, dtype=torch.int8, device="cuda"), torch.zeros(64, device="cuda")
+    for M, N in ((1 << 24, 1 << 24), ((1 << 12) * 64, (1 << 11) * 64)):
+        assert L.vocoder_matmul_int(ops, 0, M, N, 64, q.data_ptr(), 64, s.data_ptr(), q.data_ptr(), 64, s.data_ptr(), None,
+                                    0, s.data_ptr(), N, None) == V.VOC_INVALID_PARAMS, (M, N)
+        assert "too many" in V.voc_ops_last_error(ops)
+    cache = V.KVCache(2, 16, 2, 64)
+    kv = torch.zeros(1, 2, 64, device="cuda")
+    for batch, max_new in ((65535, 2048), (1, 1 << 24)):
+        b = V.KVBatch(i32([[0]]), i32([0]), i32([0, 1]), max_new, 1)
+        b.c.tokens, b.c.batch = 1, batch
+        heads = 2 if batch > 1 else 64
+        assert L.vocoder_cache_attention(ops, cache.ref, b.ref, 0, heads, kv.data_ptr(), 128, 64, 1.0, 1, 0, kv.data_ptr(),
+                                         128, 64, None) == V.VOC_INVALID_PARAMS, (batch, max_new)
+        assert "too many" in V.voc_ops_last_error(ops)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("P,H,D,group,past,new,causal,window", [
+    (64, 1, 64, 16, [40000], [1], True, 0), (32, 1, 32, 1, [20000], [1], True, 0), (128, 1, 96, 3, [9000, 20], [1, 1], True, 0),
+    (64, 1, 160, 2, [9000], [3], False, 0), (16, 1, 256, 2, [3000], [9], True, 1500), (16, 2, 64, 1, [400, 700], [40, 1], True, 0),
+    (32, 1, 224, 5, [600], [7], True, 0), (64, 2, 192, 2, [10, 8000], [1, 1], True, 0)])
+def test_attention_joins(ops, dtype, P, H, D, group, past, new, causal, window):
+    """Caches whose keys are split: one row and sixteen to a tile, few parts and many, sequences with empty parts."""
+    test_attention(ops, dtype, P, H, D, group, past, new, causal, window)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("rows,C,pad,residual", [(5, 1025, 0, True), (9, 2048, 0, True), (3, 2047, 1, False), (2500, 1504, 8, True)])
+def test_rms_norm_of_four_waves(ops, dtype, rows, C, pad, residual):
+    test_rms_norm(ops, dtype, rows, C, pad, residual)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("past,new", [([0, 60], [12, 5]), ([0, 60], [13, 6]), ([64, 127], [8, 12])])
+def test_append_of_a_few_tokens(ops, dtype, past, new):
+    test_append_holds_the_tokens(ops, dtype, 64, 2, 96, past, new)
