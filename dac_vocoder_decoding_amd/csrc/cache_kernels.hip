@@ -37,6 +37,16 @@ __device__ __forceinline__ float joint_scale(float old, uint32_t top) {
   return !(old == old) ? old : !(own == own) ? own : fmaxf(old, own);
 }
 
+// Four codes rounded again.
+__device__ __forceinline__ uint32_t rescaled4(uint32_t c, float ratio) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    r |= (static_cast<uint32_t>(static_cast<int>(__builtin_rintf(static_cast<float>(static_cast<int8_t>(c >> (8 * k))) * ratio))) & 0xffu)
+         << (8 * k);
+  return r;
+}
+
 // Any alignment, and few new tokens.  Workgroup (j, 2 * head + is_value, sequence): the j-th page that the
 // sequence's new tokens touch.  Values are stored transposed inside a page.
 template <int T>
@@ -92,12 +102,10 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendArgs a) {
 // A page of 32 x 128 is 128 units: two waves a workgroup.
 // LDS: a key page [token][D], a value page [d][token] with rows of P + 4
 // bytes (the writes of neighbouring d then fall on different banks).
-constexpr int kPageThreads = 128;
-
-template <int T, int D>
-__global__ __launch_bounds__(kPageThreads) void append_page_kernel(const AppendArgs a) {
+template <int T, int D, int NT>
+__global__ __launch_bounds__(NT) void append_page_kernel(const AppendArgs a) {
   typedef typename Elem<T>::type E;
-  constexpr int KEEP = 2, NT = kPageThreads;
+  constexpr int KEEP = 2;
   constexpr int D8 = D >> 3;
   extern __shared__ __attribute__((aligned(16))) unsigned char s_page[];
   __shared__ uint32_t s_max[NT / 64];
@@ -154,19 +162,28 @@ __global__ __launch_bounds__(kPageThreads) void append_page_kernel(const AppendA
   // Words of a row, as a shift (a key page is one long row: its image is the page).
   const int row_log = a.c.page_log - 2;
   if (lo > 0 || hi < P) {
-    for (int w = tid; w < (P * D) >> 2; w += NT)
-      *reinterpret_cast<uint32_t*>(s_page + w * 4 + (value ? (w >> row_log) * 4 : 0)) = reinterpret_cast<const uint32_t*>(codes)[w];
+    for (int w = tid; w < (P * D) >> 4; w += NT) {
+      const uint4 c = reinterpret_cast<const uint4*>(codes)[w];
+      uint32_t* p = reinterpret_cast<uint32_t*>(s_page + w * 16 + (value ? (w >> (row_log - 2)) * 4 : 0));
+      p[0] = c.x;
+      p[1] = c.y;
+      p[2] = c.z;
+      p[3] = c.w;
+    }
   }
   __syncthreads();
-  top = max(s_max[0], s_max[1]);
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) top = max(top, s_max[w]);
   const float scale = joint_scale(old, top), inv = inverse_of(scale);
   if (lo && scale != old) {
     const float ratio = inv > 0.f ? old * inv : 0.f;
-    for (int i = tid; i < lo * D; i += NT) {
-      const int t = value ? i % lo : i / D, d = value ? i / lo : i % D;
-      int8_t* p = reinterpret_cast<int8_t*>(s_page) + (value ? d * pitch + t : t * pitch + d);
-      *p = static_cast<int8_t>(__builtin_rintf(static_cast<float>(*p) * ratio));
-    }
+    // Four codes at a time; what follows the older tokens in their last word is
+    // either written below or holds no token.
+    for (int w = tid; w < (P * D) >> 2; w += NT)
+      if (value ? 4 * (w & ((P >> 2) - 1)) < lo : 4 * w < lo * D) {
+        uint32_t* p = reinterpret_cast<uint32_t*>(s_page + w * 4 + (value ? (w >> row_log) * 4 : 0));
+        *p = rescaled4(*p, ratio);
+      }
     __syncthreads();
   }
   auto put = [&](int u, const float (&v)[4][8]) {
@@ -217,6 +234,29 @@ __global__ __launch_bounds__(kPageThreads) void append_page_kernel(const AppendA
   if (tid == 0) scales[sh.slot] = scale;
 }
 
+// A thread for every unit of a page (4 tokens x 8 values), from one wave to
+// four; one wave only where the pages are enough to fill the chip with them
+// (us, two waves / as chosen: 8 prompts of 5168 x 8 heads x 64 d, pages of 32:
+// 51.4 / 35.8; 2 prompts x 4 x 256, pages of 128: 44.0 / 27.0; 32 chunks of 25
+// x 16 x 64, pages of 32: 10.1, one wave 15.4).
+template <int T, int D>
+static void go_pages(const AppendArgs& a, dim3 grid, hipStream_t s) {
+  const int P = 1 << a.c.page_log, units = P / 4 * (D / 8);
+  const size_t lds = static_cast<size_t>(D) * (P + 4);
+  const bool full = static_cast<int64_t>(grid.x) * grid.y * grid.z >= 4096;
+  if constexpr (D <= 128)  // (larger heads have no page of 64 units, heads of 32 none of more than 128)
+    if (units <= 64 && full) {
+      append_page_kernel<T, D, 64><<<grid, 64, lds, s>>>(a);
+      return;
+    }
+  if constexpr (D > 32)
+    if (units > 128) {
+      append_page_kernel<T, D, 256><<<grid, 256, lds, s>>>(a);
+      return;
+    }
+  append_page_kernel<T, D, 128><<<grid, 128, lds, s>>>(a);
+}
+
 template <int T>
 static void go_append(const AppendArgs& a, hipStream_t s) {
   const int P = 1 << a.c.page_log;
@@ -232,16 +272,15 @@ static void go_append(const AppendArgs& a, hipStream_t s) {
     append_kernel<T><<<grid, 256, 0, s>>>(a);
     return;
   }
-  const size_t lds = static_cast<size_t>(a.D) * (P + 4);
   switch (a.D / 32) {
-    case 1: append_page_kernel<T, 32><<<grid, kPageThreads, lds, s>>>(a); break;
-    case 2: append_page_kernel<T, 64><<<grid, kPageThreads, lds, s>>>(a); break;
-    case 3: append_page_kernel<T, 96><<<grid, kPageThreads, lds, s>>>(a); break;
-    case 4: append_page_kernel<T, 128><<<grid, kPageThreads, lds, s>>>(a); break;
-    case 5: append_page_kernel<T, 160><<<grid, kPageThreads, lds, s>>>(a); break;
-    case 6: append_page_kernel<T, 192><<<grid, kPageThreads, lds, s>>>(a); break;
-    case 7: append_page_kernel<T, 224><<<grid, kPageThreads, lds, s>>>(a); break;
-    default: append_page_kernel<T, 256><<<grid, kPageThreads, lds, s>>>(a); break;
+    case 1: go_pages<T, 32>(a, grid, s); break;
+    case 2: go_pages<T, 64>(a, grid, s); break;
+    case 3: go_pages<T, 96>(a, grid, s); break;
+    case 4: go_pages<T, 128>(a, grid, s); break;
+    case 5: go_pages<T, 160>(a, grid, s); break;
+    case 6: go_pages<T, 192>(a, grid, s); break;
+    case 7: go_pages<T, 224>(a, grid, s); break;
+    default: go_pages<T, 256>(a, grid, s); break;
   }
 }
 
