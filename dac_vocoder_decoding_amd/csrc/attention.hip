@@ -188,7 +188,15 @@ __device__ __forceinline__ void probabilities(const f32x4 (&st)[4], float sc, fl
 // Few query rows.  Workgroup: 16 rows, one part of the keys; its four waves
 // take every fourth block of 64 keys, operands straight from memory, and are
 // joined in order at the end.  parts > 1: the results go to the workspace
-// (unnormalised, with their maxima and sums) for join_kernel.
+// (unnormalised, with their maxima and sums) for join_kernel.  (A join by the
+// workgroup that ends last saves a launch and costs what the launch does: its
+// reads and writes have to go past eight L2s.  1 x 8000 keys of 8 x 128 d:
+// 14.3 us for 7.9 + 5.2; with a write-back of the L2 19.2.)
+// Every key and value is read once, from memory to registers, so a long cache
+// is bound by memory: one token of 4 x 32 / 8 heads x 128 d over 65536 tokens,
+// 409 MB, 74 us (5.5 TB/s) and 5 for the join.  Short ones are bound by latency
+// (sequence, page, codes, joins): 32 x 16 x 64 over 250 tokens 7.7 us; 25 rows
+// each over a window of 72 10.4.
 constexpr int kFewRows = 16;
 constexpr int few_waves(int t, int dc) { return t == EL_F32 ? (dc <= 2 ? 3 : dc <= 4 ? 2 : 1) : dc <= 2 ? 4 : dc <= 4 ? 3 : dc <= 6 ? 2 : 1; }
 
@@ -368,6 +376,15 @@ __device__ __forceinline__ void read_ahead() {
 // 4 g + i, d 32 c .., value fragment (i, h): d 16 i .., keys 16 g + 8 h ...
 // A wave's copies take 64 bytes of each of 16 rows, which spreads its writes
 // over all banks.
+// Two prompts of 5168, 32 / 8 heads x 128 d, causal (386 G operations): 467 us,
+// 0.83 P operations a second (548 in a profiled run); a large fp16 library
+// product reaches 1.32.  The matrix cores are busy 37 % of the cycles
+// and the vector units about 54 % (160 instructions for 1024 scores of a wave,
+// conversion included): a SIMD's two waves seldom do the one while the other
+// does the other.  Not kept: scores a block ahead of the products 710 (630
+// then), two groups of waves a phase apart 523 to 677 (499), wave priorities
+// 553 to 581, the value scale inside the exponent 553 (550), 64 rows a wave
+// 1269 (spills).
 constexpr int many_waves(int t, int dc) { return t == EL_F32 || dc > 4 ? 4 : 8; }
 constexpr int many_rt(int t, int dc) { return t == EL_F32 && dc > 4 ? 1 : 2; }
 
@@ -718,7 +735,10 @@ static void go_attend(const AttendArgs& a, hipStream_t s) {
   const int tile_rows = many ? 16 * many_waves(T, DC) * many_rt(T, DC) : kFewRows;
   const int64_t tiles = (rows + tile_rows - 1) / tile_rows, wgs = pairs * tiles;
   // Parts of the keys where the rows alone do not fill the chip, each at
-  // least one round of the workgroup's waves long, as the workspace allows.
+  // least one round of the workgroup's waves long, as the workspace allows: as
+  // many workgroups as the chip holds (us, half as many / these / twice: 4 x
+  // 65536 keys of 8 x 128 d 90 / 84 / 87, 32 x 2000 29 / 25 / 30, 16 x 16000
+  // of 2 x 256 74 / 49 / 55).
   const int64_t most = (keys + 255) / 256, room = static_cast<int64_t>(a.ws_bytes) / (tile_rows * (a.D + 2) * 4 * wgs);
   int64_t parts = 256 * (many ? 1 : few_waves(T, DC)) / wgs;
   parts = parts < kMaxParts ? parts : kMaxParts;

@@ -47,8 +47,11 @@ __device__ __forceinline__ uint32_t rescaled4(uint32_t c, float ratio) {
   return r;
 }
 
-// Any alignment, and few new tokens.  Workgroup (j, 2 * head + is_value, sequence): the j-th page that the
-// sequence's new tokens touch.  Values are stored transposed inside a page.
+// Any alignment, and few new tokens.  Workgroup (j, 2 * head + is_value,
+// sequence): the j-th page that the sequence's new tokens touch.  Values are
+// stored transposed inside a page.  Bound by latency, a chain of three loads
+// (the sequence, its page, the new row and the old scale): one token of 32 x 8
+// heads x 128 d 5.2 us.
 template <int T>
 __global__ __launch_bounds__(256) void append_kernel(const AppendArgs a) {
   typedef typename Elem<T>::type E;
@@ -99,7 +102,9 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendArgs a) {
 // there, four tokens of one d to a 32-bit word.  The new rows stay in
 // registers between the maximum and the codes where a thread has up to four
 // units (4 tokens x 8 values); larger pages read the rest a second time.
-// A page of 32 x 128 is 128 units: two waves a workgroup.
+// Bound by memory and by each page's chain of loads: 8 prompts of up to 5168
+// bf16 tokens of 8 x 128 d (217 MB) 58 us, 3.7 TB/s.  (Pages in the order of
+// their heads: 63; stores around the L2: 59.)
 // LDS: a key page [token][D], a value page [d][token] with rows of P + 4
 // bytes (the writes of neighbouring d then fall on different banks).
 template <int T, int D, int NT>
@@ -266,9 +271,9 @@ static void go_append(const AppendArgs& a, hipStream_t s) {
                    (a.k_t | a.k_h | a.v_t | a.v_h) % per16 == 0;
   // A few tokens leave most of a page as it is, and only a scale that grew makes
   // the small kernel touch it (us, small / page kernel, 32 x 8 heads x 128 d,
-  // pages of 64: 1 token 5.2 / 12.0, 8 tokens 9.0 / 12.8, 25 tokens 19.6 / 14.6;
-  // 32 x 16 x 64, pages of 32: 5.5 / 7.8, 7.2 / 9.0, 10.8 / 9.0).
-  if (!vec || a.c.max_new <= 12) {
+  // pages of 64: 1 token 5.2 / 7.8, 8 tokens 9.1 / 9.0, 25 tokens 19.6 / 9.5;
+  // 32 x 16 x 64, pages of 32: 5.5 / 7.0, 7.2 / 8.1, 10.7 / 8.2).
+  if (!vec || a.c.max_new <= 8) {
     append_kernel<T><<<grid, 256, 0, s>>>(a);
     return;
   }
