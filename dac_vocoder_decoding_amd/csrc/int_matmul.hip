@@ -13,22 +13,69 @@
 
 namespace voc {
 
-// 16 bytes of a row of K codes at k, zero past the row's end; any alignment.
-__device__ __forceinline__ i32x4 load_codes(const int8_t* row, int k, int K) {
-  i32x4 v = {0, 0, 0, 0};
-  if (k + 16 <= K) {
-    __builtin_memcpy(&v, row + k, 16);
-  } else if (k < K) {
-    int8_t t[16];
+// Rows of any alignment can be read in the aligned 32-bit words that hold
+// their bytes (each of them has a byte of the row, so none lies outside the
+// caller's pages) and shifted into place.  That pays where the loads are all
+// there is, for few tokens (us, as they lie / shifted: 105 x 1527 x 3563 28.0 /
+// 16.3, 64 x 7680 x 1709 25.3 / 14.8); where they wait for LDS tiles it does
+// not (6011 x 869 x 2789 54 / 64).
+__device__ __forceinline__ i32x4 shifted(const uint32_t (&w)[5], uint32_t sh) {
+  i32x4 v;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) t[i] = k + i < K ? row[k + i] : int8_t(0);
-    __builtin_memcpy(&v, t, 16);
-  }
+  for (int i = 0; i < 4; ++i) v[i] = static_cast<int>(__builtin_amdgcn_alignbyte(w[i + 1], w[i], sh));
   return v;
 }
 
+// 16 codes at p.
+template <bool SHIFT>
+__device__ __forceinline__ i32x4 load_whole(const int8_t* p) {
+  i32x4 v;
+  if constexpr (!SHIFT) {
+    __builtin_memcpy(&v, p, 16);
+    return v;
+  }
+  const uint32_t sh = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 3;
+  const uint32_t* q = reinterpret_cast<const uint32_t*>(p - sh);
+  uint32_t w[5];
+  __builtin_memcpy(w, q, 16);
+  w[4] = q[sh ? 4 : 3];
+  return shifted(w, sh);
+}
+
+// 16 codes of a row of K at k, zero past the row's end.
+template <bool SHIFT>
+__device__ __forceinline__ i32x4 load_codes(const int8_t* row, int k, int K) {
+  const int8_t* p = row + k;
+  const int n = K - k;
+  if (!SHIFT && n >= 16) return load_whole<false>(p);  // (one path for all lanes is faster where words are read)
+  const uint32_t sh = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 3;
+  const uint32_t* q = reinterpret_cast<const uint32_t*>(p - sh);
+  uint32_t w[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = n > 0 && 4 * i < n + static_cast<int>(sh) && (i < 4 || sh) ? q[i] : 0;
+  i32x4 v = shifted(w, sh);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n < 4 * i + 4) v[i] &= n <= 4 * i ? 0 : (1 << (8 * (n - 4 * i))) - 1;
+  return v;
+}
+
+// GELU: v (1 - erfc(z) / 2) for v >= 0, v erfc(z) / 2 below, z = |v| / sqrt(2),
+// with Hastings' form erfc(z) = exp(-z^2) t (c0 + c1 t + ...), t = 1 / (1 + 0.4 z).
+// The coefficients are a minimax fit over z in [0, 6] (error 2.8e-8); in fp32
+// the result is within 3.4 |v| 2^-24 of GELU.  (With erff 31.5 M outputs of
+// 4606 x 6848 x 576 take 76 us, with this 58, without GELU 47.)
 __device__ __forceinline__ float activate(float v, int act) {
-  return act ? 0.5f * v * (1.0f + erff(v * 0.70710678118654752f)) : v;
+  if (!act) return v;
+  const float z = fabsf(v) * 0.70710678f;
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.4f, z, 1.f));
+  float p = fmaf(-0.20027051f, t, 0.70919334f);
+  p = fmaf(p, t, -0.3709826f);
+  p = fmaf(p, t, 0.46833433f);
+  p = fmaf(p, t, 0.1617995f);
+  p = fmaf(p, t, 0.23192592f);
+  const float half = 0.5f * p * t * __builtin_amdgcn_exp2f(z * z * -1.44269504f);
+  return v * (v >= 0.f ? 1.f - half : half);
 }
 
 // Four consecutive features n .. n + 3 of token m (n a multiple of 4).
@@ -59,7 +106,7 @@ __device__ __forceinline__ void store4(const IntMatmulArgs& a, bool vec, int m, 
 // tokens, so LDS tiles would only add a wait; bound by the latency of the
 // loads (four steps of them in flight): 32 x 4096 x 1024, 4.2 MB of weights,
 // 4.9 us.
-template <int T, int MB>
+template <int T, int MB, bool SHIFT>
 __global__ __launch_bounds__(512) void int_matmul_few_kernel(const IntMatmulArgs a, int vec) {
   __shared__ i32x4 s_acc[8][MB][64];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -84,13 +131,13 @@ __global__ __launch_bounds__(512) void int_matmul_few_kernel(const IntMatmulArgs
       const int k = k0 + u * 64 + lg * 16;
       if (k0 + u * 64 >= k1) continue;
       if (k0 + u * 64 + 64 <= a.K) {
-        __builtin_memcpy(&w[u], brow + k, 16);
+        w[u] = load_whole<SHIFT>(brow + k);
 #pragma unroll
-        for (int j = 0; j < MB; ++j) __builtin_memcpy(&x[u][j], arow[j] + k, 16);
+        for (int j = 0; j < MB; ++j) x[u][j] = load_whole<SHIFT>(arow[j] + k);
       } else {
-        w[u] = load_codes(brow, k, a.K);
+        w[u] = load_codes<SHIFT>(brow, k, a.K);
 #pragma unroll
-        for (int j = 0; j < MB; ++j) x[u][j] = load_codes(arow[j], k, a.K);
+        for (int j = 0; j < MB; ++j) x[u][j] = load_codes<SHIFT>(arow[j], k, a.K);
       }
     }
 #pragma unroll
@@ -241,7 +288,7 @@ __global__ __launch_bounds__(WF * WT * 64) void int_matmul_tile_kernel(const Int
 #pragma unroll
     for (int p = 0; p < AHEAD; ++p)
 #pragma unroll
-      for (int u = 0; u < LW; ++u) g[p][u] = load_codes(row[u], p * kStageK + cunit, a.K);
+      for (int u = 0; u < LW; ++u) g[p][u] = load_codes<false>(row[u], p * kStageK + cunit, a.K);
     for (int c0 = 0; c0 < nstages; c0 += AHEAD) {
 #pragma unroll
       for (int p = 0; p < AHEAD; ++p) {
@@ -253,10 +300,10 @@ __global__ __launch_bounds__(WF * WT * 64) void int_matmul_tile_kernel(const Int
         __syncthreads();
         if ((c + AHEAD + 1) * kStageK <= a.K) {  // uniform: the whole stage lies inside the rows
 #pragma unroll
-          for (int u = 0; u < LW; ++u) __builtin_memcpy(&g[p][u], row[u] + (c + AHEAD) * kStageK + cunit, 16);
+          for (int u = 0; u < LW; ++u) g[p][u] = load_whole<false>(row[u] + (c + AHEAD) * kStageK + cunit);
         } else if (c + AHEAD < nstages) {
 #pragma unroll
-          for (int u = 0; u < LW; ++u) g[p][u] = load_codes(row[u], (c + AHEAD) * kStageK + cunit, a.K);
+          for (int u = 0; u < LW; ++u) g[p][u] = load_codes<false>(row[u], (c + AHEAD) * kStageK + cunit, a.K);
         }
         stage_mma(s);
       }
@@ -298,24 +345,49 @@ __global__ __launch_bounds__(WF * WT * 64) void int_matmul_tile_kernel(const Int
       }
     }
     // (The wave's own writes and reads of LDS stay in order.)
+    if (vec) {
 #pragma unroll
-    for (int q = 0; q < CT * 16 * RC / 64; ++q) {
-      const int p = q * 64 + lane, t = p / RC, c = p % RC;
-      const int m = mw + j0 * 16 + t, n = nw + c * (16 / ES);
-      const uint4 v = *reinterpret_cast<const uint4*>(part + t * RC * 16 + ((c ^ (t & 15 & (RC - 1))) << 4));
-      if (m < a.M && n < a.N) {
-        E* y = static_cast<E*>(a.y) + static_cast<int64_t>(m) * a.ldy + n;
-        if (vec && n + 16 / ES <= a.N) {
-          *reinterpret_cast<uint4*>(y) = v;
-        } else {
-          const E* e = reinterpret_cast<const E*>(&v);
+      for (int q = 0; q < CT * 16 * RC / 64; ++q) {
+        const int p = q * 64 + lane, t = p / RC, c = p % RC;
+        const int m = mw + j0 * 16 + t, n = nw + c * (16 / ES);
+        const uint4 v = *reinterpret_cast<const uint4*>(part + t * RC * 16 + ((c ^ (t & 15 & (RC - 1))) << 4));
+        if (m < a.M && n < a.N) {
+          E* y = static_cast<E*>(a.y) + static_cast<int64_t>(m) * a.ldy + n;
+          if (n + 16 / ES <= a.N) {
+            *reinterpret_cast<uint4*>(y) = v;
+          } else {
+            const E* e = reinterpret_cast<const E*>(&v);
 #pragma unroll
-          for (int k = 0; k < 16 / ES; ++k)
-            if (n + k < a.N) y[k] = e[k];
+            for (int k = 0; k < 16 / ES; ++k)
+              if (n + k < a.N) y[k] = e[k];
+          }
         }
+      }
+    } else {
+      // Rows of any alignment: a wave's stores cover consecutive features (16
+      // bytes a lane, stored value by value: 3693 x 4201 x 192 58 us for 26).
+      constexpr int NF = FF * 16;
+#pragma unroll 4
+      for (int q = 0; q < CT * 16 * NF / 64; ++q) {
+        const int p = q * 64 + lane, t = p / NF, f = p % NF;
+        const int m = mw + j0 * 16 + t, n = nw + f, byte = f * ES;
+        const E v = *reinterpret_cast<const E*>(part + t * RC * 16 + (((byte >> 4) ^ (t & (RC - 1) & 15)) << 4) + (byte & 15));
+        if (m < a.M && n < a.N) static_cast<E*>(a.y)[static_cast<int64_t>(m) * a.ldy + n] = v;
       }
     }
   }
+}
+
+template <int T, bool SHIFT>
+static void go_few(const IntMatmulArgs& a, hipStream_t s) {
+  const int vec = a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % (4 * elem_size(T)) == 0;
+  const unsigned gx = (a.N + 15) / 16;
+  if (a.M <= 16)
+    int_matmul_few_kernel<T, 1, SHIFT><<<dim3(gx), 512, 0, s>>>(a, vec);
+  else if (a.M <= 32 || a.M > 64)
+    int_matmul_few_kernel<T, 2, SHIFT><<<dim3(gx, (a.M + 31) / 32), 512, 0, s>>>(a, vec);
+  else
+    int_matmul_few_kernel<T, 4, SHIFT><<<dim3(gx), 512, 0, s>>>(a, vec);
 }
 
 template <int T, int BF, int BT, int WF, int WT, int NS, bool DMA>
@@ -344,14 +416,10 @@ static void go_int_matmul(const IntMatmulArgs& a, hipStream_t s) {
   const bool dma = a.K % 16 == 0 && a.lda % 16 == 0 && a.ldb % 16 == 0 && a.lda < (1 << 22) && a.ldb < (1 << 22) &&
                    (reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.b)) % 16 == 0;
   if (a.M <= 64 || tiles(64, 64) <= 64) {
-    const int vec = a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % (4 * elem_size(T)) == 0;
-    const unsigned gx = (a.N + 15) / 16;
-    if (a.M <= 16)
-      int_matmul_few_kernel<T, 1><<<dim3(gx), 512, 0, s>>>(a, vec);
-    else if (a.M <= 32 || a.M > 64)
-      int_matmul_few_kernel<T, 2><<<dim3(gx, (a.M + 31) / 32), 512, 0, s>>>(a, vec);
+    if ((reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.b) | a.lda | a.ldb) % 4 == 0)
+      go_few<T, false>(a, s);
     else
-      int_matmul_few_kernel<T, 4><<<dim3(gx), 512, 0, s>>>(a, vec);
+      go_few<T, true>(a, s);
   } else if (!dma) {
     go_tile<T, 64, 64, 4, 2, 2, false>(a, s);
   } else if (tiles(256, 256) >= 192) {
