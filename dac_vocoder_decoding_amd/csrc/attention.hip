@@ -364,8 +364,10 @@ __device__ __forceinline__ void read_ahead() {
   }
 }
 
-// Many query rows.  Workgroup: 8 waves (4 above 128 d and for fp32 queries)
-// of RT tiles of 16 rows.  Blocks of 64 keys and values are brought to LDS as
+// Many query rows.  Workgroup: 8 waves of RT tiles of 16 rows (one above 128 d
+// and for fp32 queries: four waves of two tiles keep a SIMD to one wave, us, as
+// chosen / that: 2 x 2000 x 16 heads of 256 d, bf16 118 / 207, of 128 d, fp32
+// 111 / 144; eight waves of two tiles spill there).  Blocks of 64 keys and values are brought to LDS as
 // fp16 once for all waves, two buffers in turn: while one is worked on, the
 // next block's codes are on their way into registers and are converted at
 // the end of the step.  Page numbers run two blocks ahead, scales one
@@ -385,15 +387,15 @@ __device__ __forceinline__ void read_ahead() {
 // then), two groups of waves a phase apart 523 to 677 (499), wave priorities
 // 553 to 581, the value scale inside the exponent 553 (550), 64 rows a wave
 // 1269 (spills).
-constexpr int many_waves(int t, int dc) { return t == EL_F32 || dc > 4 ? 4 : 8; }
-constexpr int many_rt(int t, int dc) { return t == EL_F32 && dc > 4 ? 1 : 2; }
+constexpr int kManyWaves = 8;
+constexpr int many_rt(int t, int dc) { return t == EL_F32 || dc > 4 ? 1 : 2; }
 
 template <int T, int DC>
-__global__ __launch_bounds__(64 * many_waves(T, DC)) void attend_many_kernel(const AttendArgs a, int tiles, int parts) {
+__global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(const AttendArgs a, int tiles, int parts) {
   typedef typename Elem<T>::type E;
   constexpr int D = DC * 32;
   constexpr int NT = T == EL_F32 ? 2 : 1;
-  constexpr int RT = many_rt(T, DC), NW = many_waves(T, DC), ROWS = NW * 16 * RT;
+  constexpr int RT = many_rt(T, DC), NW = kManyWaves, ROWS = NW * 16 * RT;
   constexpr int TILE = kBlockKeys * D * 2;                         // bytes of a key or value tile
   constexpr int CK = ((D + 63) / 64 + NW / 4 - 1) / (NW / 4);      // 16-code units of a key tile per thread
   constexpr int CV = (D / 16 + NW - 1) / NW;                       // and of a value tile
@@ -732,7 +734,7 @@ static void go_attend(const AttendArgs& a, hipStream_t s) {
   const int64_t seen = a.causal && !a.window ? keys - a.c.max_new / 2 : keys;
   const int64_t units = pairs * ((rows + 15) / 16) * ((seen + kBlockKeys - 1) / kBlockKeys);
   const bool many = rows > (DC <= 2 ? 128 : 80) && units >= (DC <= 2 ? 40000 : 16000);
-  const int tile_rows = many ? 16 * many_waves(T, DC) * many_rt(T, DC) : kFewRows;
+  const int tile_rows = many ? 16 * kManyWaves * many_rt(T, DC) : kFewRows;
   const int64_t tiles = (rows + tile_rows - 1) / tile_rows, wgs = pairs * tiles;
   // Parts of the keys where the rows alone do not fill the chip, each at
   // least one round of the workgroup's waves long, as the workspace allows: as
@@ -741,6 +743,10 @@ static void go_attend(const AttendArgs& a, hipStream_t s) {
   // of 2 x 256 74 / 49 / 55).
   const int64_t most = (keys + 255) / 256, room = static_cast<int64_t>(a.ws_bytes) / (tile_rows * (a.D + 2) * 4 * wgs);
   int64_t parts = 256 * (many ? 1 : few_waves(T, DC)) / wgs;
+  // Causal tiles differ in length: where each has a CU of its own, two parts
+  // let the short ones' CUs help (us, one / two: 136 tiles of 192 d 78 / 55, 160
+  // of 128 d 168 / 106, 256 of 192 d 78 / 67; not 324 of 128 d 233 / 245).
+  if (many && a.causal && !a.window && wgs <= 256 && parts < 2) parts = 2;
   parts = parts < kMaxParts ? parts : kMaxParts;
   parts = parts < most ? parts : most;
   parts = parts < room ? parts : room;
@@ -749,7 +755,7 @@ static void go_attend(const AttendArgs& a, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(wgs * parts));
   const int live = static_cast<int>(rows < tile_rows ? rows : tile_rows);
   if (many)
-    attend_many_kernel<T, DC><<<grid, 64 * many_waves(T, DC), 0, s>>>(a, nt, np);
+    attend_many_kernel<T, DC><<<grid, 64 * kManyWaves, 0, s>>>(a, nt, np);
   else
     attend_few_kernel<T, DC><<<grid, 256, 0, s>>>(a, nt, np);
   if (np > 1 && np <= 4 && live >= 16)

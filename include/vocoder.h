@@ -491,7 +491,7 @@ typedef struct voc_ops voc_ops;
 
 /* Create a handle on HIP device hip_device with its workspace (device
  * memory, VOC_OPS_WORKSPACE_BYTES).  *out receives the handle or NULL. */
-#define VOC_OPS_WORKSPACE_BYTES 33554432
+#define VOC_OPS_WORKSPACE_BYTES 134217728
 voc_status voc_ops_create(int hip_device, voc_ops **out);
 
 /* Message of the last error on ops ("" if none); with ops == NULL, of the
