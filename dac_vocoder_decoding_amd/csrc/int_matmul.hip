@@ -345,16 +345,19 @@ __global__ __launch_bounds__(WF * WT * 64) void int_matmul_tile_kernel(const Int
       }
     }
     // (The wave's own writes and reads of LDS stay in order.)
+    // Whole pieces are stored past the L2, which keeps its place for operands
+    // (us, through it / past it: 8000 x 8192 x 4096 277 / 257, 8000 x 4096 x 1024
+    // 59 / 52, 2000 x 8192 x 512 24.5 / 18.8).
     if (vec) {
 #pragma unroll
       for (int q = 0; q < CT * 16 * RC / 64; ++q) {
         const int p = q * 64 + lane, t = p / RC, c = p % RC;
         const int m = mw + j0 * 16 + t, n = nw + c * (16 / ES);
-        const uint4 v = *reinterpret_cast<const uint4*>(part + t * RC * 16 + ((c ^ (t & 15 & (RC - 1))) << 4));
+        const i32x4 v = *reinterpret_cast<const i32x4*>(part + t * RC * 16 + ((c ^ (t & 15 & (RC - 1))) << 4));
         if (m < a.M && n < a.N) {
           E* y = static_cast<E*>(a.y) + static_cast<int64_t>(m) * a.ldy + n;
           if (n + 16 / ES <= a.N) {
-            *reinterpret_cast<uint4*>(y) = v;
+            __builtin_nontemporal_store(v, reinterpret_cast<i32x4*>(y));
           } else {
             const E* e = reinterpret_cast<const E*>(&v);
 #pragma unroll
