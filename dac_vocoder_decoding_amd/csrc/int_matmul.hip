@@ -385,12 +385,16 @@ template <int T, bool SHIFT>
 static void go_few(const IntMatmulArgs& a, hipStream_t s) {
   const int vec = a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % (4 * elem_size(T)) == 0;
   const unsigned gx = (a.N + 15) / 16;
-  if (a.M <= 16)
-    int_matmul_few_kernel<T, 1, SHIFT><<<dim3(gx), 512, 0, s>>>(a, vec);
-  else if (a.M <= 32 || a.M > 64)
-    int_matmul_few_kernel<T, 2, SHIFT><<<dim3(gx, (a.M + 31) / 32), 512, 0, s>>>(a, vec);
+  auto rows = [&](int mb) { return static_cast<unsigned>((a.M + 16 * mb - 1) / (16 * mb)); };
+  // As many tokens a workgroup as leave about one to each CU (us, 64 x 1024 x
+  // 4096 with 4 / 2 / 1 blocks of 16: 11.3 / 7.7 / 7.3, 64 x 2048 x 4096 11.7 /
+  // 8.1, 64 x 3500 x 2048 7.3 / 8.4, 32 x 4096 x 1024 4.2 with 2, 4.6 with 1).
+  if (a.M > 32 && gx * rows(4) >= 192)
+    int_matmul_few_kernel<T, 4, SHIFT><<<dim3(gx, rows(4)), 512, 0, s>>>(a, vec);
+  else if (a.M > 16 && gx * rows(2) >= 192)
+    int_matmul_few_kernel<T, 2, SHIFT><<<dim3(gx, rows(2)), 512, 0, s>>>(a, vec);
   else
-    int_matmul_few_kernel<T, 4, SHIFT><<<dim3(gx), 512, 0, s>>>(a, vec);
+    int_matmul_few_kernel<T, 1, SHIFT><<<dim3(gx, rows(1)), 512, 0, s>>>(a, vec);
 }
 
 template <int T, int BF, int BT, int WF, int WT, int NS, bool DMA>
@@ -401,16 +405,19 @@ static void go_tile(const IntMatmulArgs& a, hipStream_t s) {
       <<<dim3(static_cast<unsigned>(tf) * tt), WF * WT * 64, 0, s>>>(a, tf, tt, vec);
 }
 
-// Which kernel (times on MI355X, us, rotating inputs):
-//  * up to 64 tokens, or so few 64x64 tiles that most of the chip would idle:
-//    the K-splitting kernel (128x1024x4096: 7.9 against 12.9 for tiles;
-//    64x4096x1024: 5.7 against 6.9);
+// Which kernel (us):
+//  * up to 16 tokens, or so few outputs that 64x64 tiles would leave most of the
+//    chip idle: the K-splitting kernel (K-splitting / tiles: 16x8192x4096 10.6 /
+//    12.0; 128x1024x4096, 2^17 outputs, 7.8 / 11.5; 192x1024x4096 13.2 / 11.5;
+//    64x8192x4096 21 / 12.3); for unaligned rows, which reach tiles through
+//    registers, to twice that (64x4096x4096 16.0 / 22.2);
 //  * the largest tile that still gives the 256 CUs enough workgroups:
-//    256x256 from 192 tiles (8000x4096x1024: 56 against 60 for 128x128;
-//    8000x1024x4096, 128 tiles: 59 against 39), 128x128 from 384 (two
-//    workgroups a CU), 128x64 from 384 (1000x4096x1024: 11.0 against 13.7
-//    and 14.2), else 64x64 (2000x1024x1024: 7.9 against 8.3) with eight
-//    waves (500x1024x4096: 11.9 against 12.4 with four);
+//    256x256 from 192 tiles (8000x8192x2048: 137 against 150 for 128x128;
+//    8000x1024x4096, 128 tiles: 50 against 33), 128x128 from 384 (two
+//    workgroups a CU; 2000x4096x1024 13.6 against 17.8), 128x64 from 384
+//    (1000x4096x1024: 9.6 against 11.5 and 12.9), else 64x64
+//    (500x1024x4096: 12.4 against 15.8) with eight waves (with four half a us
+//    more);
 //  * rows that are not 16-byte aligned go through registers in 64x64 tiles
 //    (689x1000x1501: 11.0; four waves 12.5, 128x64 17.4).
 template <int T>
@@ -418,7 +425,7 @@ static void go_int_matmul(const IntMatmulArgs& a, hipStream_t s) {
   auto tiles = [&](int f, int t) { return static_cast<int64_t>((a.N + f - 1) / f) * ((a.M + t - 1) / t); };
   const bool dma = a.K % 16 == 0 && a.lda % 16 == 0 && a.ldb % 16 == 0 && a.lda < (1 << 22) && a.ldb < (1 << 22) &&
                    (reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.b)) % 16 == 0;
-  if (a.M <= 64 || tiles(64, 64) <= 64) {
+  if (a.M <= 16 || static_cast<int64_t>(a.M) * a.N <= (dma ? 1 << 17 : 1 << 18)) {
     if ((reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.b) | a.lda | a.ldb) % 4 == 0)
       go_few<T, false>(a, s);
     else
