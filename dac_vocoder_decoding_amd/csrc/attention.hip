@@ -381,7 +381,7 @@ __device__ __forceinline__ void read_ahead() {
 // Two prompts of 5168, 32 / 8 heads x 128 d, causal (386 G operations): 467 us,
 // 0.83 P operations a second (548 in a profiled run); a large fp16 library
 // product reaches 1.32.  The matrix cores are busy 37 % of the cycles
-// and the vector units about 54 % (160 instructions for 1024 scores of a wave,
+// and the vector units about 54 % (155 instructions for 1024 scores of a wave,
 // conversion included): a SIMD's two waves seldom do the one while the other
 // does the other.  Not kept: scores a block ahead of the products 710 (630
 // then), two groups of waves a phase apart 523 to 677 (499), wave priorities

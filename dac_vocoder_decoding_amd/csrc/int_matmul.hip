@@ -168,8 +168,8 @@ __global__ __launch_bounds__(512) void int_matmul_few_kernel(const IntMatmulArgs
 // flight, out-of-range rows and codes read as zero (16-byte aligned rows, K
 // a multiple of 16).  Otherwise the rows go through registers, two stages
 // ahead, with their tails masked (any alignment).
-// Bound by the matrix cores: 8000 x 8192 x 4096 in 256 x 256 tiles takes 257 us
-// (2.1 P operations a second; 302 in a profiled run, the matrix cores busy 48 %
+// Bound by the matrix cores: 8000 x 8192 x 4096 in 256 x 256 tiles takes 230 us
+// (2.3 P operations a second; 280 in a profiled run, the matrix cores busy 55 %
 // of the cycles at 1.9 GHz; the library's product 244).  Four waves of
 // 128 x 128, one a SIMD, in place of eight: 414 to 460; 128 x 128 tiles with a
 // four-stage ring: 425.
@@ -346,8 +346,8 @@ __global__ __launch_bounds__(WF * WT * 64) void int_matmul_tile_kernel(const Int
     }
     // (The wave's own writes and reads of LDS stay in order.)
     // Whole pieces are stored past the L2, which keeps its place for operands
-    // (us, through it / past it: 8000 x 8192 x 4096 277 / 257, 8000 x 4096 x 1024
-    // 59 / 52, 2000 x 8192 x 512 24.5 / 18.8).
+    // (us, through it / past it: 8000 x 8192 x 4096 258 / 230, 8000 x 4096 x 1024
+    // 58 / 51, 2000 x 8192 x 512 24.5 / 18.8).
     if (vec) {
 #pragma unroll
       for (int q = 0; q < CT * 16 * RC / 64; ++q) {
