@@ -727,26 +727,34 @@ static void go_attend(const AttendArgs& a, hipStream_t s) {
   int64_t keys = a.max_total;
   if (a.window && keys > static_cast<int64_t>(a.window) + a.c.max_new) keys = static_cast<int64_t>(a.window) + a.c.max_new;
   // The kernel for many rows pays where its tiles are filled and the chip is:
-  // from about 80 rows (128 up to 64 d) a sequence and cache head, and enough
-  // units of 16 rows x 64 keys over all of them (us, few / many: 100 rows of
-  // 128 d, 20000 units 44 / 33; 256 rows, 16000 units 39 / 36; 100 rows, 2500
-  // units 21 / 25; 2000 rows of 64 d, 32000 units 44 / 51).
+  // from about 80 rows (128 up to 64 d) a sequence and cache head, with a tile
+  // for every CU (us, few / many: 32 prompts of 250 x 16 x 64 61 / 33, of 90 x
+  // 16 x 256 143 / 29) or enough units of 16 rows x 64 keys over all tiles
+  // (100 rows of 128 d, 20000 units 44 / 33; 256 rows, 16000 units 39 / 36; 100
+  // rows, 2500 units 21 / 25; 2000 rows of 64 d, 32000 units 44 / 51), which a
+  // window thins out where tiles are few (48 tiles, 1500 rows, window 700 25 /
+  // 49; 171 tiles, window 4 19 / 13).
   const int64_t seen = a.causal && !a.window ? keys - a.c.max_new / 2 : keys;
   const int64_t units = pairs * ((rows + 15) / 16) * ((seen + kBlockKeys - 1) / kBlockKeys);
-  const bool many = rows > (DC <= 2 ? 128 : 80) && units >= (DC <= 2 ? 40000 : 16000);
-  const int tile_rows = many ? 16 * kManyWaves * many_rt(T, DC) : kFewRows;
+  constexpr int kManyRows = 16 * kManyWaves * many_rt(T, DC);
+  const int64_t many_wgs = pairs * ((rows + kManyRows - 1) / kManyRows);
+  const bool sliding = a.causal && a.window;
+  const bool many = rows > (DC <= 2 ? 128 : 80) &&
+                    (many_wgs >= 256 || (units >= (DC <= 2 ? 40000 : 16000) && !(sliding && many_wgs < 128)));
+  const int tile_rows = many ? kManyRows : kFewRows;
   const int64_t tiles = (rows + tile_rows - 1) / tile_rows, wgs = pairs * tiles;
   // Parts of the keys where the rows alone do not fill the chip, each at
   // least one round of the workgroup's waves long, as the workspace allows: as
   // many workgroups as the chip holds (us, half as many / these / twice: 4 x
   // 65536 keys of 8 x 128 d 90 / 84 / 87, 32 x 2000 29 / 25 / 30, 16 x 16000
   // of 2 x 256 74 / 49 / 55).
-  const int64_t most = (keys + 255) / 256, room = static_cast<int64_t>(a.ws_bytes) / (tile_rows * (a.D + 2) * 4 * wgs);
+  const int64_t span = static_cast<int64_t>(a.window) + (tile_rows + a.group - 1) / a.group;  // of a sliding tile
+  const int64_t most = ((sliding && span < keys ? span : keys) + 255) / 256, room = static_cast<int64_t>(a.ws_bytes) / (tile_rows * (a.D + 2) * 4 * wgs);
   int64_t parts = 256 * (many ? 1 : few_waves(T, DC)) / wgs;
   // Causal tiles differ in length: where each has a CU of its own, two parts
   // let the short ones' CUs help (us, one / two: 136 tiles of 192 d 78 / 55, 160
   // of 128 d 168 / 106, 256 of 192 d 78 / 67; not 324 of 128 d 233 / 245).
-  if (many && a.causal && !a.window && wgs <= 256 && parts < 2) parts = 2;
+  if (many && a.causal && !a.window && wgs <= 256 && keys >= 1024 && parts < 2) parts = 2;
   parts = parts < kMaxParts ? parts : kMaxParts;
   parts = parts < most ? parts : most;
   parts = parts < room ? parts : room;

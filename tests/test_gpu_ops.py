@@ -845,3 +845,12 @@ def test_rms_norm_of_four_waves(ops, dtype, rows, C, pad, residual):
 @pytest.mark.parametrize("past,new", [([0, 60], [12, 5]), ([0, 60], [13, 6]), ([64, 127], [8, 12])])
 def test_append_of_a_few_tokens(ops, dtype, past, new):
     test_append_holds_the_tokens(ops, dtype, 64, 2, 96, past, new)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("P,D,past,new,causal,window", [
+    (16, 64, 0, 250, True, 0), (32, 256, 0, 90, True, 0), (64, 64, 3, 140, True, 72), (128, 96, 30, 100, False, 0)])
+def test_attention_many_short_prompts(ops, dtype, P, D, past, new, causal, window):
+    """A tile of rows to each of 16 heads of 16 sequences of different lengths, some without new tokens."""
+    test_attention(ops, dtype, P, 16, D, 1, [past * i for i in range(16)], [0 if i % 7 == 3 else new - 5 * i for i in range(16)],
+                   causal, window)
