@@ -38,12 +38,17 @@ __device__ __forceinline__ f16x8 codes_to_f16(uint32_t a, uint32_t b) {
   return u.v;
 }
 
-// The probabilities enter the matrix cores as p * (page scale / largest page
-// scale so far) * kLift with p = 2^(s - m).  m follows the row's maximum
-// only when that has moved past it by more than kSlack (a factor of 8), so
-// p reaches at most 2^kSlack; both keep the products inside fp16 and far
-// above its subnormals.
-constexpr float kLift = 4096.f, kSlack = 3.f;
+// The probabilities enter the matrix cores with their value scales, as
+// p * vs * lift with p = 2^(s - m) and lift a power of two that brings the
+// row's largest p * vs to [2^10, 2^11): what weighs most in the output then
+// uses all of an fp16 number, whatever the scales of pages that weigh little.
+// fp16 reaches 2^-25 below (half its last step), so a key's term is off by at
+// most 2^-35 of the row's largest besides its own rounding.  m follows a score
+// that passes it by more than kSlack (a factor of 8), lift a product past
+// kHigh, which fp16 still holds.  A product that high needs vs * lift past
+// kLook, so that a block of keys usually costs two comparisons (two prompts of
+// 5168, 32 / 8 heads x 128 d: 438 us; 457 with the product in the test).
+constexpr float kSlack = 3.f, kHigh = 32768.f, kLook = 4096.f;
 
 constexpr int kBlockKeys = 64;
 
@@ -114,9 +119,9 @@ __device__ __forceinline__ float load_query(const typename Elem<T>::type* qp, fl
 }
 
 // What a wave carries along for 16 query rows (a lane: row lr, the sum over
-// its own keys only).  vref is the largest page scale so far.
+// its own keys only).  ref is the largest p * vs when lift was last set.
 struct RowState {
-  float m = -INFINITY, l = 0.f, vref = 0.f, lift = 1.f;  // lift: kLift / vref
+  float m = -INFINITY, l = 0.f, ref = 0.f, lift = 1.f;
 };
 
 // Hides what a row does not see: this lane's keys key0 .. key0 + 15 count
@@ -136,35 +141,50 @@ __device__ __forceinline__ void hide(f32x4 (&st)[4], float& sc, float& vs, bool 
 }
 
 // Rescales what was summed when the scores of 16 more keys (this lane's, of
-// one page group: st times sc, value scale vs) make m or vref move.
+// one page group: st times sc, value scale vs) make m or lift move.  Returns
+// vs * lift.
 template <int NA>
-__device__ __forceinline__ void follow_maximum(const f32x4 (&st)[4], float sc, float vs, RowState& r, f32x4 (&acc)[NA]) {
+__device__ __forceinline__ float follow_maximum(const f32x4 (&st)[4], float sc, float vs, RowState& r, f32x4 (&acc)[NA]) {
   float top = st[0][0];
 #pragma unroll
   for (int j = 1; j < 16; ++j) top = fmaxf(top, st[j >> 2][j & 3]);
   top *= sc;
-  if (__any(top > r.m + kSlack || vs > r.vref)) {
-    float t = fmaxf(top, __shfl_xor(top, 16));
-    t = fmaxf(t, __shfl_xor(t, 32));
-    float v = fmaxf(vs, __shfl_xor(vs, 16));
-    v = fmaxf(v, __shfl_xor(v, 32));
-    const float m = t > r.m + kSlack ? t : r.m;
-    const float vref = fmaxf(r.vref, v);
-    const float alpha = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(r.m - m);
-    const float beta = vref > 0.f ? alpha * (r.vref / vref) : alpha;
-    r.m = m;
-    r.vref = vref;
-    r.lift = vref > 0.f ? kLift / vref : 1.f;
-    r.l *= alpha;
+  float vf = vs * r.lift;
+  if (__any(top > r.m + kSlack || vf > kLook)) {
+    // (Where m is -inf the first test decides: the second has an infinity or a
+    // NaN on its left.)
+    if (__any(top > r.m + kSlack || __builtin_amdgcn_exp2f(top - r.m) * vf > kHigh)) {
+      float t = fmaxf(top, __shfl_xor(top, 16));
+      t = fmaxf(t, __shfl_xor(t, 32));
+      const float m = t > r.m + kSlack ? t : r.m;
+      const float alpha = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(r.m - m);
+      float w = __builtin_amdgcn_exp2f(top - (m == -INFINITY ? 0.f : m)) * vs;
+      w = fmaxf(w, __shfl_xor(w, 16));
+      w = fmaxf(w, __shfl_xor(w, 32));
+      // At least 2^-112: lift and its inverse stay normal numbers.
+      const float ref = fmaxf(fmaxf(r.ref * alpha, w), 0x1p-112f);
+      const float lift = __uint_as_float((264u - (__float_as_uint(ref) >> 23)) << 23);
+      // alpha * lift / r.lift (their quotient alone may pass fp32's range).
+      const float beta = __builtin_amdgcn_ldexpf(
+          alpha, static_cast<int>(__float_as_uint(lift) >> 23) - static_cast<int>(__float_as_uint(r.lift) >> 23));
+      r.m = m;
+      r.ref = ref;
+      r.lift = lift;
+      r.l *= alpha;
 #pragma unroll
-    for (int i = 0; i < NA; ++i) acc[i] *= beta;
+      for (int i = 0; i < NA; ++i) acc[i] *= beta;
+    }
+    // Past 2^126 p is below 2^-111; an infinity would make NaN of p = 0.  (A
+    // NaN scale stays.)
+    vf = vs * r.lift;
+    vf = vf > 0x1p126f ? 0x1p126f : vf;
   }
+  return vf;
 }
 
 // The probabilities of those keys as operands of the second product.
 template <int NT>
-__device__ __forceinline__ void probabilities(const f32x4 (&st)[4], float sc, float vs, RowState& r, f16x8 (&pf)[NT][2]) {
-  const float vf = vs * r.lift;
+__device__ __forceinline__ void probabilities(const f32x4 (&st)[4], float sc, float vf, RowState& r, f16x8 (&pf)[NT][2]) {
   // A row that has seen nothing yet has only -inf here: any finite m will do.
   const float neg = r.m == -INFINITY ? 0.f : -r.m;
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -291,8 +311,8 @@ __global__ __launch_bounds__(256, few_waves(T, DC)) void attend_few_kernel(const
     f16x8 pf[NT][2];
     float sc = ks * cq, vsc = vs;
     if (!(kb >= full_lo && kb + kBlockKeys <= full_hi && __all(ok_v))) hide(st, sc, vsc, ok_v, gv, see);
-    follow_maximum(st, sc, vsc, rs, acc);
-    probabilities<NT>(st, sc, vsc, rs, pf);
+    const float vf = follow_maximum(st, sc, vsc, rs, acc);
+    probabilities<NT>(st, sc, vf, rs, pf);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       const f16x8 v0 = codes_to_f16(vc[i].x, vc[i].y), v1 = codes_to_f16(vc[i].z, vc[i].w);
@@ -571,7 +591,7 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(const Atte
         for (int r = 0; r < RT; ++r) hide(st[r], sc[r], vsc[r], in, kb + 16 * lg, see[r]);
       }
 #pragma unroll
-      for (int r = 0; r < RT; ++r) follow_maximum(st[r], sc[r], vsc[r], rs[r], acc[r]);
+      for (int r = 0; r < RT; ++r) vsc[r] = follow_maximum(st[r], sc[r], vsc[r], rs[r], acc[r]);
       f16x8 pf[RT][NT][2];
 #pragma unroll
       for (int r = 0; r < RT; ++r) probabilities<NT>(st[r], sc[r], vsc[r], rs[r], pf[r]);

@@ -617,7 +617,9 @@ voc_status vocoder_cache_append(voc_ops *ops, const voc_kv_cache *cache, const v
  * queries enter exactly (each row scaled by a power of two; what lies 2^24
  * below a row's largest value may round), the probabilities in fp16; fp32
  * queries and probabilities as two fp16 terms each, which hold about 22
- * bits.  Scores, softmax statistics and sums are fp32.
+ * bits.  A probability enters with its page's value scale; what lies below
+ * 2^-35 of the row's largest such product rounds away, whatever the scales
+ * of the pages.  Scores, softmax statistics and sums are fp32.
  * Results do not depend on what else runs; long caches are split over
  * workgroups and the parts joined in a fixed order.
  * q and o need 16-byte alignment and strides of 16-byte multiples.

@@ -854,3 +854,63 @@ def test_attention_many_short_prompts(ops, dtype, P, D, past, new, causal, windo
     """A tile of rows to each of 16 heads of 16 sequences of different lengths, some without new tokens."""
     test_attention(ops, dtype, P, 16, D, 1, [past * i for i in range(16)], [0 if i % 7 == 3 else new - 5 * i for i in range(16)],
                    causal, window)
+
+
+def attend64_by_keys(cache, table, past, new, q, scale, causal, window):
+    """Plain attention in 64 bits, with the bound of attend64 taken key by key
+    (an error e of a probability p moves the output by at most p e (|v| + |o|))
+    and fp16's last step as the kernels state it: 2^-35 of the row's largest
+    p times value scale for each key, times its code."""
+    Hq, H, D = q.shape[1], cache.kv_heads, q.shape[2]
+    outs, tols, base = [], [], 0
+    for b in range(len(past)):
+        total = past[b] + new[b]
+        rows = q[base:base + new[b]].double().transpose(0, 1)                # [Hq, n, D]
+        base += new[b]
+        if not new[b]:
+            continue
+        k = values_of(cache, table, b, total, "k").repeat_interleave(Hq // H, 0).transpose(1, 2).contiguous()
+        v = values_of(cache, table, b, total, "v").repeat_interleave(Hq // H, 0)
+        vs = page_scales(cache, table, b, total, "v").repeat_interleave(Hq // H, 0)[:, None]
+        at = past[b] + torch.arange(new[b], device="cuda")[:, None]
+        j = torch.arange(total, device="cuda")[None]
+        seen = torch.ones(new[b], total, dtype=torch.bool, device="cuda")
+        if causal:
+            seen &= j <= at
+        if window:
+            seen &= j > at - window
+        p = torch.softmax(((rows @ k) * scale).masked_fill(~seen, -math.inf), -1)
+        two = q.dtype == F32
+        e = (D + 8 + 4) * E * abs(scale) * (rows.abs() @ k.abs()) + 2.0 ** -21 + (2.0 ** -21 if two else 2.0 ** -11) \
+            + (total / 64 + 32) * E
+        o = p @ v
+        outs.append(o.transpose(0, 1))
+        tols.append(((p * e) @ v.abs() + (p * e).sum(-1, keepdim=True) * o.abs() + U[q.dtype] * o.abs() + SUB[q.dtype]
+                     + total * 2.0 ** -35 * 127 * (p * vs).amax(-1, keepdim=True)).transpose(0, 1))
+    return torch.cat(outs), torch.cat(tols)
+
+
+@pytest.mark.parametrize("dtype,ratio,push", [(F32, 20, 1.2), (F32, 40, 2.0), (F32, 70, 3.6), (F16, 20, 1.2),
+                                              (BF16, 20, 1.2), (BF16, 70, 3.6)])
+@pytest.mark.parametrize("P,H,D,past,new", [
+    (16, 2, 64, [200, 90], [1, 5]),                             # few rows
+    (16, 16, 64, [3 * i for i in range(16)], [250] * 16),       # many rows
+    (32, 16, 128, [0] * 17, [130] * 17)])
+def test_attention_value_scales_far_apart(ops, dtype, P, H, D, past, new, ratio, push):
+    """Pages whose value scales are 2^20, 2^40 and 2^70 times the others' and
+    whose keys the queries point away from (probabilities of about 2^-25,
+    2^-42 and 2^-75): they count for what they weigh, and no more."""
+    g = gen(91 + ratio)
+    cache, table = filled(g, P, H, D, past, new)
+    cache.v_scale.copy_(torch.rand(cache.v_scale.shape, generator=g, device="cuda") * 0.01 + 0.01)
+    cache.k_scale.fill_(1 / 70)
+    far = torch.stack([table[:, 0], table[:, 3]], 1).long()
+    cache.k[far] = -127
+    cache.v_scale[far] *= 2.0 ** ratio
+    if dtype == F16:
+        cache.v_scale.mul_(2.0 ** -6)               # 0.02 * 2^20 * 127 fits fp16 then
+    q = (randn(g, sum(new), H, D, std=0.3) + push * (64 / D) ** 0.5).to(dtype)
+    o = V.cache_attention(ops, cache, batch_of(table, past, new), q)
+    ref, tol = attend64_by_keys(cache, table, past, new, q, D ** -0.5, True, 0)
+    worst = ((o.double() - ref).abs() / tol).max().item()
+    assert worst <= 1, worst
