@@ -124,6 +124,13 @@ struct RowState {
   float m = -INFINITY, l = 0.f, ref = 0.f, lift = 1.f;
 };
 
+// Scores stay products st * sc up to the exponential, which takes their exact
+// difference from m, a rounded one: 2^-25 of a score, which is small beside
+// kSlack up to scores of 2^20 (of 2^30 it makes zeros and infinities).  The
+// sums are below 2^22 D, so that a block whose factors pass this limit goes
+// through hide(), which rounds them.
+__device__ __forceinline__ bool small_scores(float sc, int D) { return sc <= 0x1p-2f / static_cast<float>(D); }
+
 // Hides what a row does not see: this lane's keys key0 .. key0 + 15 count
 // where `in` and inside the row's sight.  Scores become final (their factor
 // sc 1) with -inf in hidden places, and the scale of values of which the row
@@ -310,7 +317,7 @@ __global__ __launch_bounds__(256, few_waves(T, DC)) void attend_few_kernel(const
     }
     f16x8 pf[NT][2];
     float sc = ks * cq, vsc = vs;
-    if (!(kb >= full_lo && kb + kBlockKeys <= full_hi && __all(ok_v))) hide(st, sc, vsc, ok_v, gv, see);
+    if (!(kb >= full_lo && kb + kBlockKeys <= full_hi && __all(ok_v && small_scores(sc, D)))) hide(st, sc, vsc, ok_v, gv, see);
     const float vf = follow_maximum(st, sc, vsc, rs, acc);
     probabilities<NT>(st, sc, vf, rs, pf);
 #pragma unroll
@@ -581,12 +588,14 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(const Atte
       const bool in = s_koff[n & 3][lg] >= 0;
       const float ks = s_ks[n & 3][lg], vs = s_vs[n & 3][lg];
       float sc[RT], vsc[RT];
+      bool plain = in;
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         sc[r] = ks * cq[r];
         vsc[r] = vs;
+        plain = plain && small_scores(sc[r], D);
       }
-      if (!(kb >= last.lo && kb + kBlockKeys <= first.hi && __all(in))) {
+      if (!(kb >= last.lo && kb + kBlockKeys <= first.hi && __all(plain))) {
 #pragma unroll
         for (int r = 0; r < RT; ++r) hide(st[r], sc[r], vsc[r], in, kb + 16 * lg, see[r]);
       }

@@ -914,3 +914,28 @@ def test_attention_value_scales_far_apart(ops, dtype, P, H, D, past, new, ratio,
     ref, tol = attend64_by_keys(cache, table, past, new, q, D ** -0.5, True, 0)
     worst = ((o.double() - ref).abs() / tol).max().item()
     assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("P,H,D,past,new,causal", [
+    (16, 2, 64, [300], [6], True), (64, 1, 128, [200, 64], [3, 20], False),         # few rows
+    (16, 16, 64, [300] * 16, [250] * 16, True), (32, 16, 192, [64] * 17, [130] * 17, False)])
+def test_attention_of_very_large_scores(ops, dtype, P, H, D, past, new, causal):
+    """Scores from thousands to 1e30: the key that the queries point at, 127 of
+    their signs everywhere, stands out by a factor of several, so that the
+    output is its value, rounded once."""
+    g = gen(92)
+    cache, table = filled(g, P, H, D, past, new)
+    sign = torch.randint(0, 2, (D,), generator=g, device="cuda") * 2 - 1
+    # One key scale (a larger page scale could lift another key past this one).
+    cache.k_scale.fill_(0.0123)
+    first = table[:, 0].long()
+    cache.k[first, :, 2] = (127 * sign).to(torch.int8)
+    n = sum(new)
+    gain = torch.exp(torch.linspace(math.log(1e4), math.log(1e30), n, device="cuda"))[:, None, None]
+    q = (sign * gain).expand(n, H, D).to(dtype).contiguous()
+    o = V.cache_attention(ops, cache, batch_of(table, past, new), q)
+    seq = torch.repeat_interleave(torch.arange(len(new), device="cuda"), torch.tensor(new, device="cuda"))
+    want = (cache.v[first, :, :, 2].double() * cache.v_scale[first].double()[..., None])[seq]
+    # (The second term: other keys' probabilities, below 2^-1000, and the two roundings of p times scale.)
+    assert ((o.double() - want).abs() <= (U[dtype] + 2.0 ** -20 + (0 if dtype == F32 else 2.0 ** -11)) * want.abs()).all()
