@@ -189,9 +189,17 @@ __device__ __forceinline__ float follow_maximum(const f32x4 (&st)[4], float sc, 
   return vf;
 }
 
-// The probabilities of those keys as operands of the second product.
-template <int NT>
-__device__ __forceinline__ void probabilities(const f32x4 (&st)[4], float sc, float vf, RowState& r, f16x8 (&pf)[NT][2]) {
+// The probabilities of those keys as operands of the second product, in NP fp16
+// terms.  Two hold about 22 bits; one rounds each to 11, which against 64 bits
+// costs (RMS of the output's, one term / two / the output's own rounding alone)
+// fp16 2.85e-4 / 2.07e-4 / 2.07e-4, bf16 1.67e-3 / 1.67e-3 / 1.66e-3.  Hence two
+// for fp32, one for bf16, and for fp16 two where rows are few and the second is
+// nearly free (us, one / two: 4 x 65536 keys of 8 x 128 d 89.1 / 90.0, 32 x 2000
+// 30.5 / 30.7, 32 x 25 rows of window 72 9.8 / 9.9), one where they are many (2
+// prompts of 5168 440 / 567, 32 of 250 x 16 x 64 30.4 / 33.9, 2 x 2000 x 16 x 256
+// 112 / 132).
+template <int NP>
+__device__ __forceinline__ void probabilities(const f32x4 (&st)[4], float sc, float vf, RowState& r, f16x8 (&pf)[NP][2]) {
   // A row that has seen nothing yet has only -inf here: any finite m will do.
   const float neg = r.m == -INFINITY ? 0.f : -r.m;
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -204,10 +212,10 @@ __device__ __forceinline__ void probabilities(const f32x4 (&st)[4], float sc, fl
     // take the first from the exact one (a fused multiply and conversion) for
     // one of its two uses, and near a tie the second term would belong to
     // another first one (seen: 2^-10 of a probability).
-    if constexpr (NT > 1) asm volatile("" : "+v"(w));
+    if constexpr (NP > 1) asm volatile("" : "+v"(w));
     const _Float16 hi = static_cast<_Float16>(w);
     pf[0][j >> 3][j & 7] = hi;
-    if constexpr (NT > 1) pf[1][j >> 3][j & 7] = static_cast<_Float16>(w - static_cast<float>(hi));
+    if constexpr (NP > 1) pf[1][j >> 3][j & 7] = static_cast<_Float16>(w - static_cast<float>(hi));
   }
   r.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
@@ -232,6 +240,7 @@ __global__ __launch_bounds__(256, few_waves(T, DC)) void attend_few_kernel(const
   typedef typename Elem<T>::type E;
   constexpr int D = DC * 32, NC = DC / 2, REM = DC & 1;
   constexpr int NT = T == EL_F32 ? 2 : 1;
+  constexpr int NP = T == EL_BF16 ? 1 : 2;
   constexpr int PITCH = D + 4;
   __shared__ float s_o[kFewRows * PITCH];
   __shared__ float s_m[4][kFewRows], s_l[4][kFewRows];
@@ -315,16 +324,16 @@ __global__ __launch_bounds__(256, few_waves(T, DC)) void attend_few_kernel(const
         for (int n = 0; n < NT; ++n) st[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[n][2 * NC], st[t], 0, 0, 0);
       }
     }
-    f16x8 pf[NT][2];
+    f16x8 pf[NP][2];
     float sc = ks * cq, vsc = vs;
     if (!(kb >= full_lo && kb + kBlockKeys <= full_hi && __all(ok_v && small_scores(sc, D)))) hide(st, sc, vsc, ok_v, gv, see);
     const float vf = follow_maximum(st, sc, vsc, rs, acc);
-    probabilities<NT>(st, sc, vf, rs, pf);
+    probabilities<NP>(st, sc, vf, rs, pf);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       const f16x8 v0 = codes_to_f16(vc[i].x, vc[i].y), v1 = codes_to_f16(vc[i].z, vc[i].w);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int n = 0; n < NP; ++n) {
         acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[n][0], acc[i], 0, 0, 0);
         acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[n][1], acc[i], 0, 0, 0);
       }
@@ -421,7 +430,7 @@ template <int T, int DC>
 __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(const AttendArgs a, int tiles, int parts) {
   typedef typename Elem<T>::type E;
   constexpr int D = DC * 32;
-  constexpr int NT = T == EL_F32 ? 2 : 1;
+  constexpr int NT = T == EL_F32 ? 2 : 1, NP = NT;
   constexpr int RT = many_rt(T, DC), NW = kManyWaves, ROWS = NW * 16 * RT;
   constexpr int TILE = kBlockKeys * D * 2;                         // bytes of a key or value tile
   constexpr int CK = ((D + 63) / 64 + NW / 4 - 1) / (NW / 4);      // 16-code units of a key tile per thread
@@ -601,9 +610,9 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(const Atte
       }
 #pragma unroll
       for (int r = 0; r < RT; ++r) vsc[r] = follow_maximum(st[r], sc[r], vsc[r], rs[r], acc[r]);
-      f16x8 pf[RT][NT][2];
+      f16x8 pf[RT][NP][2];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) probabilities<NT>(st[r], sc[r], vsc[r], rs[r], pf[r]);
+      for (int r = 0; r < RT; ++r) probabilities<NP>(st[r], sc[r], vsc[r], rs[r], pf[r]);
       const unsigned char* vt = s_v + (n & 1) * TILE + lane * 16;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -613,9 +622,9 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(const Atte
 #pragma unroll
           for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int x = 0; x < NT; ++x) acc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pf[r][x][h], acc[r][i], 0, 0, 0);
+            for (int x = 0; x < NP; ++x) acc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pf[r][x][h], acc[r][i], 0, 0, 0);
         }
-      read_ahead<D / 8, 4, RT * NT>();
+      read_ahead<D / 8, 4, RT * NP>();
     }
     if (n + 1 < nblk) {
       store_k(n + 1);

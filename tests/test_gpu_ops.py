@@ -856,7 +856,7 @@ def test_attention_many_short_prompts(ops, dtype, P, D, past, new, causal, windo
                    causal, window)
 
 
-def attend64_by_keys(cache, table, past, new, q, scale, causal, window):
+def attend64_by_keys(cache, table, past, new, q, scale, causal, window, two=None):
     """Plain attention in 64 bits, with the bound of attend64 taken key by key
     (an error e of a probability p moves the output by at most p e (|v| + |o|))
     and fp16's last step as the kernels state it: 2^-35 of the row's largest
@@ -880,7 +880,7 @@ def attend64_by_keys(cache, table, past, new, q, scale, causal, window):
         if window:
             seen &= j > at - window
         p = torch.softmax(((rows @ k) * scale).masked_fill(~seen, -math.inf), -1)
-        two = q.dtype == F32
+        two = q.dtype == F32 if two is None else two
         e = (D + 8 + 4) * E * abs(scale) * (rows.abs() @ k.abs()) + 2.0 ** -21 + (2.0 ** -21 if two else 2.0 ** -11) \
             + (total / 64 + 32) * E
         o = p @ v
@@ -939,3 +939,19 @@ def test_attention_of_very_large_scores(ops, dtype, P, H, D, past, new, causal):
     want = (cache.v[first, :, :, 2].double() * cache.v_scale[first].double()[..., None])[seq]
     # (The second term: other keys' probabilities, below 2^-1000, and the two roundings of p times scale.)
     assert ((o.double() - want).abs() <= (U[dtype] + 2.0 ** -20 + (0 if dtype == F32 else 2.0 ** -11)) * want.abs()).all()
+
+
+@pytest.mark.parametrize("P,H,D,group,past,new,causal,window", [
+    (32, 16, 64, 1, [250, 171, 33], [1, 1, 1], True, 0), (16, 4, 64, 1, [689, 500], [25, 19], True, 72),
+    (64, 2, 128, 4, [8000, 900], [1, 1], True, 0), (16, 1, 96, 4, [100], [20], False, 0),
+    (32, 2, 256, 1, [60], [80], True, 0)])
+def test_attention_fp16_of_few_rows_is_rounded_once(ops, P, H, D, group, past, new, causal, window):
+    """Up to 80 query rows a cache head: the probabilities of fp16 queries hold
+    two fp16 terms, so that the output's own rounding is nearly all of the error."""
+    g = gen(93 + D)
+    cache, table = filled(g, P, H, D, past, new)
+    q = randn(g, sum(new), H * group, D, dtype=F16)
+    o = V.cache_attention(ops, cache, batch_of(table, past, new), q, causal=causal, window=window)
+    ref, tol = attend64_by_keys(cache, table, past, new, q, D ** -0.5, causal, window, two=True)
+    worst = ((o.double() - ref).abs() / tol).max().item()
+    assert worst <= 1, worst
