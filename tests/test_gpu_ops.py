@@ -955,3 +955,23 @@ def test_attention_fp16_of_few_rows_is_rounded_once(ops, P, H, D, group, past, n
     ref, tol = attend64_by_keys(cache, table, past, new, q, D ** -0.5, causal, window, two=True)
     worst = ((o.double() - ref).abs() / tol).max().item()
     assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("M,N,K", [(15000, 8, 1), (40000, 8, 1), (40000, 8, 16)])
+@pytest.mark.parametrize("spread", [0.01, 0.1, 0.5, 1.0, 2.0, 4.0])
+def test_matmul_int_gelu_of_fp32(ops, M, N, K, spread):
+    """GELU itself: one code of 1 and the inputs as the row's scale make the
+    product exact.  0.5 x (1 + erf) in fp32 is within 1.8 units of |x| 2^-24;
+    so is the kernels' form with an exact reciprocal and exponential, and a
+    unit more in each of these, where erfc is at most 0.16, adds 0.4."""
+    g = gen(95)
+    a = torch.zeros(M, K, dtype=torch.int8, device="cuda")
+    a[:, 0] = 1
+    x = randn(g, M, std=spread)
+    y = V.matmul_int(ops, a, x, a[:N].contiguous(), torch.ones(N, device="cuda"), gelu=True, dtype=F32)
+    x = x.double()[:, None]
+    err = (y.double() - 0.5 * x * torch.special.erfc(-x / math.sqrt(2))).abs()
+    worst = (err / x.abs()).max().item() * 2 ** 24
+    assert worst <= 2.2, worst
+    # RMS: 0.5 x (1 + erf) has 3.8e-8 at a spread of 0.1 and less above 1.
+    assert err.norm() <= 4.2e-8 * (N ** 0.5) * gelu64(x).norm()
