@@ -359,7 +359,7 @@ __global__ __launch_bounds__(WF * WT * 64) void int_matmul_tile_kernel(const Int
         __builtin_memcpy(__builtin_assume_aligned(pr + (((byte >> 4) ^ (lr & (RC - 1))) << 4) + (byte & 15), 4 * ES), e, 4 * ES);
       }
     }
-    // (The wave's own writes and reads of LDS stay in order.)
+    wave_lds_sync();
     // Whole pieces are stored past the L2, which keeps its place for operands
     // (us, through it / past it: 8000 x 8192 x 4096 258 / 230, 8000 x 4096 x 1024
     // 58 / 51, 2000 x 8192 x 512 24.5 / 18.8).
@@ -393,6 +393,7 @@ __global__ __launch_bounds__(WF * WT * 64) void int_matmul_tile_kernel(const Int
         if (m < a.M && n < a.N) static_cast<E*>(a.y)[static_cast<int64_t>(m) * a.ldy + n] = v;
       }
     }
+    if (j0 + CT < FT) wave_lds_sync();
   }
 }
 

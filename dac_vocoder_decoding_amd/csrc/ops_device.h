@@ -78,4 +78,14 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
+// Orders a wave's LDS accesses before this point against those after it, for
+// exchanges between its own lanes: the hardware keeps a wave's LDS accesses in
+// order, and the compiler, which sees one lane's addresses only, may not move
+// them across.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 }  // namespace voc
