@@ -760,7 +760,7 @@ __global__ __launch_bounds__(256) void join_many_kernel(const AttendArgs a, int 
 }
 
 template <int T, int DC>
-static void go_attend(const AttendArgs& a, hipStream_t s) {
+static void go_attend(const AttendArgs& a, hipStream_t s, Form& form) {
   const int64_t rows = static_cast<int64_t>(a.c.max_new) * a.group, pairs = static_cast<int64_t>(a.batch) * a.c.heads;
   int64_t keys = a.max_total;
   if (a.window && keys > static_cast<int64_t>(a.window) + a.c.max_new) keys = static_cast<int64_t>(a.window) + a.c.max_new;
@@ -800,6 +800,7 @@ static void go_attend(const AttendArgs& a, hipStream_t s) {
   const int nt = static_cast<int>(tiles), np = static_cast<int>(parts);
   const dim3 grid(static_cast<unsigned>(wgs * parts));
   const int live = static_cast<int>(rows < tile_rows ? rows : tile_rows);
+  form = Form{many ? "attend_many" : "attend_few", {tile_rows, np}};
   if (many)
     attend_many_kernel<T, DC><<<grid, 64 * kManyWaves, 0, s>>>(a, nt, np);
   else
@@ -811,26 +812,26 @@ static void go_attend(const AttendArgs& a, hipStream_t s) {
 }
 
 template <int T>
-static void go_dim(const AttendArgs& a, hipStream_t s) {
+static void go_dim(const AttendArgs& a, hipStream_t s, Form& form) {
   switch (a.D / 32) {
-    case 1: go_attend<T, 1>(a, s); break;
-    case 2: go_attend<T, 2>(a, s); break;
-    case 3: go_attend<T, 3>(a, s); break;
-    case 4: go_attend<T, 4>(a, s); break;
-    case 5: go_attend<T, 5>(a, s); break;
-    case 6: go_attend<T, 6>(a, s); break;
-    case 7: go_attend<T, 7>(a, s); break;
-    default: go_attend<T, 8>(a, s); break;
+    case 1: go_attend<T, 1>(a, s, form); break;
+    case 2: go_attend<T, 2>(a, s, form); break;
+    case 3: go_attend<T, 3>(a, s, form); break;
+    case 4: go_attend<T, 4>(a, s, form); break;
+    case 5: go_attend<T, 5>(a, s, form); break;
+    case 6: go_attend<T, 6>(a, s, form); break;
+    case 7: go_attend<T, 7>(a, s, form); break;
+    default: go_attend<T, 8>(a, s, form); break;
   }
 }
 
-hipError_t launch_attend(int dtype, const AttendArgs& a, hipStream_t s) {
+hipError_t launch_attend(int dtype, const AttendArgs& a, hipStream_t s, Form& form) {
   if (dtype == EL_F32)
-    go_dim<EL_F32>(a, s);
+    go_dim<EL_F32>(a, s, form);
   else if (dtype == EL_BF16)
-    go_dim<EL_BF16>(a, s);
+    go_dim<EL_BF16>(a, s, form);
   else
-    go_dim<EL_F16>(a, s);
+    go_dim<EL_F16>(a, s, form);
   return hipGetLastError();
 }
 

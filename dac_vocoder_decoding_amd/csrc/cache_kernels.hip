@@ -245,25 +245,28 @@ __global__ __launch_bounds__(NT) void append_page_kernel(const AppendArgs a) {
 // 51.4 / 35.8; 2 prompts x 4 x 256, pages of 128: 44.0 / 27.0; 32 chunks of 25
 // x 16 x 64, pages of 32: 10.1, one wave 15.4).
 template <int T, int D>
-static void go_pages(const AppendArgs& a, dim3 grid, hipStream_t s) {
+static void go_pages(const AppendArgs& a, dim3 grid, hipStream_t s, Form& form) {
   const int P = 1 << a.c.page_log, units = P / 4 * (D / 8);
   const size_t lds = static_cast<size_t>(D) * (P + 4);
   const bool full = static_cast<int64_t>(grid.x) * grid.y * grid.z >= 4096;
   if constexpr (D <= 128)  // (larger heads have no page of 64 units, heads of 32 none of more than 128)
     if (units <= 64 && full) {
+      form = Form{"append_page", {64, P}};
       append_page_kernel<T, D, 64><<<grid, 64, lds, s>>>(a);
       return;
     }
   if constexpr (D > 32)
     if (units > 128) {
+      form = Form{"append_page", {256, P}};
       append_page_kernel<T, D, 256><<<grid, 256, lds, s>>>(a);
       return;
     }
+  form = Form{"append_page", {128, P}};
   append_page_kernel<T, D, 128><<<grid, 128, lds, s>>>(a);
 }
 
 template <int T>
-static void go_append(const AppendArgs& a, hipStream_t s) {
+static void go_append(const AppendArgs& a, hipStream_t s, Form& form) {
   const int P = 1 << a.c.page_log;
   const dim3 grid((a.c.max_new + P - 1) / P + 1, 2 * a.c.heads, a.batch);
   constexpr int per16 = 16 / sizeof(typename Elem<T>::type);
@@ -274,28 +277,29 @@ static void go_append(const AppendArgs& a, hipStream_t s) {
   // pages of 64: 1 token 5.2 / 7.8, 8 tokens 9.1 / 9.0, 25 tokens 19.6 / 9.5;
   // 32 x 16 x 64, pages of 32: 5.5 / 7.0, 7.2 / 8.1, 10.7 / 8.2).
   if (!vec || a.c.max_new <= 8) {
+    form = Form{"append", {256, P}};
     append_kernel<T><<<grid, 256, 0, s>>>(a);
     return;
   }
   switch (a.D / 32) {
-    case 1: go_pages<T, 32>(a, grid, s); break;
-    case 2: go_pages<T, 64>(a, grid, s); break;
-    case 3: go_pages<T, 96>(a, grid, s); break;
-    case 4: go_pages<T, 128>(a, grid, s); break;
-    case 5: go_pages<T, 160>(a, grid, s); break;
-    case 6: go_pages<T, 192>(a, grid, s); break;
-    case 7: go_pages<T, 224>(a, grid, s); break;
-    default: go_pages<T, 256>(a, grid, s); break;
+    case 1: go_pages<T, 32>(a, grid, s, form); break;
+    case 2: go_pages<T, 64>(a, grid, s, form); break;
+    case 3: go_pages<T, 96>(a, grid, s, form); break;
+    case 4: go_pages<T, 128>(a, grid, s, form); break;
+    case 5: go_pages<T, 160>(a, grid, s, form); break;
+    case 6: go_pages<T, 192>(a, grid, s, form); break;
+    case 7: go_pages<T, 224>(a, grid, s, form); break;
+    default: go_pages<T, 256>(a, grid, s, form); break;
   }
 }
 
-hipError_t launch_append(int dtype, const AppendArgs& a, hipStream_t s) {
+hipError_t launch_append(int dtype, const AppendArgs& a, hipStream_t s, Form& form) {
   if (dtype == EL_F32)
-    go_append<EL_F32>(a, s);
+    go_append<EL_F32>(a, s, form);
   else if (dtype == EL_BF16)
-    go_append<EL_BF16>(a, s);
+    go_append<EL_BF16>(a, s, form);
   else
-    go_append<EL_F16>(a, s);
+    go_append<EL_F16>(a, s, form);
   return hipGetLastError();
 }
 

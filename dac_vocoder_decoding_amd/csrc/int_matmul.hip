@@ -398,25 +398,28 @@ __global__ __launch_bounds__(WF * WT * 64) void int_matmul_tile_kernel(const Int
 }
 
 template <int T, bool SHIFT>
-static void go_few(const IntMatmulArgs& a, hipStream_t s) {
+static void go_few(const IntMatmulArgs& a, hipStream_t s, Form& form) {
   const int vec = a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % (4 * elem_size(T)) == 0;
   const unsigned gx = (a.N + 15) / 16;
   auto rows = [&](int mb) { return static_cast<unsigned>((a.M + 16 * mb - 1) / (16 * mb)); };
   // As many tokens a workgroup as leave about one to each CU (us, 64 x 1024 x
   // 4096 with 4 / 2 / 1 blocks of 16: 11.3 / 7.7 / 7.3, 64 x 2048 x 4096 11.7 /
   // 8.1, 64 x 3500 x 2048 7.3 / 8.4, 32 x 4096 x 1024 4.2 with 2, 4.6 with 1).
-  if (a.M > 32 && gx * rows(4) >= 192)
+  const int blocks = a.M > 32 && gx * rows(4) >= 192 ? 4 : a.M > 16 && gx * rows(2) >= 192 ? 2 : 1;
+  form = Form{SHIFT ? "product_few_shifted" : "product_few", {16, 16 * blocks}};
+  if (blocks == 4)
     int_matmul_few_kernel<T, 4, SHIFT><<<dim3(gx, rows(4)), 512, 0, s>>>(a, vec);
-  else if (a.M > 16 && gx * rows(2) >= 192)
+  else if (blocks == 2)
     int_matmul_few_kernel<T, 2, SHIFT><<<dim3(gx, rows(2)), 512, 0, s>>>(a, vec);
   else
     int_matmul_few_kernel<T, 1, SHIFT><<<dim3(gx, rows(1)), 512, 0, s>>>(a, vec);
 }
 
 template <int T, int BF, int BT, int WF, int WT, int NS, bool DMA>
-static void go_tile(const IntMatmulArgs& a, hipStream_t s) {
+static void go_tile(const IntMatmulArgs& a, hipStream_t s, Form& form) {
   const int tf = (a.N + BF - 1) / BF, tt = (a.M + BT - 1) / BT;
   const int vec = a.ldy * elem_size(T) % 16 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
+  form = Form{DMA ? "product_tile" : "product_tile_rows", {BF, BT}};
   int_matmul_tile_kernel<T, BF, BT, WF, WT, NS, DMA>
       <<<dim3(static_cast<unsigned>(tf) * tt), WF * WT * 64, 0, s>>>(a, tf, tt, vec);
 }
@@ -437,35 +440,35 @@ static void go_tile(const IntMatmulArgs& a, hipStream_t s) {
 //  * rows that are not 16-byte aligned go through registers in 64x64 tiles
 //    (689x1000x1501: 11.0; four waves 12.5, 128x64 17.4).
 template <int T>
-static void go_int_matmul(const IntMatmulArgs& a, hipStream_t s) {
+static void go_int_matmul(const IntMatmulArgs& a, hipStream_t s, Form& form) {
   auto tiles = [&](int f, int t) { return static_cast<int64_t>((a.N + f - 1) / f) * ((a.M + t - 1) / t); };
   const bool dma = a.K % 16 == 0 && a.lda % 16 == 0 && a.ldb % 16 == 0 && a.lda < (1 << 22) && a.ldb < (1 << 22) &&
                    (reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.b)) % 16 == 0;
   if (a.M <= 16 || static_cast<int64_t>(a.M) * a.N <= (dma ? 1 << 17 : 1 << 18)) {
     if ((reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.b) | a.lda | a.ldb) % 4 == 0)
-      go_few<T, false>(a, s);
+      go_few<T, false>(a, s, form);
     else
-      go_few<T, true>(a, s);
+      go_few<T, true>(a, s, form);
   } else if (!dma) {
-    go_tile<T, 64, 64, 4, 2, 2, false>(a, s);
+    go_tile<T, 64, 64, 4, 2, 2, false>(a, s, form);
   } else if (tiles(256, 256) >= 192) {
-    go_tile<T, 256, 256, 2, 4, 2, true>(a, s);
+    go_tile<T, 256, 256, 2, 4, 2, true>(a, s, form);
   } else if (tiles(128, 128) >= 384) {
-    go_tile<T, 128, 128, 2, 2, 2, true>(a, s);
+    go_tile<T, 128, 128, 2, 2, 2, true>(a, s, form);
   } else if (tiles(128, 64) >= 384) {
-    go_tile<T, 128, 64, 2, 2, 3, true>(a, s);
+    go_tile<T, 128, 64, 2, 2, 3, true>(a, s, form);
   } else {
-    go_tile<T, 64, 64, 4, 2, 4, true>(a, s);
+    go_tile<T, 64, 64, 4, 2, 4, true>(a, s, form);
   }
 }
 
-hipError_t launch_int_matmul(int dtype, const IntMatmulArgs& a, hipStream_t s) {
+hipError_t launch_int_matmul(int dtype, const IntMatmulArgs& a, hipStream_t s, Form& form) {
   if (dtype == EL_F32)
-    go_int_matmul<EL_F32>(a, s);
+    go_int_matmul<EL_F32>(a, s, form);
   else if (dtype == EL_BF16)
-    go_int_matmul<EL_BF16>(a, s);
+    go_int_matmul<EL_BF16>(a, s, form);
   else
-    go_int_matmul<EL_F16>(a, s);
+    go_int_matmul<EL_F16>(a, s, form);
   return hipGetLastError();
 }
 

@@ -10,6 +10,12 @@ namespace voc {
 enum ElemType { EL_F32 = 0, EL_BF16 = 1, EL_F16 = 2 };  // = voc_dtype
 inline int elem_size(int t) { return t == EL_F32 ? 4 : 2; }
 
+// The kernel that a launch chose (vocoder.h: voc_dbg_last_kernel).
+struct Form {
+  const char* kernel = "";
+  int shape[2] = {0, 0};
+};
+
 // Rows of 8-bit codes with one scale each (weight == null: no norm).
 struct RowsArgs {
   const void* x;
@@ -23,7 +29,7 @@ struct RowsArgs {
   int C;
 };
 constexpr int kRowsMaxC = 16384;
-hipError_t launch_rows(int dtype, const RowsArgs& a, hipStream_t s);
+hipError_t launch_rows(int dtype, const RowsArgs& a, hipStream_t s, Form& form);
 
 struct IntMatmulArgs {
   const int8_t* a;
@@ -36,7 +42,7 @@ struct IntMatmulArgs {
   int M, N, K;
   int act;            // VOC_ACT_*
 };
-hipError_t launch_int_matmul(int dtype, const IntMatmulArgs& a, hipStream_t s);
+hipError_t launch_int_matmul(int dtype, const IntMatmulArgs& a, hipStream_t s, Form& form);
 
 // The cache and the sequences of one step, as every kernel reads them.
 struct CacheView {
@@ -79,7 +85,7 @@ struct AppendArgs {
   int64_t k_t, k_h, v_t, v_h;  // element strides of the new keys and values
   int D, batch;
 };
-hipError_t launch_append(int dtype, const AppendArgs& a, hipStream_t s);
+hipError_t launch_append(int dtype, const AppendArgs& a, hipStream_t s, Form& form);
 
 struct AttendArgs {
   CacheView c;
@@ -94,6 +100,6 @@ struct AttendArgs {
   void* ws;
   size_t ws_bytes;
 };
-hipError_t launch_attend(int dtype, const AttendArgs& a, hipStream_t s);
+hipError_t launch_attend(int dtype, const AttendArgs& a, hipStream_t s, Form& form);
 
 }  // namespace voc

@@ -16,6 +16,7 @@ using namespace voc;
 struct voc_ops {
   int device = 0;
   void* ws = nullptr;
+  Form form;  // of the last launch
   char err[256] = "";
 };
 
@@ -151,6 +152,15 @@ VOC_API voc_status voc_ops_create(int hip_device, voc_ops** out) {
 
 VOC_API const char* voc_ops_last_error(const voc_ops* ops) { return ops ? ops->err : g_ops_create_error; }
 
+VOC_API const char* voc_dbg_last_kernel(const voc_ops* ops, int shape[2]) {
+  const Form none, &f = ops ? ops->form : none;
+  if (shape) {
+    shape[0] = f.shape[0];
+    shape[1] = f.shape[1];
+  }
+  return f.kernel;
+}
+
 VOC_API void voc_ops_destroy(voc_ops* ops) {
   if (!ops) return;
   {
@@ -175,7 +185,7 @@ VOC_API voc_status vocoder_rms_norm(voc_ops* o, int dtype, int64_t rows, int64_t
   if (!aligned(residual, elem_size(dtype)) || !aligned(h_out, elem_size(dtype)) || !aligned(weight, 4))
     return fail(o, VOC_INVALID_PARAMS, "pointers must be aligned to their elements");
   const RowsArgs a{x, residual, h_out, weight, eps, q, scale, rows, ldx, ldr, ldh, ldq, static_cast<int>(C)};
-  return on_device(o, "rms_norm", [&] { return launch_rows(dtype, a, static_cast<hipStream_t>(hip_stream)); });
+  return on_device(o, "rms_norm", [&] { return launch_rows(dtype, a, static_cast<hipStream_t>(hip_stream), o->form); });
 }
 
 VOC_API voc_status vocoder_quantize_rows(voc_ops* o, int dtype, int64_t rows, int64_t C, const void* x, int64_t ldx,
@@ -185,7 +195,7 @@ VOC_API voc_status vocoder_quantize_rows(voc_ops* o, int dtype, int64_t rows, in
   voc_status st = check_rows(o, dtype, rows, C, x, ldx, q, ldq, scale);
   if (st != VOC_OK || rows == 0) return st;
   const RowsArgs a{x, nullptr, nullptr, nullptr, 0.f, q, scale, rows, ldx, 0, 0, ldq, static_cast<int>(C)};
-  return on_device(o, "quantize_rows", [&] { return launch_rows(dtype, a, static_cast<hipStream_t>(hip_stream)); });
+  return on_device(o, "quantize_rows", [&] { return launch_rows(dtype, a, static_cast<hipStream_t>(hip_stream), o->form); });
 }
 
 VOC_API voc_status vocoder_matmul_int(voc_ops* o, int out_dtype, int64_t M, int64_t N, int64_t K, const int8_t* a,
@@ -208,7 +218,7 @@ VOC_API voc_status vocoder_matmul_int(voc_ops* o, int out_dtype, int64_t M, int6
     return fail(o, VOC_INVALID_PARAMS, "pointers must be aligned to their elements");
   const IntMatmulArgs g{a, b, a_scale, b_scale, bias, y, lda, ldb, ldy, static_cast<int>(M), static_cast<int>(N),
                         static_cast<int>(K), act};
-  return on_device(o, "matmul_int", [&] { return launch_int_matmul(out_dtype, g, static_cast<hipStream_t>(hip_stream)); });
+  return on_device(o, "matmul_int", [&] { return launch_int_matmul(out_dtype, g, static_cast<hipStream_t>(hip_stream), o->form); });
 }
 
 VOC_API voc_status vocoder_cache_append(voc_ops* o, const voc_kv_cache* cache, const voc_kv_batch* batch, int dtype,
@@ -235,7 +245,7 @@ VOC_API voc_status vocoder_cache_append(voc_ops* o, const voc_kv_cache* cache, c
   a.v_h = v_head_stride;
   a.D = cache->head_dim;
   a.batch = static_cast<int>(batch->batch);
-  return on_device(o, "cache_append", [&] { return launch_append(dtype, a, static_cast<hipStream_t>(hip_stream)); });
+  return on_device(o, "cache_append", [&] { return launch_append(dtype, a, static_cast<hipStream_t>(hip_stream), o->form); });
 }
 
 VOC_API voc_status vocoder_cache_attention(voc_ops* o, const voc_kv_cache* cache, const voc_kv_batch* batch, int dtype,
@@ -279,5 +289,5 @@ VOC_API voc_status vocoder_cache_attention(voc_ops* o, const voc_kv_cache* cache
   // A launch holds fewer than 2^32 threads (16 query rows in 256).
   if (static_cast<int64_t>(a.batch) * heads * ((batch->max_new + 15) / 16 + 1) >= 1 << 24)
     return fail(o, VOC_INVALID_PARAMS, "too many query rows for one call");
-  return on_device(o, "cache_attention", [&] { return launch_attend(dtype, a, static_cast<hipStream_t>(hip_stream)); });
+  return on_device(o, "cache_attention", [&] { return launch_attend(dtype, a, static_cast<hipStream_t>(hip_stream), o->form); });
 }

@@ -156,46 +156,50 @@ __global__ __launch_bounds__(256) void rows_kernel(const RowsArgs a) {
   }
 }
 
-template <int T, bool VEC>
-static void pick_rows(const RowsArgs& a, hipStream_t s) {
+template <int T, int NG, int WPR, bool VEC>
+static void launch_form(const RowsArgs& a, hipStream_t s, Form& form) {
+  form = Form{"rows", {NG, WPR}};
   // Enough workgroups to fill every CU eight times over (1024 or 8192: within 10 %).
-  const int64_t most = 2048;
-  const dim3 one(static_cast<unsigned>(a.rows < most ? a.rows : most));
-  const dim3 four(static_cast<unsigned>((a.rows + 3) / 4 < most ? (a.rows + 3) / 4 : most));
+  const int64_t most = 2048, wgs = WPR == 1 ? (a.rows + 3) / 4 : a.rows;
+  rows_kernel<T, NG, WPR, VEC><<<dim3(static_cast<unsigned>(wgs < most ? wgs : most)), 256, 0, s>>>(a);
+}
+
+template <int T, bool VEC>
+static void pick_rows(const RowsArgs& a, hipStream_t s, Form& form) {
   if (a.C <= 512)
-    rows_kernel<T, 1, 1, VEC><<<four, 256, 0, s>>>(a);
+    launch_form<T, 1, 1, VEC>(a, s, form);
   else if (a.C <= 1024)
-    rows_kernel<T, 2, 1, VEC><<<four, 256, 0, s>>>(a);
+    launch_form<T, 2, 1, VEC>(a, s, form);
   else if (a.C <= 2048)
-    rows_kernel<T, 1, 4, VEC><<<one, 256, 0, s>>>(a);
+    launch_form<T, 1, 4, VEC>(a, s, form);
   else if (a.C <= 4096)
-    rows_kernel<T, 2, 4, VEC><<<one, 256, 0, s>>>(a);
+    launch_form<T, 2, 4, VEC>(a, s, form);
   else if (a.C <= 8192)
-    rows_kernel<T, 4, 4, VEC><<<one, 256, 0, s>>>(a);
+    launch_form<T, 4, 4, VEC>(a, s, form);
   else
-    rows_kernel<T, 8, 4, VEC><<<one, 256, 0, s>>>(a);
+    launch_form<T, 8, 4, VEC>(a, s, form);
 }
 
 template <int T>
-static void go_rows(const RowsArgs& a, hipStream_t s) {
+static void go_rows(const RowsArgs& a, hipStream_t s, Form& form) {
   auto on16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
   constexpr int per16 = 16 / sizeof(typename Elem<T>::type);
   const bool vec = a.C % 8 == 0 && on16(a.x) && on16(a.r) && on16(a.h) && on16(a.weight) &&
                    reinterpret_cast<uintptr_t>(a.q) % 8 == 0 && a.ldx % per16 == 0 && a.ldr % per16 == 0 &&
                    a.ldh % per16 == 0 && a.ldq % 8 == 0;
   if (vec)
-    pick_rows<T, true>(a, s);
+    pick_rows<T, true>(a, s, form);
   else
-    pick_rows<T, false>(a, s);
+    pick_rows<T, false>(a, s, form);
 }
 
-hipError_t launch_rows(int dtype, const RowsArgs& a, hipStream_t s) {
+hipError_t launch_rows(int dtype, const RowsArgs& a, hipStream_t s, Form& form) {
   if (dtype == EL_F32)
-    go_rows<EL_F32>(a, s);
+    go_rows<EL_F32>(a, s, form);
   else if (dtype == EL_BF16)
-    go_rows<EL_BF16>(a, s);
+    go_rows<EL_BF16>(a, s, form);
   else
-    go_rows<EL_F16>(a, s);
+    go_rows<EL_F16>(a, s, form);
   return hipGetLastError();
 }
 

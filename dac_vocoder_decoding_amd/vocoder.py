@@ -161,6 +161,7 @@ def lib():
             "voc_ops_create": (I, [I, ctypes.POINTER(P)]),
             "voc_ops_last_error": (ctypes.c_char_p, [P]),
             "voc_ops_destroy": (None, [P]),
+            "voc_dbg_last_kernel": (ctypes.c_char_p, [P, ctypes.POINTER(I)]),
             "vocoder_rms_norm": (I, [P, I, I64, I64, P, I64, P, I64, P, I64, P, F, P, I64, P, P]),
             "vocoder_quantize_rows": (I, [P, I, I64, I64, P, I64, P, I64, P, P]),
             "vocoder_matmul_int": (I, [P, I, I64, I64, I64, P, I64, P, P, I64, P, P, I, P, I64, P]),
@@ -521,6 +522,12 @@ def voc_ops_last_error(ops) -> str:
 
 def voc_ops_destroy(ops) -> None:
     lib().voc_ops_destroy(ops)
+
+
+def voc_dbg_last_kernel(ops):
+    """(name, shape) of the kernel that the last call on ops launched."""
+    shape = (ctypes.c_int * 2)()
+    return lib().voc_dbg_last_kernel(ops, shape).decode(), tuple(shape)
 
 
 def open_ops(device: int = 0):

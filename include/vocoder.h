@@ -636,6 +636,17 @@ voc_status vocoder_cache_attention(voc_ops *ops, const voc_kv_cache *cache,
                                    int64_t o_token_stride, int64_t o_head_stride,
                                    void *hip_stream);
 
+/* Which kernel the last launch on ops chose ("" before the first), with what
+ * its choice by sizes comes to, so that tests can check that they reach the
+ * kernel they are about:
+ *   "rows"                        groups of 8 values a thread, waves a row
+ *   "product_few", "product_few_shifted"   features, tokens of a workgroup
+ *   "product_tile", "product_tile_rows"    the same (fed by DMA, through registers)
+ *   "append", "append_page"       threads of a workgroup, page_tokens
+ *   "attend_few", "attend_many"   query rows of a workgroup, parts of the keys
+ * shape may be NULL.  No error state is touched. */
+const char *voc_dbg_last_kernel(const voc_ops *ops, int shape[2]);
+
 #ifdef __cplusplus
 }
 #endif

@@ -856,11 +856,12 @@ def test_attention_many_short_prompts(ops, dtype, P, D, past, new, causal, windo
                    causal, window)
 
 
-def attend64_by_keys(cache, table, past, new, q, scale, causal, window, two=None):
+def attend64_by_keys(cache, table, past, new, q, scale, causal, window, two=None, hole=()):
     """Plain attention in 64 bits, with the bound of attend64 taken key by key
     (an error e of a probability p moves the output by at most p e (|v| + |o|))
     and fp16's last step as the kernels state it: 2^-35 of the row's largest
-    p times value scale for each key, times its code."""
+    p times value scale for each key, times its code.  `hole`: (sequence, column)
+    of pages that are missing from the table that the kernel was given."""
     Hq, H, D = q.shape[1], cache.kv_heads, q.shape[2]
     outs, tols, base = [], [], 0
     for b in range(len(past)):
@@ -879,7 +880,10 @@ def attend64_by_keys(cache, table, past, new, q, scale, causal, window, two=None
             seen &= j <= at
         if window:
             seen &= j > at - window
+        for c in (c for s, c in hole if s == b):
+            seen[:, c * cache.page_tokens:(c + 1) * cache.page_tokens] = False
         p = torch.softmax(((rows @ k) * scale).masked_fill(~seen, -math.inf), -1)
+        p = torch.where(seen.any(-1, keepdim=True), p, 0.0)
         two = q.dtype == F32 if two is None else two
         e = (D + 8 + 4) * E * abs(scale) * (rows.abs() @ k.abs()) + 2.0 ** -21 + (2.0 ** -21 if two else 2.0 ** -11) \
             + (total / 64 + 32) * E
@@ -975,3 +979,158 @@ def test_matmul_int_gelu_of_fp32(ops, M, N, K, spread):
     assert worst <= 2.2, worst
     # RMS: 0.5 x (1 + erf) has 3.8e-8 at a spread of 0.1 and less above 1.
     assert err.norm() <= 4.2e-8 * (N ** 0.5) * gelu64(x).norm()
+
+
+# ---------------------------------------- attention's kernel for many rows
+def check_kernel(ops, name, shape=None):
+    got = V.voc_dbg_last_kernel(ops)
+    assert got[0] == name and (shape is None or got[1] == shape), got
+
+
+def close(o, ref, tol):
+    worst = ((o.double() - ref).abs() / tol).max().item()
+    assert worst <= 1, worst
+
+
+MANY = [
+    # P, kv heads, D, group, past, new, causal, window, parts (None: 1 or 2)
+    (16, 16, 160, 1, [9 * i for i in range(16)], [130 - 3 * i for i in range(16)], True, 0, 1),
+    (32, 16, 192, 1, [50] * 16, [99] * 16, True, 40, 1),
+    (64, 8, 224, 2, [3 * i for i in range(32)], [41 + i % 7 for i in range(32)], False, 0, 1),
+    (128, 16, 256, 1, [0] * 16, [128] * 16, True, 0, 1),
+    (16, 4, 32, 3, [i for i in range(64)], [64] * 64, True, 0, 1),
+    (64, 4, 128, 5, [200 - 3 * i for i in range(64)], [20] * 64, True, 0, 1),
+    # Long enough for two parts of the keys, a short sequence among them.
+    (16, 16, 160, 1, [1000, 7], [600, 333], True, 0, 2), (32, 16, 192, 1, [1000, 0], [599, 600], True, 0, 2),
+    (64, 16, 224, 1, [1111, 40], [601, 1], True, 0, 2), (128, 16, 256, 1, [1000, 900], [600, 600], True, 0, 2),
+    (16, 16, 96, 1, [1000, 1], [600, 577], True, 0, 2), (64, 16, 128, 1, [1005, 65], [600, 600], True, 0, 2),
+    (32, 16, 64, 1, [1000, 0, 64, 999], [500, 500, 3, 450], True, 0, 2),
+    (16, 16, 32, 1, [1000, 0, 64, 999], [500, 500, 3, 450], True, 0, 2),
+    # Many parts.
+    (64, 8, 128, 1, [7900], [256], False, 0, None), (32, 8, 256, 1, [8000], [257], False, 0, None),
+    (128, 2, 192, 8, [16100], [70], True, 0, None),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("P,H,D,group,past,new,causal,window,parts", MANY)
+def test_attention_of_many_rows(ops, dtype, P, H, D, group, past, new, causal, window, parts):
+    g = gen(P + D + sum(past))
+    cache, table = filled(g, P, H, D, past, new)
+    q = randn(g, sum(new), H * group, D, dtype=dtype)
+    b = batch_of(table, past, new)
+    o = V.cache_attention(ops, cache, b, q, causal=causal, window=window)
+    name, shape = V.voc_dbg_last_kernel(ops)
+    assert name == "attend_many" and shape[0] == (128 if dtype == F32 or D > 128 else 256), (name, shape)
+    assert shape[1] > 4 if parts is None else shape[1] == parts, shape
+    close(o, *attend64(cache, table, past, new, q, D ** -0.5, causal, window))
+    assert torch.equal(o, V.cache_attention(ops, cache, b, q, causal=causal, window=window))
+
+
+# Few rows, many rows whole, many rows in two parts.
+SIZES = [("attend_few", 32, 4, 64, [100, 61], [20, 3], 1), ("attend_many", 16, 16, 64, [40] * 16, [140] * 16, 1),
+         ("attend_many", 64, 16, 192, [1000, 100], [600, 600], 2)]
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("kernel,P,H,D,past,new,parts", SIZES)
+def test_attention_negative_scale_and_sharp_scores(ops, dtype, kernel, P, H, D, past, new, parts):
+    g = gen(96)
+    for spread, std, scale in ((1.0, 1.0, -0.15), (30.0, 4.0, D ** -0.5), (30.0, 4.0, -(D ** -0.5))):
+        cache, table = filled(g, P, H, D, past, new, spread=spread)
+        q = randn(g, sum(new), H, D, dtype=dtype, std=std)
+        o = V.cache_attention(ops, cache, batch_of(table, past, new), q, scale=scale)
+        check_kernel(ops, kernel, (V.voc_dbg_last_kernel(ops)[1][0], parts))
+        close(o, *attend64_by_keys(cache, table, past, new, q, scale, True, 0))
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("kernel,P,H,D,past,new,parts", SIZES)
+def test_attention_missing_and_non_finite_pages(ops, dtype, kernel, P, H, D, past, new, parts):
+    """Pages that are missing (also the first, the last and a whole block of 64
+    keys), windows that lie in them, pages with NaN scales, a NaN query."""
+    g = gen(97)
+    cache, table = filled(g, P, H, D, past, new)
+    q = randn(g, sum(new), H, D, dtype=dtype)
+    last = (past[0] + new[0] - 1) // P
+    block = [c for c in range(last) if c * P < 64 <= c * P + P or 64 <= c * P < 128]     # keys 64 .. 127 and some
+    for columns in ([1], [0, last], block):
+        hole = table.clone()
+        for i, c in enumerate(columns):
+            hole[0, c] = -1 if i % 2 else 1 << 30
+        for window in (0, 3):
+            out = torch.full_like(q, 7.0)
+            V.cache_attention(ops, cache, batch_of(hole, past, new), q, window=window, out=out)
+            ref, tol = attend64_by_keys(cache, table, past, new, q, D ** -0.5, True, window, hole=[(0, c) for c in columns])
+            assert torch.equal((out == 0).all(-1), (ref == 0).all(-1))
+            # (Windows of 3 keys give values beyond fp16 here: those round to infinity.)
+            over = ref.to(dtype).isinf()
+            assert torch.equal(out[over], ref.to(dtype)[over]) and ((out.double() - ref).abs() <= tol)[~over].all()
+    o = V.cache_attention(ops, cache, batch_of(torch.full_like(table, -1), past, new), q, out=torch.full_like(q, 7.0))
+    check_kernel(ops, kernel)
+    assert (o == 0).all()
+    ref, tol = attend64_by_keys(cache, table, past, new, q, D ** -0.5, True, 0)
+    at = past[0] + torch.arange(new[0], device="cuda")
+    for s in (cache.k_scale, cache.v_scale):
+        kept, bad = s.clone(), torch.zeros(sum(new), H, dtype=torch.bool, device="cuda")
+        for column, head in ((past[0] // P + 1, 1), (0, 2)):
+            s[int(table[0, column]), head] = float("nan")
+            bad[:new[0], head] |= at >= column * P
+        o = V.cache_attention(ops, cache, batch_of(table, past, new), q)
+        assert o[bad].isnan().all() and ((o.double() - ref).abs() <= tol)[~bad].all()
+        s.copy_(kept)
+    q[5, 1, 3] = float("nan")
+    o = V.cache_attention(ops, cache, batch_of(table, past, new), q)
+    bad = torch.zeros(sum(new), H, dtype=torch.bool, device="cuda")
+    bad[5, 1] = True
+    assert o[bad].isnan().all() and ((o.double() - ref).abs() <= tol)[~bad].all()
+
+
+@pytest.mark.parametrize("kernel,P,H,D,past,new,parts", SIZES)
+def test_attention_strided_with_rows_between(ops, kernel, P, H, D, past, new, parts):
+    g = gen(98)
+    cache, table = filled(g, P, H, D, past, new)
+    n = sum(new)
+    big = randn(g, n + 5, 3, H, D, dtype=F16)
+    q = big[:, 1]
+    out = torch.full((n + 5, H, 2, D), 9.0, dtype=F16, device="cuda")[:, :, 0]
+    starts = [2 + s for s in starts_of(new)]
+    b = V.KVBatch(table, i32(past), i32(starts), max(new) + 6, 4096)
+    V.cache_attention(ops, cache, b, q, out=out)
+    check_kernel(ops, kernel)
+    close(out[2:2 + n], *attend64(cache, table, past, new, q[2:2 + n], D ** -0.5, True, 0))
+    assert (out[:2] == 9).all() and (out[2 + n:] == 9).all()
+
+
+@pytest.mark.parametrize("kernel,P,H,D,past,new,parts", SIZES)
+def test_attention_ranges_of_queries(ops, kernel, P, H, D, past, new, parts):
+    """Rows of very large, very small and zero queries beside ordinary ones."""
+    g = gen(99)
+    cache, table = filled(g, P, H, D, past, new)
+    n = sum(new)
+    gain = torch.tensor([1e30, 1e-30, 0.0, 1.0, 1e-38, 1e4], device="cuda").repeat(-(-n // 6))[:n, None, None]
+    for dtype in (F32, BF16):
+        q = (randn(g, n, H, D) * gain).to(dtype)
+        o = V.cache_attention(ops, cache, batch_of(table, past, new), q, scale=1e-3)
+        check_kernel(ops, kernel)
+        ref, tol = attend64_by_keys(cache, table, past, new, q, 1e-3, True, 0)
+        # (Among scores of 1e28 ties cannot be told from near ties.)
+        assert ((o.double() - ref).abs() <= tol)[gain[:, 0, 0] < 1e30].all()
+        assert torch.isfinite(o).all()
+
+
+def test_attention_of_many_rows_beyond_4_gib(ops):
+    """The same offsets past 32 bits for the kernel for many rows."""
+    g = gen(86)
+    P, H, D, pages, n = 128, 8, 256, 17000, 2300
+    cache = V.KVCache.from_tensors(
+        torch.empty(pages, H, P, D, dtype=torch.int8, device="cuda"),
+        torch.empty(pages, H, D, P, dtype=torch.int8, device="cuda"),
+        torch.full((pages, H), float("nan"), device="cuda"), torch.full((pages, H), float("nan"), device="cuda"))
+    table = torch.arange(pages - 18, pages, device="cuda", dtype=torch.int32).flip(0)[None].contiguous()
+    k, v, q = (randn(g, n, H, D, dtype=F16) for _ in range(3))
+    b = batch_of(table, [0], [n])
+    V.cache_append(ops, cache, b, k, v)
+    o = V.cache_attention(ops, cache, b, q)
+    check_kernel(ops, "attend_many")
+    close(o, *attend64(cache, table, [0], [n], q, 1 / 16, True, 0))
