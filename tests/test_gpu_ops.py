@@ -1134,3 +1134,51 @@ def test_attention_of_many_rows_beyond_4_gib(ops):
     o = V.cache_attention(ops, cache, b, q)
     check_kernel(ops, "attend_many")
     close(o, *attend64(cache, table, [0], [n], q, 1 / 16, True, 0))
+
+
+# ----------------------------------------------- every form of the product
+def check_product_on_gpu(y, a, b, sa, sb, bias, gelu):
+    """check_product with the integer sums in 64-bit floats (below 2^53) on the GPU."""
+    prod = (a.double() @ b.double().t()) * sa.double()[:, None] * sb.double()
+    add = torch.zeros_like(sb, dtype=torch.float64) if bias is None else bias.double()
+    ref, size = prod + add, prod.abs() + add.abs()
+    err = 4 * E * size
+    if gelu:
+        err, ref = 1.13 * err + 8 * E * size, gelu64(ref)
+    close(y, ref, err * (1 + U[y.dtype]) + U[y.dtype] * ref.abs() + SUB[y.dtype] + 1e-300)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("M,N,K,pad,offset,kernel,shape", [
+    # Few tokens, 16, 32 and 64 a workgroup, rows that can be read as they lie.
+    (3, 500, 200, 0, 0, "product_few", (16, 16)), (16, 4100, 64, 16, 0, "product_few", (16, 16)),
+    (32, 4096, 1024, 0, 0, "product_few", (16, 32)), (17, 3100, 200, 0, 4, "product_few", (16, 32)),
+    (33, 3100, 128, 0, 0, "product_few", (16, 64)), (64, 2000, 4096, 0, 0, "product_few", (16, 32)),
+    (70, 1560, 1056, 4, 4, "product_few", (16, 64)),
+    # Rows that are read in shifted words.
+    (5, 1000, 333, 0, 1, "product_few_shifted", (16, 16)), (20, 3100, 333, 0, 3, "product_few_shifted", (16, 32)),
+    (40, 3100, 77, 0, 0, "product_few_shifted", (16, 64)), (70, 2000, 333, 2, 5, "product_few_shifted", (16, 64)),
+    (64, 3200, 1709, 0, 0, "product_few_shifted", (16, 64)), (1, 70, 3, 0, 1, "product_few_shifted", (16, 16)),
+    # Every tile.
+    (700, 640, 2064, 0, 0, "product_tile", (64, 64)), (390, 700, 16, 0, 0, "product_tile", (64, 64)),
+    (2000, 1600, 208, 0, 16, "product_tile", (128, 64)), (2500, 2500, 400, 16, 0, "product_tile", (128, 128)),
+    (3331, 3900, 272, 0, 0, "product_tile", (256, 256)), (1300, 1210, 77, 0, 0, "product_tile_rows", (64, 64)),
+    (600, 700, 128, 8, 0, "product_tile_rows", (64, 64))])
+def test_matmul_int_forms_with_bias_and_gelu(ops, dtype, M, N, K, pad, offset, kernel, shape):
+    g = gen(M + N + K)
+
+    def codes(rows):
+        x = torch.randint(-127, 128, (rows * (K + pad) + offset,), generator=g, device="cuda", dtype=torch.int8)
+        return x[offset:].view(rows, K + pad)[:, :K]
+
+    a, b = codes(M), codes(N)
+    sa = torch.rand(M, generator=g, device="cuda") * 0.02
+    sb = torch.rand(N, generator=g, device="cuda") * 0.02 / math.sqrt(K)
+    bias = randn(g, N)
+    for use, gelu in ((bias, True), (bias, False), (None, True)):
+        for width in (N, N + 3):                       # rows of outputs that are aligned and that are not
+            big = torch.full((M + 1, width), 7.0, dtype=dtype, device="cuda")
+            y = V.matmul_int(ops, a, sa, b, sb, bias=use, gelu=gelu, out=big[:M, :N])
+            check_kernel(ops, kernel, shape)
+            check_product_on_gpu(y, a, b, sa, sb, use, gelu)
+            assert (big[M:] == 7).all() and (big[:, N:] == 7).all()
