@@ -1182,3 +1182,78 @@ def test_matmul_int_forms_with_bias_and_gelu(ops, dtype, M, N, K, pad, offset, k
             check_kernel(ops, kernel, shape)
             check_product_on_gpu(y, a, b, sa, sb, use, gelu)
             assert (big[M:] == 7).all() and (big[:, N:] == 7).all()
+
+
+# ------------------------------------------------ every form of the append
+def appended(cache, table, past, new, k, v):
+    """What cache_append leaves, by the stated formulas in fp32 on the CPU:
+    (codes [pages, H, P, D], scales) of keys and values."""
+    inv127 = torch.tensor(1.0, dtype=F32) / 127
+    P, out = cache.page_tokens, []
+    starts = starts_of(new)
+    for codes, scale, x in ((cache.k, cache.k_scale, k), (cache.v.transpose(2, 3), cache.v_scale, v)):
+        codes, scale, x = codes.cpu().float(), scale.cpu().clone(), x.cpu().float()
+        for b in range(len(past)):
+            for t0 in range(past[b] // P * P, past[b] + new[b], P):
+                page, lo, hi = int(table[b, t0 // P]), max(t0, past[b]), min(t0 + P, past[b] + new[b])
+                rows = x[starts[b] + lo - past[b]:starts[b] + hi - past[b]].transpose(0, 1)      # [H, tokens, D]
+                amax = rows.abs().amax((1, 2))
+                own = torch.where(amax < 2.0 ** -100, torch.zeros(()), amax * inv127)
+                was = scale[page].clone() if lo > t0 else torch.zeros_like(own)
+                now = torch.maximum(was, own)
+                inv = torch.where(now > 0, 1 / now, torch.zeros(()))[:, None, None]
+                if lo > t0:
+                    kept = codes[page][:, :lo - t0]
+                    codes[page][:, :lo - t0] = torch.where((now > was)[:, None, None], (kept * (was[:, None, None] * inv)).round(), kept)
+                codes[page][:, lo - t0:hi - t0] = (rows * inv).round().clamp(-127, 127)
+                scale[page] = now
+        out += [codes, scale]
+    return out
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("P,H,D,past,new,lean,kernel,threads", [
+    # Few tokens, into partly filled pages and over their ends.
+    (16, 2, 64, [5, 15, 0], [1, 2, 8], 0, "append", 256), (64, 3, 96, [60, 63, 200], [8, 1, 5], 0, "append", 256),
+    (128, 1, 256, [127, 3], [2, 7], 0, "append", 256),
+    # Rows of any alignment, any number of tokens.
+    (16, 2, 64, [5, 0], [40, 17], 1, "append", 256), (64, 3, 128, [100, 64], [9, 130], 3, "append", 256),
+    (32, 1, 160, [31, 7], [200, 1], 1, "append", 256),
+    # Pages built whole: one wave, where there are pages enough; two; four; more units than stay in registers.
+    (16, 16, 64, [(7 * i) % 40 for i in range(40)], [40] * 40, 0, "append_page", 64),
+    (16, 16, 128, [(5 * i) % 33 for i in range(40)], [40 - i % 9 for i in range(40)], 0, "append_page", 64),
+    (32, 16, 64, [(9 * i) % 64 for i in range(48)], [33] * 48, 0, "append_page", 64),
+    (32, 2, 64, [5, 31, 32, 0], [9, 70, 3, 64], 0, "append_page", 128), (128, 2, 32, [100, 0], [60, 9], 0, "append_page", 128),
+    (16, 1, 224, [3, 0], [30, 16], 0, "append_page", 128),
+    (64, 2, 128, [70, 3, 0], [25, 200, 64], 0, "append_page", 256), (128, 1, 256, [130, 1], [300, 127], 0, "append_page", 256),
+    (64, 2, 192, [33, 63], [10, 66], 0, "append_page", 256)])
+def test_append_follows_its_formulas(ops, dtype, P, H, D, past, new, lean, kernel, threads):
+    """Codes and scales bit for bit, over pages that hold tokens: some heads'
+    scales grow by the new tokens, some by far, some stay, one is all zeros."""
+    g = gen(P + D + sum(new))
+    table, pages = table_for(g, [-(-(p + n) // P) for p, n in zip(past, new)], spare=1)
+    cache = V.KVCache(pages, P, H, D)
+    for codes, scale in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        codes.copy_(torch.randint(-127, 128, codes.shape, generator=g, device="cuda", dtype=torch.int8))
+        scale.copy_(torch.rand(scale.shape, generator=g, device="cuda") * 0.02 + 0.005)
+    n, wide = sum(new), 2 * H * D + 8 * (1 if lean else 0)
+    big = randn(g, n, wide, dtype=dtype)[:, lean:lean + 2 * H * D].view(n, 2 * H, D)
+    gain = torch.tensor([1.0, 0.05, 30.0], device="cuda")[torch.arange(2 * H, device="cuda") % 3]
+    big.mul_(gain[:, None].to(dtype))
+    big[:, H + H // 2] = 0
+    k, v = big[:, :H], big[:, H:]
+    want = appended(cache, table, past, new, k, v)
+    before = cache.k.clone(), cache.v.clone(), cache.k_scale.clone(), cache.v_scale.clone()
+    V.cache_append(ops, cache, batch_of(table, past, new), k, v)
+    check_kernel(ops, kernel, (threads, P))
+    got = [cache.k.cpu().float(), cache.k_scale.cpu(), cache.v.transpose(2, 3).cpu().float(), cache.v_scale.cpu()]
+    assert torch.equal(got[1], want[1]) and torch.equal(got[3], want[3])
+    touched = torch.zeros(pages, dtype=torch.bool, device="cuda")
+    for b in range(len(past)):
+        for c in range(past[b] // P, -(-(past[b] + new[b]) // P)):
+            page, live = int(table[b, c]), min(P, past[b] + new[b] - c * P)
+            touched[page] = True
+            for i in (0, 2):
+                assert torch.equal(got[i][page, :, :live], want[i][page, :, :live]), (b, c, i)
+    for x, old in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), before):
+        assert torch.equal(x[~touched], old[~touched])
