@@ -504,7 +504,10 @@ def run_stage(ctx, stage: int, x, stream=None):
 # The calls of vocoder.h take raw pointers and strides; the helpers below take
 # CUDA tensors, read the strides off them, check the shapes that the library
 # cannot see, and allocate what is not given.  All of them run on `stream`
-# (default: torch's current stream).
+# (default: torch's current stream).  With another stream than the current
+# one, tensors that are read or written stay allocated until that stream has
+# passed the call, and new ones are allocated on it and may be used and freed
+# on the current one; the order of the work on the two is the caller's.
 
 def voc_ops_create(device: int = 0):
     """Returns (status, ops)."""
@@ -557,10 +560,41 @@ def _use_torch() -> None:
 
 
 def _stream_of(stream, t):
-    """`stream`, or the current stream of t's device."""
+    """The address of `stream` (of the current stream of t's device if that is
+    None), and the stream itself if it is not the current one."""
+    device = t.get_device()
+    here = _raw_stream(device)
     if stream is None:
-        return _raw_stream(t.get_device())
-    return stream if isinstance(stream, int) else stream.cuda_stream
+        return here, None
+    raw = stream if isinstance(stream, int) else stream.cuda_stream
+    if raw == here:
+        return raw, None
+    if isinstance(stream, int):
+        import torch
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    return raw, stream
+
+
+def _new(other, shape, dtype, device):
+    """An empty tensor for a call on `other` (None: on the current stream).
+
+    One from the current stream's pool could be memory that work pending there
+    still uses, and could be handed out again while `other` still writes it."""
+    if other is None:
+        return _empty(shape, dtype=dtype, device=device)
+    import torch
+    with torch.cuda.stream(other):
+        t = _empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _keep(other, *tensors) -> None:
+    """Keeps the memory of tensors (None among them) until `other` has passed
+    what was launched on it so far."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(other)
 
 
 def _dtype(t) -> int:
@@ -600,25 +634,27 @@ def rms_norm(ops, x, weight, eps: float = 1e-6, residual=None, h=None, q=None, s
     residual, and is x itself without one."""
     shape, dtype, device = x.shape, x.dtype, x.device
     ldx = _rows("x", x, shape, dtype)
+    raw, other = _stream_of(stream, x)
     rows, C = shape
     r = hp = None
     ldr = ldh = 0
     if residual is not None:
         ldr, r = _rows("residual", residual, shape, dtype), residual.data_ptr()
         if h is None:
-            h, ldh = _empty(shape, dtype=dtype, device=device), C
+            h, ldh = _new(other, shape, dtype, device), C
             hp = h.data_ptr()
     if h is not None and hp is None:
         ldh, hp = _rows("h", h, shape, dtype), h.data_ptr()
     if q is None:
-        q, ldq = _empty(shape, dtype=_int8, device=device), C
+        q, ldq = _new(other, shape, _int8, device), C
     else:
         ldq = _rows("q", q, shape, _int8)
     if scale is None:
-        scale = _empty(rows, dtype=_float32, device=device)
+        scale = _new(other, rows, _float32, device)
     st = lib().vocoder_rms_norm(ops, _dtype(dtype), rows, C, x.data_ptr(), ldx, r, ldr, hp, ldh,
-                                _vector("weight", weight, C), eps, q.data_ptr(), ldq, _vector("scale", scale, rows),
-                                _stream_of(stream, x))
+                                _vector("weight", weight, C), eps, q.data_ptr(), ldq, _vector("scale", scale, rows), raw)
+    if other is not None:
+        _keep(other, x, residual, h, weight, q, scale)
     if st:
         _check_ops(st, ops)
     return q, scale, x if h is None else h
@@ -629,15 +665,18 @@ def quantize_rows(ops, x, q=None, scale=None, stream=None):
     (vocoder_quantize_rows)."""
     shape, dtype, device = x.shape, x.dtype, x.device
     ldx = _rows("x", x, shape, dtype)
+    raw, other = _stream_of(stream, x)
     rows, C = shape
     if q is None:
-        q, ldq = _empty(shape, dtype=_int8, device=device), C
+        q, ldq = _new(other, shape, _int8, device), C
     else:
         ldq = _rows("q", q, shape, _int8)
     if scale is None:
-        scale = _empty(rows, dtype=_float32, device=device)
+        scale = _new(other, rows, _float32, device)
     st = lib().vocoder_quantize_rows(ops, _dtype(dtype), rows, C, x.data_ptr(), ldx, q.data_ptr(), ldq,
-                                     _vector("scale", scale, rows), _stream_of(stream, x))
+                                     _vector("scale", scale, rows), raw)
+    if other is not None:
+        _keep(other, x, q, scale)
     if st:
         _check_ops(st, ops)
     return q, scale
@@ -651,11 +690,12 @@ def matmul_int(ops, a, a_scale, b, b_scale, bias=None, gelu: bool = False, dtype
     M, K = a.shape
     N = b.shape[0]
     ldb = _rows("b", b, (N, K), _int8)
+    raw, other = _stream_of(stream, a)
     if out is None:
         if dtype is None:
             import torch
             dtype = torch.float16
-        out, ldy = _empty((M, N), dtype=dtype, device=a.device), N
+        out, ldy = _new(other, (M, N), dtype, a.device), N
     else:
         if dtype is None:
             dtype = out.dtype
@@ -663,7 +703,9 @@ def matmul_int(ops, a, a_scale, b, b_scale, bias=None, gelu: bool = False, dtype
     st = lib().vocoder_matmul_int(
         ops, _dtype(dtype), M, N, K, a.data_ptr(), lda, _vector("a_scale", a_scale, M), b.data_ptr(), ldb,
         _vector("b_scale", b_scale, N), None if bias is None else _vector("bias", bias, N),
-        VOC_ACT_GELU if gelu else VOC_ACT_NONE, out.data_ptr(), ldy, _stream_of(stream, a))
+        VOC_ACT_GELU if gelu else VOC_ACT_NONE, out.data_ptr(), ldy, raw)
+    if other is not None:
+        _keep(other, a, a_scale, b, b_scale, bias, out)
     if st:
         _check_ops(st, ops)
     return out
@@ -694,7 +736,7 @@ class KVCache:
                              (k_scale, (n, h), torch.float32), (v_scale, (n, h), torch.float32)):
             if tuple(t.shape) != shape or t.dtype != dt or not t.is_cuda or not t.is_contiguous():
                 raise ValueError(f"cache: a contiguous CUDA {dt} tensor of shape {shape} is needed")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.k, self.v, self.k_scale, self.v_scale = self.tensors = k, v, k_scale, v_scale
         self.kv_heads, self.page_tokens, self.head_dim = h, p, d
         self.c = voc_kv_cache(p, h, d, n, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
         self.ref = ctypes.byref(self.c)
@@ -712,7 +754,7 @@ class KVBatch:
                                ("starts", starts, (B + 1,))):
             if t.dtype != torch.int32 or not t.is_cuda or tuple(t.shape) != shape or not t.is_contiguous():
                 raise ValueError(f"{what}: a contiguous CUDA int32 tensor of shape {shape} is needed")
-        self.page_table, self.past, self.starts = page_table, past, starts
+        self.page_table, self.past, self.starts = self.tensors = page_table, past, starts
         self.c = voc_kv_batch(B, 0, max_new, max_total, starts.data_ptr(), past.data_ptr(), page_table.data_ptr(),
                               page_table.shape[1])
         self.ref = ctypes.byref(self.c)
@@ -737,8 +779,11 @@ def cache_append(ops, cache: KVCache, batch: KVBatch, k, v, stream=None) -> None
     kt, kh = _heads("k", k, shape, dtype)
     vt, vh = _heads("v", v, shape, dtype)
     batch.c.tokens = tokens
+    raw, other = _stream_of(stream, k)
     st = lib().vocoder_cache_append(ops, cache.ref, batch.ref, _dtype(dtype), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
-                                    _stream_of(stream, k))
+                                    raw)
+    if other is not None:
+        _keep(other, k, v, *cache.tensors, *batch.tensors)
     if st:
         _check_ops(st, ops)
 
@@ -751,13 +796,16 @@ def cache_attention(ops, cache: KVCache, batch: KVBatch, q, scale: float | None 
     qt, qh = _heads("q", q, shape, dtype)
     if shape[2] != dim:
         raise ValueError(f"q: head_dim {dim} is needed, got {shape[2]}")
+    raw, other = _stream_of(stream, q)
     if out is None:
-        out = _empty(shape, dtype=dtype, device=q.device)
+        out = _new(other, shape, dtype, q.device)
     ot, oh = _heads("out", out, shape, dtype)
     batch.c.tokens = shape[0]
     st = lib().vocoder_cache_attention(ops, cache.ref, batch.ref, _dtype(dtype), shape[1], q.data_ptr(), qt, qh,
                                        dim ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(), ot, oh,
-                                       _stream_of(stream, q))
+                                       raw)
+    if other is not None:
+        _keep(other, q, out, *cache.tensors, *batch.tensors)
     if st:
         _check_ops(st, ops)
     return out

@@ -1257,3 +1257,68 @@ def test_append_follows_its_formulas(ops, dtype, P, H, D, past, new, lean, kerne
                 assert torch.equal(got[i][page, :, :live], want[i][page, :, :live]), (b, c, i)
     for x, old in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), before):
         assert torch.equal(x[~touched], old[~touched])
+
+
+# ------------------------------------------------------- memory and streams
+def calls_on(ops, n):
+    """name -> (inputs, call(inputs, stream) -> new outputs): every helper, its
+    outputs and its inputs of sizes that nothing else in these tests has."""
+    g = gen(120)
+    cache, table = filled(g, 16, 8, 64, [30], [n])
+    b = batch_of(table, [30], [n])
+    w, codes, s = torch.ones(512, device="cuda"), torch.ones(512, 512, dtype=torch.int8, device="cuda"), torch.ones(512, device="cuda")
+    rows = lambda *shape, dtype=F32: torch.ones(n, *shape, device="cuda", dtype=dtype)     # noqa: E731
+    return {
+        "rms_norm": (lambda: [rows(512), rows(512)], lambda x, t: V.rms_norm(ops, x[0], w, residual=x[1], stream=t)),
+        "quantize_rows": (lambda: [rows(512)], lambda x, t: V.quantize_rows(ops, x[0], stream=t)),
+        "matmul_int": (lambda: [rows(512, dtype=torch.int8), rows()], lambda x, t: [V.matmul_int(ops, *x, codes, s, stream=t)]),
+        "cache_append": (lambda: [rows(8, 64), rows(8, 64)], lambda x, t: [V.cache_append(ops, cache, b, *x, stream=t)][:0]),
+        "cache_attention": (lambda: [rows(8, 64)], lambda x, t: [V.cache_attention(ops, cache, b, x[0], stream=t)]),
+    }
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("name", ["rms_norm", "quantize_rows", "matmul_int", "cache_append", "cache_attention"])
+def test_explicit_stream_keeps_memory(ops, name, raw):
+    """While a call is pending on an explicit stream, the memory that it reads
+    and writes is not handed out again on the current one, and its outputs are
+    no memory that pending work of the current stream may still use."""
+    n = 4099
+    make, call = calls_on(ops, n)[name]
+    s = torch.cuda.Stream()
+    stream = s.cuda_stream if raw else s
+    want = [x.clone() for x in call(make(), None)]
+    torch.cuda.synchronize()
+    sizes = [(x.shape, x.dtype) for x in make() + want]
+    torch.cuda.synchronize()
+    # The allocator does hand out a freed block of a size again at once.
+    for shape, dtype in sizes:
+        t = torch.empty(shape, dtype=dtype, device="cuda")
+        at = t.data_ptr()
+        del t
+        assert torch.empty(shape, dtype=dtype, device="cuda").data_ptr() == at
+    # Blocks of the outputs' sizes that pending work of the current stream uses.
+    x = make()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    busy = [torch.empty(shape, dtype=dtype, device="cuda") for shape, dtype in sizes]
+    taken = {t.data_ptr() for t in busy}
+    del busy
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)                     # about 0.1 s
+    y = call(x, stream)
+    assert not taken & {t.data_ptr() for t in y}
+    held = {t.data_ptr() for t in x + list(y)}
+    del x, y
+    fresh = [torch.empty(shape, dtype=dtype, device="cuda") for shape, dtype in sizes for _ in range(3)]
+    pending = not s.query()
+    assert not held & {t.data_ptr() for t in fresh}
+    assert pending                                         # (else the above says nothing)
+    # And what comes out is right, used on the current stream after the wait, freed there.
+    x = make()
+    s.wait_stream(torch.cuda.current_stream())
+    y = call(x, stream)
+    torch.cuda.current_stream().wait_stream(s)
+    for got, right in zip(y, want):
+        assert torch.equal(got, right)
+    torch.cuda.synchronize()
