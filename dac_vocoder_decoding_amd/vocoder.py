@@ -325,8 +325,10 @@ def encode(ctx, audio, latent_channels: int, stream=None):
     b, _, n = audio.shape
     hop = vocoder_output_length(ctx, 1)
     assert n % hop == 0
-    z = torch.empty(b, latent_channels, n // hop, device=audio.device)
-    check(vocoder_encode(ctx, audio, b, n // hop, z, stream), ctx)
+    other, z = _output(stream, audio, b, latent_channels, n // hop)
+    st = vocoder_encode(ctx, audio, b, n // hop, z, stream)
+    _keep(other, audio, z)
+    check(st, ctx)
     return z
 
 
@@ -419,6 +421,18 @@ def check(st: int, ctx=None) -> None:
 
 
 # ---------------------------------------------------- marshalling helpers
+# With an explicit `stream` that is not the current one, the new tensor may be
+# used and freed on the current one, and the input is kept until `stream` has
+# passed the call; the order of the work on the two is the caller's.
+def _output(stream, t, *shape):
+    """(the stream of the call if it is not the current one, a new CUDA fp32
+    tensor for the call's output beside its input t)."""
+    if _empty is None:
+        _use_torch()
+    other = None if stream is None else _stream_of(stream, t)[1]
+    return other, _new(other, shape, _float32, t.device)
+
+
 def open_context(cfg_dict: dict, tensors: dict, device: int = 0, **overrides):
     """vocoder_create + vocoder_load_weights; raises VocError on failure."""
     cfg = config_from_dict({**cfg_dict, **overrides})
@@ -452,8 +466,10 @@ def decode(ctx, latent, stream=None):
     assert latent.is_cuda and latent.dtype == torch.float32 and latent.is_contiguous()
     expect_dim("latent", latent.shape, 1, latent_channels(ctx))
     b, _, t = latent.shape
-    pcm = torch.empty(b, out_channels(ctx), vocoder_output_length(ctx, t), device=latent.device)
-    check(vocoder_decode(ctx, latent, b, t, pcm, stream), ctx)
+    other, pcm = _output(stream, latent, b, out_channels(ctx), vocoder_output_length(ctx, t))
+    st = vocoder_decode(ctx, latent, b, t, pcm, stream)
+    _keep(other, latent, pcm)
+    check(st, ctx)
     return pcm
 
 
@@ -468,9 +484,11 @@ def decode_windows(ctx, windows, sides: int, last_frames: int, crop_left: int, c
     N = vocoder_windows_output_length(ctx, n, L, last_frames, crop_left, crop_right)
     if N < 0:
         raise VocError(VOC_INVALID_PARAMS, "bad window lengths or crops")
-    pcm = torch.empty(sides * out_channels(ctx), N, device=windows.device)
-    check(vocoder_decode_windows(ctx, windows, n, sides, L, last_frames, crop_left, crop_right,
-                                 pcm, stream), ctx)
+    other, pcm = _output(stream, windows, sides * out_channels(ctx), N)
+    st = vocoder_decode_windows(ctx, windows, n, sides, L, last_frames, crop_left, crop_right,
+                                pcm, stream)
+    _keep(other, windows, pcm)
+    check(st, ctx)
     return pcm
 
 
@@ -482,8 +500,10 @@ def stream_decode(ctx, latent, stream=None):
     expect_dim("latent", latent.shape, 0, _stream_rows.get(_key(ctx), 0))
     expect_dim("latent", latent.shape, 1, latent_channels(ctx))
     rows, _, t = latent.shape
-    pcm = torch.empty(rows, out_channels(ctx), vocoder_output_length(ctx, t), device=latent.device)
-    check(vocoder_stream_decode(ctx, latent, t, pcm, stream), ctx)
+    other, pcm = _output(stream, latent, rows, out_channels(ctx), vocoder_output_length(ctx, t))
+    st = vocoder_stream_decode(ctx, latent, t, pcm, stream)
+    _keep(other, latent, pcm)
+    check(st, ctx)
     return pcm
 
 
@@ -495,8 +515,10 @@ def run_stage(ctx, stage: int, x, stream=None):
     st, c_in, c_out, t_out = voc_dbg_stage_shape(ctx, stage, t)
     check(st, ctx)
     expect_dim("stage input", x.shape, 1, c_in)
-    out = torch.empty(b, c_out, t_out, device=x.device)
-    check(voc_dbg_run_stage(ctx, stage, x, b, t, out, stream), ctx)
+    other, out = _output(stream, x, b, c_out, t_out)
+    st = voc_dbg_run_stage(ctx, stage, x, b, t, out, stream)
+    _keep(other, x, out)
+    check(st, ctx)
     return out
 
 
@@ -590,11 +612,12 @@ def _new(other, shape, dtype, device):
 
 
 def _keep(other, *tensors) -> None:
-    """Keeps the memory of tensors (None among them) until `other` has passed
-    what was launched on it so far."""
-    for t in tensors:
-        if t is not None:
-            t.record_stream(other)
+    """Keeps the memory of tensors (None among them) until `other` (None: the
+    current stream, whose memory it is) has passed what was launched on it."""
+    if other is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(other)
 
 
 def _dtype(t) -> int:

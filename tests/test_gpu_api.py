@@ -194,3 +194,46 @@ def test_measured_peaks_are_plausible():
     assert V.voc_dbg_peak(0, 100)[0] == V.VOC_INVALID_PARAMS
     assert V.voc_dbg_peak(5, 100)[0] == V.VOC_INVALID_PARAMS
     assert V.voc_dbg_peak(1, 0)[0] == V.VOC_INVALID_PARAMS
+
+
+@pytest.mark.parametrize("name", ["decode", "decode_windows", "run_stage"])
+def test_explicit_stream_keeps_memory(weights, name):
+    """While a call is pending on an explicit stream, the memory that it reads
+    and writes is not handed out again on the current one, and its output is no
+    memory that pending work of the current stream may still use."""
+    ctx = V.open_context(CFG, weights)
+    c = CFG["latent_channels"]
+    call = {"decode": lambda x, t: V.decode(ctx, x, stream=t),
+            "decode_windows": lambda x, t: V.decode_windows(ctx, x, 1, 37, 3, 5, stream=t),
+            "run_stage": lambda x, t: V.run_stage(ctx, 0, x, stream=t)}[name]
+    try:
+        x = to_dev(I.make_latent(CFG, batch=3, frames=37))
+        assert x.shape[1] == c
+        want = call(x, None).clone()
+        shape = want.shape
+        s = torch.cuda.Stream()
+        call(x, s)                                         # (the context's workspace is there from here on)
+        torch.cuda.synchronize()
+        keep = x.clone()
+        torch.cuda._sleep(20_000_000)
+        busy = torch.empty(shape, device="cuda")
+        taken = busy.data_ptr()
+        del busy
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(200_000_000)                 # about 0.1 s
+        y = call(x, s)
+        assert y.data_ptr() != taken
+        held = {x.data_ptr(), y.data_ptr()}
+        sizes = (x.shape, shape)
+        del x, y
+        fresh = [torch.empty(size, device="cuda") for size in sizes for _ in range(3)]
+        pending = not s.query()
+        assert not held & {t.data_ptr() for t in fresh}
+        assert pending                                     # (else the above says nothing)
+        s.wait_stream(torch.cuda.current_stream())
+        y = call(keep, s)
+        torch.cuda.current_stream().wait_stream(s)
+        assert torch.equal(y, want)
+    finally:
+        torch.cuda.synchronize()
+        V.vocoder_destroy(ctx)
