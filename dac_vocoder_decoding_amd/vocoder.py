@@ -531,10 +531,16 @@ def run_stage(ctx, stage: int, x, stream=None):
 # passed the call, and new ones are allocated on it and may be used and freed
 # on the current one; the order of the work on the two is the caller's.
 
+class voc_ops(ctypes.c_void_p):
+    """A handle of the operators and the device that it belongs to."""
+    device = 0
+
+
 def voc_ops_create(device: int = 0):
     """Returns (status, ops)."""
-    ops = ctypes.c_void_p()
+    ops = voc_ops()
     st = lib().voc_ops_create(device, ctypes.byref(ops))
+    ops.device = device
     if st == VOC_OK:
         _use_torch()
     return st, ops
@@ -633,20 +639,30 @@ def _check_ops(st: int, ops) -> None:
         raise VocError(st, voc_ops_last_error(ops))
 
 
-def _rows(what: str, t, shape, dtype) -> int:
-    """Checks a CUDA matrix whose rows are contiguous; returns its row stride."""
-    if t.shape != shape or len(shape) != 2 or t.dtype is not dtype or not t.is_cuda:
+def _elsewhere(what: str, t, device: int):
+    where = f"CUDA device {t.get_device()}" if t.is_cuda else "the CPU"
+    return ValueError(f"{what}: a tensor on the handle's CUDA device {device} is needed, this one is on {where}")
+
+
+def _rows(what: str, t, shape, dtype, device: int) -> int:
+    """Checks a matrix on `device` whose rows are contiguous; returns its row
+    stride."""
+    if t.shape != shape or len(shape) != 2 or t.dtype is not dtype:
         raise ValueError(f"{what}: a CUDA matrix {tuple(shape)} {dtype} is needed, got {tuple(t.shape)} {t.dtype}")
+    if t.get_device() != device:
+        raise _elsewhere(what, t, device)
     step, one = t.stride()
     if one != 1 and shape[1] > 1:
         raise ValueError(f"{what}: rows have to be contiguous")
     return step if shape[0] > 1 else max(step, shape[1])
 
 
-def _vector(what: str, t, n: int) -> int:
-    """Checks n contiguous CUDA float32 values; returns their address."""
-    if t.dtype is not _float32 or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+def _vector(what: str, t, n: int, device: int) -> int:
+    """Checks n contiguous float32 values on `device`; returns their address."""
+    if t.dtype is not _float32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what}: {n} contiguous CUDA float32 values are needed")
+    if t.get_device() != device:
+        raise _elsewhere(what, t, device)
     return t.data_ptr()
 
 
@@ -656,26 +672,27 @@ def rms_norm(ops, x, weight, eps: float = 1e-6, residual=None, h=None, q=None, s
     or residual itself), into a new tensor if that is None and there is a
     residual, and is x itself without one."""
     shape, dtype, device = x.shape, x.dtype, x.device
-    ldx = _rows("x", x, shape, dtype)
+    ldx = _rows("x", x, shape, dtype, ops.device)
     raw, other = _stream_of(stream, x)
     rows, C = shape
     r = hp = None
     ldr = ldh = 0
     if residual is not None:
-        ldr, r = _rows("residual", residual, shape, dtype), residual.data_ptr()
+        ldr, r = _rows("residual", residual, shape, dtype, ops.device), residual.data_ptr()
         if h is None:
             h, ldh = _new(other, shape, dtype, device), C
             hp = h.data_ptr()
     if h is not None and hp is None:
-        ldh, hp = _rows("h", h, shape, dtype), h.data_ptr()
+        ldh, hp = _rows("h", h, shape, dtype, ops.device), h.data_ptr()
     if q is None:
         q, ldq = _new(other, shape, _int8, device), C
     else:
-        ldq = _rows("q", q, shape, _int8)
+        ldq = _rows("q", q, shape, _int8, ops.device)
     if scale is None:
         scale = _new(other, rows, _float32, device)
     st = lib().vocoder_rms_norm(ops, _dtype(dtype), rows, C, x.data_ptr(), ldx, r, ldr, hp, ldh,
-                                _vector("weight", weight, C), eps, q.data_ptr(), ldq, _vector("scale", scale, rows), raw)
+                                _vector("weight", weight, C, ops.device), eps, q.data_ptr(), ldq,
+                                _vector("scale", scale, rows, ops.device), raw)
     if other is not None:
         _keep(other, x, residual, h, weight, q, scale)
     if st:
@@ -687,17 +704,17 @@ def quantize_rows(ops, x, q=None, scale=None, stream=None):
     """(q int8 [rows, C], scale fp32 [rows]) of the rows x [rows, C]
     (vocoder_quantize_rows)."""
     shape, dtype, device = x.shape, x.dtype, x.device
-    ldx = _rows("x", x, shape, dtype)
+    ldx = _rows("x", x, shape, dtype, ops.device)
     raw, other = _stream_of(stream, x)
     rows, C = shape
     if q is None:
         q, ldq = _new(other, shape, _int8, device), C
     else:
-        ldq = _rows("q", q, shape, _int8)
+        ldq = _rows("q", q, shape, _int8, ops.device)
     if scale is None:
         scale = _new(other, rows, _float32, device)
     st = lib().vocoder_quantize_rows(ops, _dtype(dtype), rows, C, x.data_ptr(), ldx, q.data_ptr(), ldq,
-                                     _vector("scale", scale, rows), raw)
+                                     _vector("scale", scale, rows, ops.device), raw)
     if other is not None:
         _keep(other, x, q, scale)
     if st:
@@ -709,10 +726,10 @@ def matmul_int(ops, a, a_scale, b, b_scale, bias=None, gelu: bool = False, dtype
     """act((a b^T) * a_scale[:, None] * b_scale + bias) [M, N] for int8 a
     [M, K] and b [N, K] (vocoder_matmul_int), in `dtype` (default float16) or
     the dtype of `out`."""
-    lda = _rows("a", a, a.shape, _int8)
+    lda = _rows("a", a, a.shape, _int8, ops.device)
     M, K = a.shape
     N = b.shape[0]
-    ldb = _rows("b", b, (N, K), _int8)
+    ldb = _rows("b", b, (N, K), _int8, ops.device)
     raw, other = _stream_of(stream, a)
     if out is None:
         if dtype is None:
@@ -722,10 +739,11 @@ def matmul_int(ops, a, a_scale, b, b_scale, bias=None, gelu: bool = False, dtype
     else:
         if dtype is None:
             dtype = out.dtype
-        ldy = _rows("out", out, (M, N), dtype)
+        ldy = _rows("out", out, (M, N), dtype, ops.device)
     st = lib().vocoder_matmul_int(
-        ops, _dtype(dtype), M, N, K, a.data_ptr(), lda, _vector("a_scale", a_scale, M), b.data_ptr(), ldb,
-        _vector("b_scale", b_scale, N), None if bias is None else _vector("bias", bias, N),
+        ops, _dtype(dtype), M, N, K, a.data_ptr(), lda, _vector("a_scale", a_scale, M, ops.device), b.data_ptr(), ldb,
+        _vector("b_scale", b_scale, N, ops.device),
+        None if bias is None else _vector("bias", bias, N, ops.device),
         VOC_ACT_GELU if gelu else VOC_ACT_NONE, out.data_ptr(), ldy, raw)
     if other is not None:
         _keep(other, a, a_scale, b, b_scale, bias, out)
@@ -759,6 +777,9 @@ class KVCache:
                              (k_scale, (n, h), torch.float32), (v_scale, (n, h), torch.float32)):
             if tuple(t.shape) != shape or t.dtype != dt or not t.is_cuda or not t.is_contiguous():
                 raise ValueError(f"cache: a contiguous CUDA {dt} tensor of shape {shape} is needed")
+            if t.device != k.device:
+                raise ValueError(f"cache: all of its tensors have to be on {k.device}, one is on {t.device}")
+        self.device = k.get_device()
         self.k, self.v, self.k_scale, self.v_scale = self.tensors = k, v, k_scale, v_scale
         self.kv_heads, self.page_tokens, self.head_dim = h, p, d
         self.c = voc_kv_cache(p, h, d, n, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
@@ -777,21 +798,31 @@ class KVBatch:
                                ("starts", starts, (B + 1,))):
             if t.dtype != torch.int32 or not t.is_cuda or tuple(t.shape) != shape or not t.is_contiguous():
                 raise ValueError(f"{what}: a contiguous CUDA int32 tensor of shape {shape} is needed")
+            if t.device != past.device:
+                raise ValueError(f"{what}: the batch's tensors have to be on {past.device}, this one is on {t.device}")
+        self.device = past.get_device()
         self.page_table, self.past, self.starts = self.tensors = page_table, past, starts
         self.c = voc_kv_batch(B, 0, max_new, max_total, starts.data_ptr(), past.data_ptr(), page_table.data_ptr(),
                               page_table.shape[1])
         self.ref = ctypes.byref(self.c)
 
 
-def _heads(what: str, t, shape, dtype):
-    """Checks a CUDA tensor [tokens, heads, dim] with contiguous dim; returns
-    its token and head strides."""
-    if t.shape != shape or len(shape) != 3 or t.dtype is not dtype or not t.is_cuda:
+def _heads(what: str, t, shape, dtype, device: int):
+    """Checks a tensor [tokens, heads, dim] on `device` with contiguous dim;
+    returns its token and head strides."""
+    if t.shape != shape or len(shape) != 3 or t.dtype is not dtype:
         raise ValueError(f"{what}: a CUDA tensor {tuple(shape)} {dtype} is needed, got {tuple(t.shape)} {t.dtype}")
+    if t.get_device() != device:
+        raise _elsewhere(what, t, device)
     step, head, one = t.stride()
     if one != 1:
         raise ValueError(f"{what}: the last dimension has to be contiguous")
     return step, head
+
+
+def _check_devices(ops, cache: KVCache, batch: KVBatch) -> None:
+    if cache.device != ops.device or batch.device != ops.device:
+        raise ValueError(f"the cache is on CUDA device {cache.device}, the batch on {batch.device}, the handle on {ops.device}")
 
 
 def cache_append(ops, cache: KVCache, batch: KVBatch, k, v, stream=None) -> None:
@@ -799,8 +830,9 @@ def cache_append(ops, cache: KVCache, batch: KVBatch, k, v, stream=None) -> None
     (vocoder_cache_append)."""
     dtype, tokens = k.dtype, k.shape[0]
     shape = (tokens, cache.kv_heads, cache.head_dim)
-    kt, kh = _heads("k", k, shape, dtype)
-    vt, vh = _heads("v", v, shape, dtype)
+    kt, kh = _heads("k", k, shape, dtype, ops.device)
+    vt, vh = _heads("v", v, shape, dtype, ops.device)
+    _check_devices(ops, cache, batch)
     batch.c.tokens = tokens
     raw, other = _stream_of(stream, k)
     st = lib().vocoder_cache_append(ops, cache.ref, batch.ref, _dtype(dtype), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
@@ -816,13 +848,14 @@ def cache_attention(ops, cache: KVCache, batch: KVBatch, q, scale: float | None 
     """Attention of q [tokens, heads, head_dim] over the cache
     (vocoder_cache_attention); scale defaults to head_dim ** -0.5."""
     shape, dtype, dim = q.shape, q.dtype, cache.head_dim
-    qt, qh = _heads("q", q, shape, dtype)
+    qt, qh = _heads("q", q, shape, dtype, ops.device)
     if shape[2] != dim:
         raise ValueError(f"q: head_dim {dim} is needed, got {shape[2]}")
     raw, other = _stream_of(stream, q)
     if out is None:
         out = _new(other, shape, dtype, q.device)
-    ot, oh = _heads("out", out, shape, dtype)
+    ot, oh = _heads("out", out, shape, dtype, ops.device)
+    _check_devices(ops, cache, batch)
     batch.c.tokens = shape[0]
     st = lib().vocoder_cache_attention(ops, cache.ref, batch.ref, _dtype(dtype), shape[1], q.data_ptr(), qt, qh,
                                        dim ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(), ot, oh,
