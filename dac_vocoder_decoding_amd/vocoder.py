@@ -789,7 +789,8 @@ class KVCache:
 class KVBatch:
     """The sequences of one step (voc_kv_batch): page_table int32 [B, pages],
     past int32 [B], starts int32 [B + 1], and the host's bounds max_new (new
-    tokens of a sequence) and max_total (past + new)."""
+    tokens of a sequence) and max_total (past + new).  Calls leave it as it
+    is, so that threads with handles of their own may share one."""
 
     def __init__(self, page_table, past, starts, max_new: int, max_total: int):
         import torch
@@ -820,6 +821,15 @@ def _heads(what: str, t, shape, dtype, device: int):
     return step, head
 
 
+def _with_tokens(batch: KVBatch, tokens: int) -> voc_kv_batch:
+    """The batch for a call with `tokens` packed rows, a struct of that call's
+    own: in a shared one another thread could change the number between this
+    call's checks and its launch."""
+    c = voc_kv_batch.from_buffer_copy(batch.c)
+    c.tokens = tokens
+    return c
+
+
 def _check_devices(ops, cache: KVCache, batch: KVBatch) -> None:
     if cache.device != ops.device or batch.device != ops.device:
         raise ValueError(f"the cache is on CUDA device {cache.device}, the batch on {batch.device}, the handle on {ops.device}")
@@ -833,9 +843,9 @@ def cache_append(ops, cache: KVCache, batch: KVBatch, k, v, stream=None) -> None
     kt, kh = _heads("k", k, shape, dtype, ops.device)
     vt, vh = _heads("v", v, shape, dtype, ops.device)
     _check_devices(ops, cache, batch)
-    batch.c.tokens = tokens
+    c = _with_tokens(batch, tokens)
     raw, other = _stream_of(stream, k)
-    st = lib().vocoder_cache_append(ops, cache.ref, batch.ref, _dtype(dtype), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+    st = lib().vocoder_cache_append(ops, cache.ref, ctypes.byref(c), _dtype(dtype), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
                                     raw)
     if other is not None:
         _keep(other, k, v, *cache.tensors, *batch.tensors)
@@ -856,8 +866,8 @@ def cache_attention(ops, cache: KVCache, batch: KVBatch, q, scale: float | None 
         out = _new(other, shape, dtype, q.device)
     ot, oh = _heads("out", out, shape, dtype, ops.device)
     _check_devices(ops, cache, batch)
-    batch.c.tokens = shape[0]
-    st = lib().vocoder_cache_attention(ops, cache.ref, batch.ref, _dtype(dtype), shape[1], q.data_ptr(), qt, qh,
+    c = _with_tokens(batch, shape[0])
+    st = lib().vocoder_cache_attention(ops, cache.ref, ctypes.byref(c), _dtype(dtype), shape[1], q.data_ptr(), qt, qh,
                                        dim ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(), ot, oh,
                                        raw)
     if other is not None:

@@ -113,3 +113,42 @@ def test_parts_of_a_cache_and_a_batch_are_on_one_device():
                                T(1, (4, 2), torch.float32))
     with pytest.raises(ValueError):
         V.KVBatch(T(1, (1, 4), torch.int32), T(0, (1,), torch.int32), T(0, (2,), torch.int32), 3, 3)
+
+
+@pytest.mark.parametrize("outer,inner", [("append", "attention"), ("attention", "append"), ("append", "append"),
+                                         ("attention", "attention")])
+def test_threads_may_share_a_batch(monkeypatch, outer, inner):
+    """A call that another thread's call on the same batch overtakes, after its
+    checks and before the library reads its arguments, keeps its own count of
+    packed rows: the kernels take that count for the bound of its tensors."""
+    import threading
+
+    import torch
+    V._use_torch()
+    monkeypatch.setattr(V, "_raw_stream", lambda device: 0)
+    cache = V.KVCache.from_tensors(OnGpu(0, (4, 2, 16, 32), torch.int8), OnGpu(0, (4, 2, 32, 16), torch.int8),
+                                   OnGpu(0, (4, 2), torch.float32), OnGpu(0, (4, 2), torch.float32))
+    batch = V.KVBatch(OnGpu(0, (1, 4), torch.int32), OnGpu(0, (1,), torch.int32), OnGpu(0, (2,), torch.int32), 9, 9)
+    seen = {}
+
+    def call(which, tokens):
+        x = OnGpu(0, (tokens, 2, 32), torch.float32)
+        if which == "append":
+            V.cache_append(V.voc_ops(1), cache, batch, x, x)
+        else:
+            V.cache_attention(V.voc_ops(1), cache, batch, x, out=x)
+
+    class Library:
+        def __getattr__(self, name):
+            def entry(ops, cache, ref, *args):
+                if threading.current_thread() is threading.main_thread():
+                    other = threading.Thread(target=call, args=(inner, 3))
+                    other.start()
+                    other.join()
+                seen[threading.current_thread() is threading.main_thread()] = ref._obj.tokens
+                return 0
+            return entry
+
+    monkeypatch.setattr(V, "lib", Library)
+    call(outer, 7)
+    assert seen == {True: 7, False: 3}
