@@ -96,3 +96,79 @@ def test_front_ahead_of_the_stream_decoder():
         torch.cuda.synchronize()
         V.vocoder_destroy(ctx)
         front.close()
+
+
+def biased(shape, seed, device="cuda"):
+    """Weights whose biases matter."""
+    w = F.make_weights(shape, seed, device)
+    for i in range(shape.layers):
+        w[f"layers.{i}.up_bias"] *= 50                      # spread 0.5
+    return w
+
+
+# A row of normal values whose largest is 4 of its standard deviations is held
+# in steps of 4 / 127, an rms error of 0.9 % of its size.  Eight such roundings
+# a layer and the output's, independent of each other: sqrt(17) 0.9 % = 3.7 %.
+BOUND = 0.04
+
+
+@pytest.mark.parametrize("steps", [[40], [1] * 12 + [28], [7, 1, 32]])
+def test_front_within_its_roundings(steps):
+    """The stage against the plain model within the size of its roundings, and
+    models with a planted mistake at least twice as far off."""
+    w = biased(SHAPE, 5)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    frames = torch.randn(3, SHAPE.channels, 40, generator=g, device="cuda")
+    ref = plain(SHAPE, w, frames)
+
+    def off(x):
+        return ((x.double() - ref).norm() / ref.norm()).item()
+
+    import dataclasses
+    change = dataclasses.replace
+    none = {k: v * (0 if "bias" in k else 1) for k, v in w.items()}
+    swapped = {k: w[k.replace("norm1", "norm2") if "norm1" in k else k.replace("norm2", "norm1")] if "norm" in k and "layers" in k
+               else v for k, v in w.items()}
+    mistakes = {"window + 1": plain(change(SHAPE, window=10), w, frames), "window - 1": plain(change(SHAPE, window=8), w, frames),
+                "no bias": plain(SHAPE, none, frames), "one layer": plain(change(SHAPE, layers=1), w, frames),
+                "rotation": plain(change(SHAPE, rotary_base=100.0), w, frames), "norms": plain(SHAPE, swapped, frames)}
+    for name, x in mistakes.items():
+        assert off(x) > 2 * BOUND, (name, off(x))
+    front = F.Front(SHAPE, w, rows=3, max_frames=40)
+    try:
+        out, at = [], 0
+        for t in steps:
+            out.append(front.step(frames[:, :, at:at + t].contiguous()))
+            at += t
+        err = off(torch.cat(out, 2))
+        print(f"steps {steps[:3]}..: relative error {err:.4f}")
+        assert err <= BOUND, err
+    finally:
+        torch.cuda.synchronize()
+        front.close()
+
+
+def test_front_and_decoder_make_the_decoded_clip():
+    """Chunks through the stage and the stream decoder: the latent within the
+    stage's roundings, the samples those of one decode of that latent."""
+    cfg = I.config(7, batch=2, frames=12)
+    shape = F.Shape(channels=cfg["latent_channels"], layers=1, window=5)
+    w = biased(shape, 1)
+    front = F.Front(shape, w, rows=2, max_frames=12)
+    ctx = V.open_context(cfg, I.make_weights(cfg, twin=True))
+    try:
+        V.check(V.vocoder_stream_reset(ctx, 2), ctx)
+        frames = torch.from_numpy(I.make_latent(cfg, batch=2, frames=12)).cuda()
+        latent, pcm = [], []
+        for k, t in ((0, 5), (5, 1), (6, 6)):
+            latent.append(front.step(frames[:, :, k:k + t].contiguous()))
+            pcm.append(V.stream_decode(ctx, latent[-1]))
+        latent, pcm = torch.cat(latent, 2), torch.cat(pcm, 2)
+        ref = plain(shape, w, frames)
+        assert ((latent.double() - ref).norm() / ref.norm()).item() <= BOUND
+        assert torch.equal(pcm, V.decode(ctx, latent.contiguous()))
+    finally:
+        torch.cuda.synchronize()
+        V.vocoder_destroy(ctx)
+        front.close()

@@ -1322,3 +1322,30 @@ def test_explicit_stream_keeps_memory(ops, name, raw):
     for got, right in zip(y, want):
         assert torch.equal(got, right)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("step", [1, 7, 9, 50])
+def test_append_then_attend_step_by_step(ops, dtype, step):
+    """Two sequences of 50 tokens in steps: after every append the cache holds
+    what the formulas make of the cache before it, bit for bit, and every output
+    is the attention over just that cache."""
+    g = gen(83 + step)
+    P, H, D, n = 16, 2, 64, 50
+    table, pages = table_for(g, [4, 4])
+    cache = V.KVCache(pages, P, H, D)
+    q, k, v = (randn(g, 2, n, H, D, dtype=dtype) for _ in range(3))
+    for t in range(0, n, step):
+        m = min(step, n - t)
+        past, new = [t, t], [m, m]
+        rows = [x[:, t:t + m].reshape(2 * m, H, D) for x in (q, k, v)]
+        want = appended(cache, table, past, new, rows[1], rows[2])
+        b = batch_of(table, past, new)
+        V.cache_append(ops, cache, b, rows[1], rows[2])
+        assert torch.equal(cache.k_scale.cpu(), want[1]) and torch.equal(cache.v_scale.cpu(), want[3])
+        for s in range(2):
+            for c in range(-(-(t + m) // P)):
+                page, live = int(table[s, c]), min(P, t + m - c * P)
+                assert torch.equal(cache.k[page, :, :live].cpu().float(), want[0][page, :, :live])
+                assert torch.equal(cache.v[page, :, :, :live].transpose(1, 2).cpu().float(), want[2][page, :, :live])
+        close(V.cache_attention(ops, cache, b, rows[0]), *attend64(cache, table, past, new, rows[0], 0.125, True, 0))
