@@ -192,12 +192,11 @@ __device__ __forceinline__ float follow_maximum(const f32x4 (&st)[4], float sc, 
 // The probabilities of those keys as operands of the second product, in NP fp16
 // terms.  Two hold about 22 bits; one rounds each to 11, which against 64 bits
 // costs (RMS of the output's, one term / two / the output's own rounding alone)
-// fp16 2.85e-4 / 2.07e-4 / 2.07e-4, bf16 1.67e-3 / 1.67e-3 / 1.66e-3.  Hence two
-// for fp32, one for bf16, and for fp16 two where rows are few and the second is
-// nearly free (us, one / two: 4 x 65536 keys of 8 x 128 d 89.1 / 90.0, 32 x 2000
-// 30.5 / 30.7, 32 x 25 rows of window 72 9.8 / 9.9), one where they are many (2
-// prompts of 5168 440 / 567, 32 of 250 x 16 x 64 30.4 / 33.9, 2 x 2000 x 16 x 256
-// 112 / 132).
+// fp16 2.85e-4 / 2.07e-4 / 2.07e-4, bf16 1.67e-3 / 1.66e-3 / 1.66e-3.  Hence two
+// where rows are few, which wait for memory (us, one / two, bf16: 4 x 65536 keys
+// of 8 x 128 d 89.5 / 90.4, 32 x 2000 30.6 / 31.2, 32 x 25 rows of window 72
+// 10.3 / 10.5), and for fp32; one for 16 bits where rows are many (2 prompts of
+// 5168 440 / 567, 32 of 250 x 16 x 64 30.4 / 33.9, 2 x 2000 x 16 x 256 112 / 132).
 template <int NP>
 __device__ __forceinline__ void probabilities(const f32x4 (&st)[4], float sc, float vf, RowState& r, f16x8 (&pf)[NP][2]) {
   // A row that has seen nothing yet has only -inf here: any finite m will do.
@@ -239,8 +238,7 @@ template <int T, int DC>
 __global__ __launch_bounds__(256, few_waves(T, DC)) void attend_few_kernel(const AttendArgs a, int tiles, int parts) {
   typedef typename Elem<T>::type E;
   constexpr int D = DC * 32, NC = DC / 2, REM = DC & 1;
-  constexpr int NT = T == EL_F32 ? 2 : 1;
-  constexpr int NP = T == EL_BF16 ? 1 : 2;
+  constexpr int NT = T == EL_F32 ? 2 : 1, NP = 2;
   constexpr int PITCH = D + 4;
   __shared__ float s_o[kFewRows * PITCH];
   __shared__ float s_m[4][kFewRows], s_l[4][kFewRows];

@@ -617,11 +617,11 @@ voc_status vocoder_cache_append(voc_ops *ops, const voc_kv_cache *cache, const v
  * queries enter exactly (each row scaled by a power of two; what lies 2^24
  * below a row's largest value may round), fp32 queries as two fp16 terms,
  * which hold about 22 bits.  The probabilities enter as two such terms for
- * fp32, and for fp16 where a sequence and cache head have few query rows
- * (always up to 80); else, and for bf16, as one.  A probability enters with
- * its page's value scale; what lies below 2^-35 of the row's largest such
- * product rounds away, whatever the scales of the pages.  Scores, softmax
- * statistics and sums are fp32.
+ * fp32, and wherever a sequence and cache head have few query rows (always
+ * up to 80); else as one.  A probability enters with its page's value scale;
+ * what lies below 2^-35 of the row's largest such product rounds away,
+ * whatever the scales of the pages.  Scores, softmax statistics and sums are
+ * fp32.
  * Results do not depend on what else runs; long caches are split over
  * workgroups and the parts joined in a fixed order.
  * q and o need 16-byte alignment and strides of 16-byte multiples.

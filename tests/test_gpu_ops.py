@@ -945,16 +945,17 @@ def test_attention_of_very_large_scores(ops, dtype, P, H, D, past, new, causal):
     assert ((o.double() - want).abs() <= (U[dtype] + 2.0 ** -20 + (0 if dtype == F32 else 2.0 ** -11)) * want.abs()).all()
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("P,H,D,group,past,new,causal,window", [
     (32, 16, 64, 1, [250, 171, 33], [1, 1, 1], True, 0), (16, 4, 64, 1, [689, 500], [25, 19], True, 72),
     (64, 2, 128, 4, [8000, 900], [1, 1], True, 0), (16, 1, 96, 4, [100], [20], False, 0),
     (32, 2, 256, 1, [60], [80], True, 0)])
-def test_attention_fp16_of_few_rows_is_rounded_once(ops, P, H, D, group, past, new, causal, window):
-    """Up to 80 query rows a cache head: the probabilities of fp16 queries hold
-    two fp16 terms, so that the output's own rounding is nearly all of the error."""
+def test_attention_of_few_rows_is_rounded_once(ops, dtype, P, H, D, group, past, new, causal, window):
+    """Up to 80 query rows a cache head: the probabilities hold two fp16 terms,
+    so that the output's own rounding is nearly all of the error."""
     g = gen(93 + D)
     cache, table = filled(g, P, H, D, past, new)
-    q = randn(g, sum(new), H * group, D, dtype=F16)
+    q = randn(g, sum(new), H * group, D, dtype=dtype)
     o = V.cache_attention(ops, cache, batch_of(table, past, new), q, causal=causal, window=window)
     ref, tol = attend64_by_keys(cache, table, past, new, q, D ** -0.5, causal, window, two=True)
     worst = ((o.double() - ref).abs() / tol).max().item()
