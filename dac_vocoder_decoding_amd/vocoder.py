@@ -588,12 +588,10 @@ def _use_torch() -> None:
 
 
 def _stream_of(stream, t):
-    """The address of `stream` (of the current stream of t's device if that is
-    None), and the stream itself if it is not the current one."""
+    """The address of `stream`, and the stream itself if it is not the current
+    one of t's device."""
     device = t.get_device()
     here = _raw_stream(device)
-    if stream is None:
-        return here, None
     raw = stream if isinstance(stream, int) else stream.cuda_stream
     if raw == here:
         return raw, None
@@ -671,28 +669,28 @@ def rms_norm(ops, x, weight, eps: float = 1e-6, residual=None, h=None, q=None, s
     (vocoder_rms_norm).  h = x + residual is stored into `h` (which may be x
     or residual itself), into a new tensor if that is None and there is a
     residual, and is x itself without one."""
-    shape, dtype, device = x.shape, x.dtype, x.device
-    ldx = _rows("x", x, shape, dtype, ops.device)
-    raw, other = _stream_of(stream, x)
+    shape, dtype, device, at = x.shape, x.dtype, x.device, ops.device
+    ldx = _rows("x", x, shape, dtype, at)
+    raw, other = (_raw_stream(at), None) if stream is None else _stream_of(stream, x)
     rows, C = shape
     r = hp = None
     ldr = ldh = 0
     if residual is not None:
-        ldr, r = _rows("residual", residual, shape, dtype, ops.device), residual.data_ptr()
+        ldr, r = _rows("residual", residual, shape, dtype, at), residual.data_ptr()
         if h is None:
             h, ldh = _new(other, shape, dtype, device), C
             hp = h.data_ptr()
     if h is not None and hp is None:
-        ldh, hp = _rows("h", h, shape, dtype, ops.device), h.data_ptr()
+        ldh, hp = _rows("h", h, shape, dtype, at), h.data_ptr()
     if q is None:
         q, ldq = _new(other, shape, _int8, device), C
     else:
-        ldq = _rows("q", q, shape, _int8, ops.device)
+        ldq = _rows("q", q, shape, _int8, at)
     if scale is None:
         scale = _new(other, rows, _float32, device)
     st = lib().vocoder_rms_norm(ops, _dtype(dtype), rows, C, x.data_ptr(), ldx, r, ldr, hp, ldh,
-                                _vector("weight", weight, C, ops.device), eps, q.data_ptr(), ldq,
-                                _vector("scale", scale, rows, ops.device), raw)
+                                _vector("weight", weight, C, at), eps, q.data_ptr(), ldq,
+                                _vector("scale", scale, rows, at), raw)
     if other is not None:
         _keep(other, x, residual, h, weight, q, scale)
     if st:
@@ -703,18 +701,18 @@ def rms_norm(ops, x, weight, eps: float = 1e-6, residual=None, h=None, q=None, s
 def quantize_rows(ops, x, q=None, scale=None, stream=None):
     """(q int8 [rows, C], scale fp32 [rows]) of the rows x [rows, C]
     (vocoder_quantize_rows)."""
-    shape, dtype, device = x.shape, x.dtype, x.device
-    ldx = _rows("x", x, shape, dtype, ops.device)
-    raw, other = _stream_of(stream, x)
+    shape, dtype, device, at = x.shape, x.dtype, x.device, ops.device
+    ldx = _rows("x", x, shape, dtype, at)
+    raw, other = (_raw_stream(at), None) if stream is None else _stream_of(stream, x)
     rows, C = shape
     if q is None:
         q, ldq = _new(other, shape, _int8, device), C
     else:
-        ldq = _rows("q", q, shape, _int8, ops.device)
+        ldq = _rows("q", q, shape, _int8, at)
     if scale is None:
         scale = _new(other, rows, _float32, device)
     st = lib().vocoder_quantize_rows(ops, _dtype(dtype), rows, C, x.data_ptr(), ldx, q.data_ptr(), ldq,
-                                     _vector("scale", scale, rows, ops.device), raw)
+                                     _vector("scale", scale, rows, at), raw)
     if other is not None:
         _keep(other, x, q, scale)
     if st:
@@ -726,11 +724,12 @@ def matmul_int(ops, a, a_scale, b, b_scale, bias=None, gelu: bool = False, dtype
     """act((a b^T) * a_scale[:, None] * b_scale + bias) [M, N] for int8 a
     [M, K] and b [N, K] (vocoder_matmul_int), in `dtype` (default float16) or
     the dtype of `out`."""
-    lda = _rows("a", a, a.shape, _int8, ops.device)
+    at = ops.device
+    lda = _rows("a", a, a.shape, _int8, at)
     M, K = a.shape
     N = b.shape[0]
-    ldb = _rows("b", b, (N, K), _int8, ops.device)
-    raw, other = _stream_of(stream, a)
+    ldb = _rows("b", b, (N, K), _int8, at)
+    raw, other = (_raw_stream(at), None) if stream is None else _stream_of(stream, a)
     if out is None:
         if dtype is None:
             import torch
@@ -739,11 +738,11 @@ def matmul_int(ops, a, a_scale, b, b_scale, bias=None, gelu: bool = False, dtype
     else:
         if dtype is None:
             dtype = out.dtype
-        ldy = _rows("out", out, (M, N), dtype, ops.device)
+        ldy = _rows("out", out, (M, N), dtype, at)
     st = lib().vocoder_matmul_int(
-        ops, _dtype(dtype), M, N, K, a.data_ptr(), lda, _vector("a_scale", a_scale, M, ops.device), b.data_ptr(), ldb,
-        _vector("b_scale", b_scale, N, ops.device),
-        None if bias is None else _vector("bias", bias, N, ops.device),
+        ops, _dtype(dtype), M, N, K, a.data_ptr(), lda, _vector("a_scale", a_scale, M, at), b.data_ptr(), ldb,
+        _vector("b_scale", b_scale, N, at),
+        None if bias is None else _vector("bias", bias, N, at),
         VOC_ACT_GELU if gelu else VOC_ACT_NONE, out.data_ptr(), ldy, raw)
     if other is not None:
         _keep(other, a, a_scale, b, b_scale, bias, out)
@@ -830,21 +829,21 @@ def _with_tokens(batch: KVBatch, tokens: int) -> voc_kv_batch:
     return c
 
 
-def _check_devices(ops, cache: KVCache, batch: KVBatch) -> None:
-    if cache.device != ops.device or batch.device != ops.device:
-        raise ValueError(f"the cache is on CUDA device {cache.device}, the batch on {batch.device}, the handle on {ops.device}")
+def _apart(ops, cache: KVCache, batch: KVBatch):
+    return ValueError(f"the cache is on CUDA device {cache.device}, the batch on {batch.device}, the handle on {ops.device}")
 
 
 def cache_append(ops, cache: KVCache, batch: KVBatch, k, v, stream=None) -> None:
     """Append k and v [tokens, kv_heads, head_dim] to the cache
     (vocoder_cache_append)."""
-    dtype, tokens = k.dtype, k.shape[0]
+    dtype, tokens, device = k.dtype, k.shape[0], ops.device
     shape = (tokens, cache.kv_heads, cache.head_dim)
-    kt, kh = _heads("k", k, shape, dtype, ops.device)
-    vt, vh = _heads("v", v, shape, dtype, ops.device)
-    _check_devices(ops, cache, batch)
+    kt, kh = _heads("k", k, shape, dtype, device)
+    vt, vh = _heads("v", v, shape, dtype, device)
+    if not device == cache.device == batch.device:
+        raise _apart(ops, cache, batch)
     c = _with_tokens(batch, tokens)
-    raw, other = _stream_of(stream, k)
+    raw, other = (_raw_stream(device), None) if stream is None else _stream_of(stream, k)
     st = lib().vocoder_cache_append(ops, cache.ref, ctypes.byref(c), _dtype(dtype), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
                                     raw)
     if other is not None:
@@ -857,15 +856,16 @@ def cache_attention(ops, cache: KVCache, batch: KVBatch, q, scale: float | None 
                     window: int = 0, out=None, stream=None):
     """Attention of q [tokens, heads, head_dim] over the cache
     (vocoder_cache_attention); scale defaults to head_dim ** -0.5."""
-    shape, dtype, dim = q.shape, q.dtype, cache.head_dim
-    qt, qh = _heads("q", q, shape, dtype, ops.device)
+    shape, dtype, dim, device = q.shape, q.dtype, cache.head_dim, ops.device
+    qt, qh = _heads("q", q, shape, dtype, device)
     if shape[2] != dim:
         raise ValueError(f"q: head_dim {dim} is needed, got {shape[2]}")
-    raw, other = _stream_of(stream, q)
+    raw, other = (_raw_stream(device), None) if stream is None else _stream_of(stream, q)
     if out is None:
         out = _new(other, shape, dtype, q.device)
-    ot, oh = _heads("out", out, shape, dtype, ops.device)
-    _check_devices(ops, cache, batch)
+    ot, oh = _heads("out", out, shape, dtype, device)
+    if not device == cache.device == batch.device:
+        raise _apart(ops, cache, batch)
     c = _with_tokens(batch, shape[0])
     st = lib().vocoder_cache_attention(ops, cache.ref, ctypes.byref(c), _dtype(dtype), shape[1], q.data_ptr(), qt, qh,
                                        dim ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(), ot, oh,
