@@ -192,8 +192,9 @@ __device__ __forceinline__ float follow_maximum(const f32x4 (&st)[4], float sc, 
 // The probabilities of those keys as operands of the second product, in NP fp16
 // terms.  Two hold about 22 bits; one rounds each to 11, which against 64 bits
 // costs (RMS of the output's, one term / two / the output's own rounding alone)
-// fp16 2.85e-4 / 2.07e-4 / 2.07e-4, bf16 1.67e-3 / 1.66e-3 / 1.66e-3.  Hence two
-// where rows are few, which wait for memory (us, one / two, bf16: 4 x 65536 keys
+// fp16 2.85e-4 / 2.07e-4 / 2.07e-4, bf16 1.67e-3 / 1.66e-3 / 1.66e-3; of the
+// outputs 38 % / 0.1 % (fp16) and 9 % / 0.02 % are not the nearest value.  Hence
+// two where rows are few, which wait for memory (us, one / two, bf16: 4 x 65536 keys
 // of 8 x 128 d 89.5 / 90.4, 32 x 2000 30.6 / 31.2, 32 x 25 rows of window 72
 // 10.3 / 10.5), and for fp32; one for 16 bits where rows are many (2 prompts of
 // 5168 440 / 567, 32 of 250 x 16 x 64 30.4 / 33.9, 2 x 2000 x 16 x 256 112 / 132).
@@ -228,9 +229,9 @@ __device__ __forceinline__ void probabilities(const f32x4 (&st)[4], float sc, fl
 // 14.3 us for 7.9 + 5.2; with a write-back of the L2 19.2.)
 // Every key and value is read once, from memory to registers, so a long cache
 // is bound by memory: one token of 4 x 32 / 8 heads x 128 d over 65536 tokens,
-// 409 MB, 74 us (5.5 TB/s) and 5 for the join.  Short ones are bound by latency
-// (sequence, page, codes, joins): 32 x 16 x 64 over 250 tokens 7.7 us; 25 rows
-// each over a window of 72 10.4.
+// 409 MB, 76 us (5.4 TB/s) and 5 for the join.  Short ones are bound by latency
+// (sequence, page, codes, joins): 32 x 16 x 64 over 250 tokens 8.4 us; 25 rows
+// each over a window of 72 10.9.
 constexpr int kFewRows = 16;
 constexpr int few_waves(int t, int dc) { return t == EL_F32 ? (dc <= 2 ? 3 : dc <= 4 ? 2 : 1) : dc <= 2 ? 4 : dc <= 4 ? 3 : dc <= 6 ? 2 : 1; }
 
@@ -412,12 +413,13 @@ __device__ __forceinline__ void read_ahead() {
 // 4 g + i, d 32 c .., value fragment (i, h): d 16 i .., keys 16 g + 8 h ...
 // A wave's copies take 64 bytes of each of 16 rows, which spreads its writes
 // over all banks.
-// Two prompts of 5168, 32 / 8 heads x 128 d, causal (386 G operations): 467 us,
-// 0.83 P operations a second (548 in a profiled run); a large fp16 library
-// product reaches 1.32.  The matrix cores are busy 37 % of the cycles
-// and the vector units about 54 % (155 instructions for 1024 scores of a wave,
+// Two prompts of 5168, 32 / 8 heads x 128 d, causal (386 G operations): 455 us,
+// 0.85 P operations a second (539 in a profiled run); a large fp16 library
+// product reaches 1.32.  The matrix cores are busy 38 % of the cycles
+// and the vector units about half (146 instructions for 1024 scores of a wave,
 // conversion included): a SIMD's two waves seldom do the one while the other
-// does the other.  Not kept: scores a block ahead of the products 710 (630
+// does the other.  fp32 queries, with two terms in both products, take 832.
+// Not kept, of an earlier form: scores a block ahead of the products 710 (630
 // then), two groups of waves a phase apart 523 to 677 (499), wave priorities
 // 553 to 581, the value scale inside the exponent 553 (550), 64 rows a wave
 // 1269 (spills).

@@ -100,7 +100,7 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendArgs a) {
 // Many new tokens, rows of 16-byte multiples.  The page's image is built in
 // LDS and written whole, 16 bytes at a time: a value page is turned over
 // there, four tokens of one d to a 32-bit word.  The new rows stay in
-// registers between the maximum and the codes where a thread has up to four
+// registers between the maximum and the codes where a thread has up to two
 // units (4 tokens x 8 values); larger pages read the rest a second time.
 // Bound by memory and by each page's chain of loads: 8 prompts of up to 5168
 // bf16 tokens of 8 x 128 d (217 MB) 58 us, 3.7 TB/s.  (Pages in the order of

@@ -404,7 +404,8 @@ static void go_few(const IntMatmulArgs& a, hipStream_t s, Form& form) {
   auto rows = [&](int mb) { return static_cast<unsigned>((a.M + 16 * mb - 1) / (16 * mb)); };
   // As many tokens a workgroup as leave about one to each CU (us, 64 x 1024 x
   // 4096 with 4 / 2 / 1 blocks of 16: 11.3 / 7.7 / 7.3, 64 x 2048 x 4096 11.7 /
-  // 8.1, 64 x 3500 x 2048 7.3 / 8.4, 32 x 4096 x 1024 4.2 with 2, 4.6 with 1).
+  // 8.1, 32 x 4096 x 1024 4.2 with 2, 4.6 with 1; 64 x 3500 x 2048, whose rows
+  // come here where they are not 16-byte aligned, 7.3 / 8.4).
   const int blocks = a.M > 32 && gx * rows(4) >= 192 ? 4 : a.M > 16 && gx * rows(2) >= 192 ? 2 : 1;
   form = Form{SHIFT ? "product_few_shifted" : "product_few", {16, 16 * blocks}};
   if (blocks == 4)
@@ -438,7 +439,7 @@ static void go_tile(const IntMatmulArgs& a, hipStream_t s, Form& form) {
 //    (500x1024x4096: 12.4 against 15.8) with eight waves (with four half a us
 //    more);
 //  * rows that are not 16-byte aligned go through registers in 64x64 tiles
-//    (689x1000x1501: 11.0; four waves 12.5, 128x64 17.4).
+//    (689x1000x1501: 11.1; four waves 12.5, 128x64 17.4).
 template <int T>
 static void go_int_matmul(const IntMatmulArgs& a, hipStream_t s, Form& form) {
   auto tiles = [&](int f, int t) { return static_cast<int64_t>((a.N + f - 1) / f) * ((a.M + t - 1) / t); };

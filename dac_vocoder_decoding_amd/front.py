@@ -3,10 +3,13 @@
 The codec that the causal decoder belongs to hands its frames through a small
 transformer with a sliding window and a key/value cache first (qwentts.cpp
 ARCHITECTURE page, "Audio tokenizer decoder", "Streaming decode (stateful
-path)").  `Front` is such a stage for many streams at once, on the library's
-8-bit operators: weights and activations as rows of 8-bit codes, the cache in
-8-bit pages.  One step takes the next t frames of every stream and returns
-the latent frames that vocoder_stream_decode takes.
+path)").  `Front` runs a transformer of that kind for many streams at once on
+the library's 8-bit operators: weights and activations as rows of 8-bit codes,
+the cache in 8-bit pages.  One step takes the next t frames of every stream and
+returns the latent frames that vocoder_stream_decode takes.  It is a plain
+decoder-only stack (RMS norms, rotary positions, a GELU widening): a codec's
+own gates, layer scales and upsampler are not in it, and its output is the last
+norm's 8-bit rows.
 
     front = Front(Shape(channels=1024, ...), make_weights(shape, seed), rows=32, max_frames=250)
     latent = front.step(frames)            # [rows, channels, t], t >= 1, any t per step

@@ -486,7 +486,9 @@ voc_status voc_dbg_peak(int what, int64_t n, double *value, void *hip_stream);
  * so that what is computed from it is NaN.  Scales are never negative.
  *
  * Threading: as for voc_ctx, one handle per host thread and stream (the
- * handle owns the workspace in which split attention joins its parts). */
+ * handle owns the workspace in which split attention joins its parts).  The
+ * structs below are only read and may be shared.  All buffers of a call are
+ * on the handle's device. */
 typedef struct voc_ops voc_ops;
 
 /* Create a handle on HIP device hip_device with its workspace (device
