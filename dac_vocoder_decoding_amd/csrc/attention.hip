@@ -41,7 +41,8 @@ __device__ __forceinline__ f16x8 codes_to_f16(uint32_t a, uint32_t b) {
 // The probabilities enter the matrix cores with their value scales, as
 // p * vs * lift with p = 2^(s - m) and lift a power of two that brings the
 // row's largest p * vs to [2^10, 2^11): what weighs most in the output then
-// uses all of an fp16 number, whatever the scales of pages that weigh little.
+// uses all of an fp16 number, whatever the scales (up to 2^100 apart) of pages
+// that weigh little.
 // fp16 reaches 2^-25 below (half its last step), so a key's term is off by at
 // most 2^-35 of the row's largest besides its own rounding.  m follows a score
 // that passes it by more than kSlack (a factor of 8), lift a product past

@@ -66,7 +66,7 @@ __device__ __forceinline__ i32x4 load_codes(const int8_t* row, int k, int K) {
 // this alone is within 3.9 |v| 2^-24 of GELU, most of it near zero, where erfc is
 // 1 less a small number.  fp32 outputs therefore take v / 2 (1 + v R(v^2))
 // up to |v| = sqrt(2), R a minimax polynomial of erf(v / sqrt(2)) / v (relative
-// error 3.1e-8): within 1.8 |v| 2^-24 everywhere (0.5 v (1 + erf) in fp32: 1.8),
+// error 3.1e-8): within 1.7 |v| 2^-24 everywhere (0.5 v (1 + erf) in fp32: 2.0),
 // and for v of spread 0.1 the RMS error is 2.6e-8 of the RMS in place of 1.1e-7.
 // 16-bit outputs, whose rounding hides that, keep erfc alone (us, 4606 x 6848 x
 // 576: fp32 62, with erfc alone 54, without GELU 44; bf16 43).

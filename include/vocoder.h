@@ -621,9 +621,9 @@ voc_status vocoder_cache_append(voc_ops *ops, const voc_kv_cache *cache, const v
  * which hold about 22 bits.  The probabilities enter as two such terms for
  * fp32, and wherever a sequence and cache head have few query rows (always
  * up to 80); else as one.  A probability enters with its page's value scale;
- * what lies below 2^-35 of the row's largest such product rounds away,
- * whatever the scales of the pages.  Scores, softmax statistics and sums are
- * fp32.
+ * what lies below 2^-35 of the row's largest such product rounds away (for
+ * value scales of a row's pages up to 2^100 apart).  Scores, softmax
+ * statistics and sums are fp32.
  * Results do not depend on what else runs; long caches are split over
  * workgroups and the parts joined in a fixed order.
  * q and o need 16-byte alignment and strides of 16-byte multiples.
