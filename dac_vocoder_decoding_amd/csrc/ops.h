@@ -41,8 +41,25 @@ struct IntMatmulArgs {
   int64_t lda, ldb, ldy;
   int M, N, K;
   int act;            // VOC_ACT_*
+  // The adapters' part (adapters.hip): u[m][rank], up 16-bit [adapters][N][rank].
+  const float* u;
+  const uint16_t* up;
+  const int32_t* adapter;  // of each row
+  int adapters, rank;      // rank: a multiple of 16
+  bool up_bf16;            // else fp16
 };
 hipError_t launch_int_matmul(int dtype, const IntMatmulArgs& a, hipStream_t s, Form& form);
+
+// The product with a low-rank term a row: u = scale[i] (down_i a) sa first,
+// then the product, which adds up_i u.
+struct AdaptArgs {
+  IntMatmulArgs g;
+  const uint16_t* down;  // [adapters][rank][ldd]
+  int64_t ldd;
+  const float* scale;    // [adapters] or null
+  float* u;              // [M][rank]
+};
+hipError_t launch_int_matmul_adapters(int dtype, const AdaptArgs& a, hipStream_t s, Form& form);
 
 // The cache and the sequences of one step, as every kernel reads them.
 struct CacheView {
@@ -86,6 +103,51 @@ struct AppendArgs {
   int D, batch;
 };
 hipError_t launch_append(int dtype, const AppendArgs& a, hipStream_t s, Form& form);
+
+// The heads of every token: x and y [token][head][value] (y may be x), w the
+// norm's weights or null (no norm).
+struct HeadSet {
+  const void* x;
+  void* y;
+  const float* w;
+  int64_t x_t, x_h, y_t, y_h;  // element strides
+  int heads;
+};
+struct HeadShape {
+  const float* freq;
+  int D, pairs;  // the first 2 * pairs values rotate
+  int adjacent;  // pairs 2i, 2i + 1; else i, i + pairs
+  float eps;
+};
+constexpr int kHeadMaxD = 256;
+struct NormRotateArgs {
+  HeadShape h;
+  HeadSet q, k;             // k.heads 0: none
+  const int32_t* position;  // of each token; null where nothing rotates
+  int64_t tokens;
+};
+hipError_t launch_norm_rotate(int dtype, const NormRotateArgs& a, hipStream_t s, Form& form);
+
+struct StepArgs {
+  CacheView c;
+  HeadShape h;
+  HeadSet q, k;  // k.y is not used: keys go into the cache
+  const void* v;
+  int64_t v_t, v_h;
+  int batch;
+};
+int64_t step_workgroups(const StepArgs& a);  // of one sequence, at the most
+hipError_t launch_step(int dtype, const StepArgs& a, hipStream_t s, Form& form);
+
+struct ReadArgs {
+  CacheView c;
+  void* k;  // or null
+  void* v;  // or null
+  int64_t k_t, k_h, v_t, v_h;
+  int D, batch;
+};
+int64_t read_workgroups(const ReadArgs& a);  // of one sequence
+hipError_t launch_read(int dtype, const ReadArgs& a, hipStream_t s, Form& form);
 
 struct AttendArgs {
   CacheView c;

@@ -125,6 +125,53 @@ voc_status check_cache(voc_ops* o, const voc_kv_cache* c, const voc_kv_batch* b,
   return VOC_OK;
 }
 
+// The arguments that a product has with and without adapters.
+voc_status check_product(voc_ops* o, int out_dtype, int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t lda,
+                         const float* a_scale, const int8_t* b, int64_t ldb, const float* b_scale, const float* bias,
+                         int act, const void* y, int64_t ldy) {
+  if (!dtype_ok(out_dtype)) return fail(o, VOC_INVALID_PARAMS, "unknown dtype %d", out_dtype);
+  if (act != VOC_ACT_NONE && act != VOC_ACT_GELU) return fail(o, VOC_INVALID_PARAMS, "unknown act %d", act);
+  if (M < 0 || M > (1 << 24) || N < 0 || N > (1 << 24)) return fail(o, VOC_INVALID_PARAMS, "M or N out of range");
+  if (K < 1 || K > 131071) return fail(o, VOC_INVALID_PARAMS, "K must be 1 .. 131071");
+  if (M == 0 || N == 0) return VOC_OK;
+  // A launch holds fewer than 2^32 threads (the smallest tiles: 64 x 64 in 512).
+  if (((M + 63) / 64) * ((N + 63) / 64) >= 1 << 23) return fail(o, VOC_INVALID_PARAMS, "too many outputs for one call");
+  if (!a || !a_scale || !b || !b_scale || !y) return fail(o, VOC_INVALID_PARAMS, "NULL pointer");
+  if (!stride_ok(lda, K) || !stride_ok(ldb, K) || !stride_ok(ldy, N))
+    return fail(o, VOC_INVALID_PARAMS, "row strides must be at least the row's length");
+  if (!aligned(a_scale, 4) || !aligned(b_scale, 4) || !aligned(bias, 4) || !aligned(y, elem_size(out_dtype)))
+    return fail(o, VOC_INVALID_PARAMS, "pointers must be aligned to their elements");
+  return VOC_OK;
+}
+
+constexpr int kMaxHeads = 4096;
+
+voc_status check_heads(voc_ops* o, int dtype, int head_dim, const float* freq, int pairs, int adjacent, float eps,
+                       HeadShape* h) {
+  if (!dtype_ok(dtype)) return fail(o, VOC_INVALID_PARAMS, "unknown dtype %d", dtype);
+  if (head_dim < 1 || head_dim > kHeadMaxD) return fail(o, VOC_INVALID_PARAMS, "head_dim must be 1 .. %d", kHeadMaxD);
+  if (pairs < 0 || 2 * int64_t(pairs) > head_dim) return fail(o, VOC_INVALID_PARAMS, "pairs must be 0 .. head_dim / 2");
+  if (adjacent != 0 && adjacent != 1) return fail(o, VOC_INVALID_PARAMS, "adjacent must be 0 or 1");
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(o, VOC_INVALID_PARAMS, "eps must be finite and not negative");
+  if (pairs && !freq) return fail(o, VOC_INVALID_PARAMS, "freq is NULL");
+  if (!aligned(freq, 4)) return fail(o, VOC_INVALID_PARAMS, "freq must be 4-byte aligned");
+  *h = HeadShape{freq, head_dim, pairs, adjacent, eps};
+  return VOC_OK;
+}
+
+voc_status check_head_set(voc_ops* o, int dtype, int heads, const void* x, int64_t x_t, int64_t x_h, const float* w, void* y,
+                          int64_t y_t, int64_t y_h, HeadSet* set) {
+  *set = HeadSet{};
+  if (heads == 0) return VOC_OK;
+  if (!x || !y) return fail(o, VOC_INVALID_PARAMS, "NULL pointer");
+  if (!aligned(x, elem_size(dtype)) || !aligned(y, elem_size(dtype)) || !aligned(w, 4))
+    return fail(o, VOC_INVALID_PARAMS, "pointers must be aligned to their elements");
+  for (const int64_t s : {x_t, x_h, y_t, y_h})
+    if (!stride_ok(s, 0)) return fail(o, VOC_INVALID_PARAMS, "strides out of range");
+  *set = HeadSet{x, y, w, x_t, x_h, y_t, y_h, heads};
+  return VOC_OK;
+}
+
 }  // namespace
 
 VOC_API voc_status voc_ops_create(int hip_device, voc_ops** out) {
@@ -204,21 +251,138 @@ VOC_API voc_status vocoder_matmul_int(voc_ops* o, int out_dtype, int64_t M, int6
                                       void* hip_stream) {
   if (!o) return VOC_INVALID_PARAMS;
   o->err[0] = 0;
-  if (!dtype_ok(out_dtype)) return fail(o, VOC_INVALID_PARAMS, "unknown dtype %d", out_dtype);
-  if (act != VOC_ACT_NONE && act != VOC_ACT_GELU) return fail(o, VOC_INVALID_PARAMS, "unknown act %d", act);
-  if (M < 0 || M > (1 << 24) || N < 0 || N > (1 << 24)) return fail(o, VOC_INVALID_PARAMS, "M or N out of range");
-  if (K < 1 || K > 131071) return fail(o, VOC_INVALID_PARAMS, "K must be 1 .. 131071");
-  if (M == 0 || N == 0) return VOC_OK;
-  // A launch holds fewer than 2^32 threads (the smallest tiles: 64 x 64 in 512).
-  if (((M + 63) / 64) * ((N + 63) / 64) >= 1 << 23) return fail(o, VOC_INVALID_PARAMS, "too many outputs for one call");
-  if (!a || !a_scale || !b || !b_scale || !y) return fail(o, VOC_INVALID_PARAMS, "NULL pointer");
-  if (!stride_ok(lda, K) || !stride_ok(ldb, K) || !stride_ok(ldy, N))
-    return fail(o, VOC_INVALID_PARAMS, "row strides must be at least the row's length");
-  if (!aligned(a_scale, 4) || !aligned(b_scale, 4) || !aligned(bias, 4) || !aligned(y, elem_size(out_dtype)))
-    return fail(o, VOC_INVALID_PARAMS, "pointers must be aligned to their elements");
+  const voc_status st = check_product(o, out_dtype, M, N, K, a, lda, a_scale, b, ldb, b_scale, bias, act, y, ldy);
+  if (st != VOC_OK || M == 0 || N == 0) return st;
   const IntMatmulArgs g{a, b, a_scale, b_scale, bias, y, lda, ldb, ldy, static_cast<int>(M), static_cast<int>(N),
                         static_cast<int>(K), act};
   return on_device(o, "matmul_int", [&] { return launch_int_matmul(out_dtype, g, static_cast<hipStream_t>(hip_stream), o->form); });
+}
+
+VOC_API voc_status vocoder_matmul_int_adapters(voc_ops* o, int out_dtype, int64_t M, int64_t N, int64_t K, const int8_t* a,
+                                               int64_t lda, const float* a_scale, const int8_t* b, int64_t ldb,
+                                               const float* b_scale, const float* bias, int act,
+                                               const voc_adapters* ad, const int32_t* adapter, void* y, int64_t ldy,
+                                               void* hip_stream) {
+  if (!o) return VOC_INVALID_PARAMS;
+  o->err[0] = 0;
+  const voc_status st = check_product(o, out_dtype, M, N, K, a, lda, a_scale, b, ldb, b_scale, bias, act, y, ldy);
+  if (st != VOC_OK) return st;
+  if (!ad) return fail(o, VOC_INVALID_PARAMS, "adapters is NULL");
+  if (ad->dtype != VOC_F16 && ad->dtype != VOC_BF16) return fail(o, VOC_INVALID_PARAMS, "adapters hold fp16 or bf16");
+  if (ad->count < 1 || ad->count > (1 << 24)) return fail(o, VOC_INVALID_PARAMS, "the number of adapters is out of range");
+  if (ad->rank < 16 || ad->rank > 256 || ad->rank % 16)
+    return fail(o, VOC_INVALID_PARAMS, "the adapters' rank must be a multiple of 16 up to 256");
+  if (!stride_ok(ad->down_stride, K) || ad->down_stride % 8)
+    return fail(o, VOC_INVALID_PARAMS, "down_stride must be a multiple of 8, at least K");
+  if (M == 0 || N == 0) return VOC_OK;
+  if (!ad->down || !ad->up || !adapter) return fail(o, VOC_INVALID_PARAMS, "NULL pointer");
+  if (!aligned(ad->down, 16) || !aligned(ad->up, 16) || !aligned(ad->scale, 4) || !aligned(adapter, 4))
+    return fail(o, VOC_INVALID_PARAMS, "down and up must be 16-byte aligned, scale and adapter 4-byte aligned");
+  AdaptArgs p{};
+  p.g = IntMatmulArgs{a, b, a_scale, b_scale, bias, y, lda, ldb, ldy, static_cast<int>(M), static_cast<int>(N),
+                      static_cast<int>(K), act};
+  p.u = static_cast<float*>(o->ws);
+  p.g.u = p.u;
+  p.g.up = static_cast<const uint16_t*>(ad->up);
+  p.g.adapter = adapter;
+  p.g.adapters = ad->count;
+  p.g.rank = ad->rank;
+  p.g.up_bf16 = ad->dtype == VOC_BF16;
+  p.down = static_cast<const uint16_t*>(ad->down);
+  p.ldd = ad->down_stride;
+  p.scale = ad->scale;
+  // As many rows at a time as the workspace holds u of (at least 131072).
+  const int64_t most = VOC_OPS_WORKSPACE_BYTES / (4 * ad->rank) & ~int64_t(1023);
+  return on_device(o, "matmul_int_adapters", [&] {
+    for (int64_t m = 0; m < M; m += most) {
+      AdaptArgs part = p;
+      part.g.M = static_cast<int>(M - m < most ? M - m : most);
+      part.g.a += m * lda;
+      part.g.sa += m;
+      part.g.adapter += m;
+      part.g.y = static_cast<char*>(y) + m * ldy * elem_size(out_dtype);
+      const hipError_t e = launch_int_matmul_adapters(out_dtype, part, static_cast<hipStream_t>(hip_stream), o->form);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  });
+}
+
+VOC_API voc_status vocoder_norm_rotate(voc_ops* o, int dtype, int64_t tokens, int head_dim, const int32_t* position,
+                                       const float* freq, int pairs, int adjacent, float eps, int heads, const void* q,
+                                       int64_t q_t, int64_t q_h, const float* q_weight, void* q_out, int64_t qo_t,
+                                       int64_t qo_h, int kv_heads, const void* k, int64_t k_t, int64_t k_h,
+                                       const float* k_weight, void* k_out, int64_t ko_t, int64_t ko_h, void* hip_stream) {
+  if (!o) return VOC_INVALID_PARAMS;
+  o->err[0] = 0;
+  NormRotateArgs a{};
+  voc_status st = check_heads(o, dtype, head_dim, freq, pairs, adjacent, eps, &a.h);
+  if (st != VOC_OK) return st;
+  if (tokens < 0 || tokens > (int64_t(1) << 26)) return fail(o, VOC_INVALID_PARAMS, "tokens must be 0 .. 2^26");
+  if (heads < 0 || heads > kMaxHeads || kv_heads < 0 || kv_heads > kMaxHeads)
+    return fail(o, VOC_INVALID_PARAMS, "heads or kv_heads out of range");
+  if (tokens == 0 || heads + kv_heads == 0) return VOC_OK;
+  if (pairs && !position) return fail(o, VOC_INVALID_PARAMS, "position is NULL");
+  if (!aligned(position, 4)) return fail(o, VOC_INVALID_PARAMS, "position must be 4-byte aligned");
+  if ((st = check_head_set(o, dtype, heads, q, q_t, q_h, q_weight, q_out, qo_t, qo_h, &a.q)) != VOC_OK) return st;
+  if ((st = check_head_set(o, dtype, kv_heads, k, k_t, k_h, k_weight, k_out, ko_t, ko_h, &a.k)) != VOC_OK) return st;
+  a.position = position;
+  a.tokens = tokens;
+  return on_device(o, "norm_rotate", [&] { return launch_norm_rotate(dtype, a, static_cast<hipStream_t>(hip_stream), o->form); });
+}
+
+VOC_API voc_status vocoder_norm_rotate_append(voc_ops* o, const voc_kv_cache* cache, const voc_kv_batch* batch, int dtype,
+                                              const float* freq, int pairs, int adjacent, float eps, int heads,
+                                              const void* q, int64_t q_t, int64_t q_h, const float* q_weight,
+                                              void* q_out, int64_t qo_t, int64_t qo_h, const void* k, int64_t k_t,
+                                              int64_t k_h, const float* k_weight, const void* v, int64_t v_t,
+                                              int64_t v_h, void* hip_stream) {
+  if (!o) return VOC_INVALID_PARAMS;
+  o->err[0] = 0;
+  StepArgs a{};
+  voc_status st = check_cache(o, cache, batch, &a.c);
+  if (st != VOC_OK) return st;
+  st = check_heads(o, dtype, cache->head_dim, freq, pairs, adjacent, eps, &a.h);
+  if (st != VOC_OK) return st;
+  if (heads < 0 || heads > kMaxHeads) return fail(o, VOC_INVALID_PARAMS, "heads out of range");
+  if (batch->batch == 0 || batch->tokens == 0 || batch->max_new == 0) return VOC_OK;
+  if ((st = check_head_set(o, dtype, heads, q, q_t, q_h, q_weight, q_out, qo_t, qo_h, &a.q)) != VOC_OK) return st;
+  // (The keys' outputs are the cache's own.)
+  if ((st = check_head_set(o, dtype, cache->kv_heads, k, k_t, k_h, k_weight, cache->k, 0, 0, &a.k)) != VOC_OK) return st;
+  if (!v) return fail(o, VOC_INVALID_PARAMS, "NULL pointer");
+  if (!aligned(v, elem_size(dtype))) return fail(o, VOC_INVALID_PARAMS, "pointers must be aligned to their elements");
+  if (!stride_ok(v_t, 0) || !stride_ok(v_h, 0)) return fail(o, VOC_INVALID_PARAMS, "strides out of range");
+  a.v = v;
+  a.v_t = v_t;
+  a.v_h = v_h;
+  a.batch = static_cast<int>(batch->batch);
+  if (step_workgroups(a) * a.batch >= 1 << 24) return fail(o, VOC_INVALID_PARAMS, "too many tokens for one call");
+  return on_device(o, "norm_rotate_append", [&] { return launch_step(dtype, a, static_cast<hipStream_t>(hip_stream), o->form); });
+}
+
+VOC_API voc_status vocoder_cache_read(voc_ops* o, const voc_kv_cache* cache, const voc_kv_batch* batch, int dtype, void* k,
+                                      int64_t k_t, int64_t k_h, void* v, int64_t v_t, int64_t v_h, void* hip_stream) {
+  if (!o) return VOC_INVALID_PARAMS;
+  o->err[0] = 0;
+  ReadArgs a{};
+  voc_status st = check_cache(o, cache, batch, &a.c);
+  if (st != VOC_OK) return st;
+  if (!dtype_ok(dtype)) return fail(o, VOC_INVALID_PARAMS, "unknown dtype %d", dtype);
+  if (batch->batch == 0 || batch->tokens == 0 || batch->max_new == 0 || (!k && !v)) return VOC_OK;
+  if (!aligned(k, elem_size(dtype)) || !aligned(v, elem_size(dtype)))
+    return fail(o, VOC_INVALID_PARAMS, "pointers must be aligned to their elements");
+  for (const int64_t s : {k ? k_t : 0, k ? k_h : 0, v ? v_t : 0, v ? v_h : 0})
+    if (!stride_ok(s, 0)) return fail(o, VOC_INVALID_PARAMS, "strides out of range");
+  a.k = k;
+  a.v = v;
+  a.k_t = k ? k_t : 0;
+  a.k_h = k ? k_h : 0;
+  a.v_t = v ? v_t : 0;
+  a.v_h = v ? v_h : 0;
+  a.D = cache->head_dim;
+  a.batch = static_cast<int>(batch->batch);
+  if (read_workgroups(a) * a.batch >= 1 << 24) return fail(o, VOC_INVALID_PARAMS, "too many tokens for one call");
+  return on_device(o, "cache_read", [&] { return launch_read(dtype, a, static_cast<hipStream_t>(hip_stream), o->form); });
 }
 
 VOC_API voc_status vocoder_cache_append(voc_ops* o, const voc_kv_cache* cache, const voc_kv_batch* batch, int dtype,

@@ -94,6 +94,18 @@ class voc_kv_cache(ctypes.Structure):
     ]
 
 
+class voc_adapters(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int),
+        ("count", ctypes.c_int),
+        ("rank", ctypes.c_int),
+        ("down_stride", ctypes.c_int64),
+        ("down", ctypes.c_void_p),
+        ("up", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+    ]
+
+
 class voc_kv_batch(ctypes.Structure):
     _fields_ = [
         ("batch", ctypes.c_int64),
@@ -165,6 +177,11 @@ def lib():
             "vocoder_rms_norm": (I, [P, I, I64, I64, P, I64, P, I64, P, I64, P, F, P, I64, P, P]),
             "vocoder_quantize_rows": (I, [P, I, I64, I64, P, I64, P, I64, P, P]),
             "vocoder_matmul_int": (I, [P, I, I64, I64, I64, P, I64, P, P, I64, P, P, I, P, I64, P]),
+            "vocoder_matmul_int_adapters": (I, [P, I, I64, I64, I64, P, I64, P, P, I64, P, P, I, P, P, P, I64, P]),
+            "vocoder_norm_rotate": (I, [P, I, I64, I, P, P, I, I, F] + [I, P, I64, I64, P, P, I64, I64] * 2 + [P]),
+            "vocoder_norm_rotate_append": (I, [P, P, P, I, P, I, I, F, I, P, I64, I64, P, P, I64, I64, P, I64, I64, P, P,
+                                               I64, I64, P]),
+            "vocoder_cache_read": (I, [P, P, P, I, P, I64, I64, P, I64, I64, P]),
             "vocoder_cache_append": (I, [P, P, P, I, P, I64, I64, P, I64, I64, P]),
             "vocoder_cache_attention": (I, [P, P, P, I, I, P, I64, I64, F, I, I64, P, I64, I64, P]),
         }
@@ -574,13 +591,13 @@ def open_ops(device: int = 0):
 # call takes about 5 us in the library; the checks here are written to cost
 # little beside that.
 _dtypes: dict = {}
-_int8 = _float32 = _empty = _raw_stream = None
+_int8 = _int32 = _float32 = _empty = _raw_stream = None
 
 
 def _use_torch() -> None:
-    global _int8, _float32, _empty, _raw_stream
+    global _int8, _int32, _float32, _empty, _raw_stream
     import torch
-    _int8, _float32, _empty = torch.int8, torch.float32, torch.empty
+    _int8, _int32, _float32, _empty = torch.int8, torch.int32, torch.float32, torch.empty
     # The public torch.cuda.current_stream() builds a Stream object (3 us).
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda device: torch.cuda.current_stream(device).cuda_stream)
@@ -659,6 +676,15 @@ def _vector(what: str, t, n: int, device: int) -> int:
     """Checks n contiguous float32 values on `device`; returns their address."""
     if t.dtype is not _float32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what}: {n} contiguous CUDA float32 values are needed")
+    if t.get_device() != device:
+        raise _elsewhere(what, t, device)
+    return t.data_ptr()
+
+
+def _indices(what: str, t, n: int, device: int) -> int:
+    """Checks n contiguous int32 values on `device`; returns their address."""
+    if t.dtype is not _int32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what}: {n} contiguous CUDA int32 values are needed")
     if t.get_device() != device:
         raise _elsewhere(what, t, device)
     return t.data_ptr()
@@ -751,6 +777,92 @@ def matmul_int(ops, a, a_scale, b, b_scale, bias=None, gelu: bool = False, dtype
     return out
 
 
+class Adapters:
+    """Low-rank adapters of one product (voc_adapters): down [count, rank, K]
+    and up [count, N, rank], both float16 or bfloat16, and scale fp32 [count]
+    (default 1).  They are laid out once, in tensors of their own with the rank
+    padded to a multiple of 16 and K to one of 8 by zeros; `set` replaces one."""
+
+    def __init__(self, down, up, scale=None):
+        import torch
+        if down.dim() != 3 or up.dim() != 3 or down.shape[0] != up.shape[0] or down.shape[1] != up.shape[2]:
+            raise ValueError(f"adapters: down [count, rank, K] and up [count, N, rank] are needed, got {tuple(down.shape)} "
+                             f"and {tuple(up.shape)}")
+        if down.dtype not in (torch.float16, torch.bfloat16) or up.dtype != down.dtype:
+            raise ValueError(f"adapters: both float16 or both bfloat16 are needed, got {down.dtype} and {up.dtype}")
+        if not down.is_cuda or up.device != down.device:
+            raise ValueError(f"adapters: all of their tensors have to be on one CUDA device, not {down.device} and {up.device}")
+        self.count, self.rank, self.K = down.shape
+        self.N = up.shape[1]
+        if not (self.count and self.K and self.N) or not 1 <= self.rank <= 256:
+            raise ValueError("adapters: ranks of 1 to 256, and at least one adapter, input and output are needed")
+        rank, stride = -(-self.rank // 16) * 16, -(-self.K // 8) * 8
+        self.device = down.get_device()
+        self.down = torch.zeros(self.count, rank, stride, dtype=down.dtype, device=down.device)
+        self.up = torch.zeros(self.count, self.N, rank, dtype=up.dtype, device=up.device)
+        self.scale = torch.ones(self.count, device=down.device)
+        self.down[:, :self.rank, :self.K] = down
+        self.up[:, :, :self.rank] = up
+        if scale is not None:
+            if scale.shape != (self.count,) or scale.device != down.device:
+                raise ValueError(f"adapters: scale [{self.count}] on {down.device} is needed")
+            self.scale.copy_(scale)
+        self.tensors = self.down, self.up, self.scale
+        self.c = voc_adapters(VOC_F16 if down.dtype == torch.float16 else VOC_BF16, self.count, rank, stride,
+                              self.down.data_ptr(), self.up.data_ptr(), self.scale.data_ptr())
+        self.ref = ctypes.byref(self.c)
+
+    def set(self, index: int, down, up, scale: float = 1.0) -> None:
+        """Replaces adapter `index` by down [r, K] and up [N, r] (r up to the
+        rank these were made with), on the current stream."""
+        r = down.shape[0]
+        if not 0 <= index < self.count:
+            raise ValueError(f"adapter {index}: there are {self.count}")
+        if r > self.rank or tuple(down.shape) != (r, self.K) or tuple(up.shape) != (self.N, r):
+            raise ValueError(f"adapter: down [r, {self.K}] and up [{self.N}, r], r up to {self.rank}, are needed")
+        self.down[index].zero_()
+        self.up[index].zero_()
+        self.down[index, :r, :self.K] = down
+        self.up[index, :, :r] = up
+        self.scale[index] = scale
+
+
+def matmul_int_adapters(ops, a, a_scale, b, b_scale, adapters: Adapters, adapter, bias=None, gelu: bool = False, dtype=None,
+                        out=None, stream=None):
+    """matmul_int with the low-rank term of each row's adapter before act
+    (vocoder_matmul_int_adapters): adapter int32 [M], a number outside
+    [0, adapters.count) for none."""
+    at = ops.device
+    lda = _rows("a", a, a.shape, _int8, at)
+    M, K = a.shape
+    N = b.shape[0]
+    ldb = _rows("b", b, (N, K), _int8, at)
+    if (K, N) != (adapters.K, adapters.N):
+        raise ValueError(f"adapters: of a product {adapters.K} -> {adapters.N}, this one is {K} -> {N}")
+    if adapters.device != at:
+        raise _elsewhere("adapters", adapters.down, at)
+    raw, other = (_raw_stream(at), None) if stream is None else _stream_of(stream, a)
+    if out is None:
+        if dtype is None:
+            import torch
+            dtype = torch.float16
+        out, ldy = _new(other, (M, N), dtype, a.device), N
+    else:
+        if dtype is None:
+            dtype = out.dtype
+        ldy = _rows("out", out, (M, N), dtype, at)
+    st = lib().vocoder_matmul_int_adapters(
+        ops, _dtype(dtype), M, N, K, a.data_ptr(), lda, _vector("a_scale", a_scale, M, at), b.data_ptr(), ldb,
+        _vector("b_scale", b_scale, N, at),
+        None if bias is None else _vector("bias", bias, N, at),
+        VOC_ACT_GELU if gelu else VOC_ACT_NONE, adapters.ref, _indices("adapter", adapter, M, at), out.data_ptr(), ldy, raw)
+    if other is not None:
+        _keep(other, a, a_scale, b, b_scale, bias, adapter, out, *adapters.tensors)
+    if st:
+        _check_ops(st, ops)
+    return out
+
+
 class KVCache:
     """A paged 8-bit cache (voc_kv_cache): k int8 [pages, kv_heads,
     page_tokens, head_dim], v int8 [pages, kv_heads, head_dim, page_tokens],
@@ -820,6 +932,55 @@ def _heads(what: str, t, shape, dtype, device: int):
     return step, head
 
 
+def _turning(freq, head_dim: int, device: int):
+    """Number and address of the rotary frequencies (None: nothing rotates)."""
+    if freq is None:
+        return 0, None
+    pairs = freq.numel()
+    if 2 * pairs > head_dim:
+        raise ValueError(f"freq: at most {head_dim // 2} frequencies for heads of {head_dim}, got {pairs}")
+    return pairs, _vector("freq", freq, pairs, device)
+
+
+def norm_rotate(ops, q, k=None, position=None, freq=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                adjacent: bool = False, q_out=None, k_out=None, stream=None):
+    """(q, k) of the query heads q [tokens, heads, head_dim] and the key heads
+    k [tokens, kv_heads, head_dim] (or None): each head's RMS norm (where its
+    weight [head_dim] is given) and its first 2 * len(freq) values rotated by
+    position [tokens] (int32) times freq (vocoder_norm_rotate).  Pairs are
+    (2i, 2i + 1) if adjacent, else (i, i + len(freq)).  q_out and k_out may be q
+    and k themselves."""
+    shape, dtype, device = q.shape, q.dtype, ops.device
+    qt, qh = _heads("q", q, shape, dtype, device)
+    tokens, heads, dim = shape
+    raw, other = (_raw_stream(device), None) if stream is None else _stream_of(stream, q)
+    pairs, fp = _turning(freq, dim, device)
+    if q_out is None:
+        q_out = _new(other, shape, dtype, q.device)
+    ot, oh = _heads("q_out", q_out, shape, dtype, device)
+    qw = None if q_weight is None else _vector("q_weight", q_weight, dim, device)
+    kv_heads = kp = kt = kh = kw = kop = kot = koh = 0
+    if k is not None:
+        kv_heads = k.shape[1]
+        kshape = (tokens, kv_heads, dim)
+        kt, kh = _heads("k", k, kshape, dtype, device)
+        if k_out is None:
+            k_out = _new(other, kshape, dtype, q.device)
+        kot, koh = _heads("k_out", k_out, kshape, dtype, device)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+        kw = None if k_weight is None else _vector("k_weight", k_weight, dim, device)
+    if pairs and position is None:
+        raise ValueError("position: needed where values rotate")
+    pp = None if position is None else _indices("position", position, tokens, device)
+    st = lib().vocoder_norm_rotate(ops, _dtype(dtype), tokens, dim, pp, fp, pairs, int(adjacent), eps, heads, q.data_ptr(), qt,
+                                   qh, qw, q_out.data_ptr(), ot, oh, kv_heads, kp, kt, kh, kw, kop, kot, koh, raw)
+    if other is not None:
+        _keep(other, q, k, position, freq, q_weight, k_weight, q_out, k_out)
+    if st:
+        _check_ops(st, ops)
+    return q_out, k_out if k is not None else None
+
+
 def _with_tokens(batch: KVBatch, tokens: int) -> voc_kv_batch:
     """The batch for a call with `tokens` packed rows, a struct of that call's
     own: in a shared one another thread could change the number between this
@@ -850,6 +1011,70 @@ def cache_append(ops, cache: KVCache, batch: KVBatch, k, v, stream=None) -> None
         _keep(other, k, v, *cache.tensors, *batch.tensors)
     if st:
         _check_ops(st, ops)
+
+
+def norm_rotate_append(ops, cache: KVCache, batch: KVBatch, q, k, v, freq=None, q_weight=None, k_weight=None,
+                       eps: float = 1e-6, adjacent: bool = False, out=None, stream=None):
+    """norm_rotate of q [tokens, heads, head_dim] and k [tokens, kv_heads,
+    head_dim] by the batch's positions, and cache_append of those keys and of v,
+    in one launch (vocoder_norm_rotate_append).  Returns the queries, in `out`
+    (which may be q itself) or a new tensor; with q None only the cache is
+    written."""
+    dtype, tokens, device, dim = k.dtype, k.shape[0], ops.device, cache.head_dim
+    shape = (tokens, cache.kv_heads, dim)
+    kt, kh = _heads("k", k, shape, dtype, device)
+    vt, vh = _heads("v", v, shape, dtype, device)
+    if not device == cache.device == batch.device:
+        raise _apart(ops, cache, batch)
+    raw, other = (_raw_stream(device), None) if stream is None else _stream_of(stream, k)
+    pairs, fp = _turning(freq, dim, device)
+    heads = qp = qt = qh = op = ot = oh = 0
+    qw = None if q_weight is None else _vector("q_weight", q_weight, dim, device)
+    kw = None if k_weight is None else _vector("k_weight", k_weight, dim, device)
+    if q is not None:
+        heads = q.shape[1]
+        qshape = (tokens, heads, dim)
+        qt, qh = _heads("q", q, qshape, dtype, device)
+        if out is None:
+            out = _new(other, qshape, dtype, q.device)
+        ot, oh = _heads("out", out, qshape, dtype, device)
+        qp, op = q.data_ptr(), out.data_ptr()
+    c = _with_tokens(batch, tokens)
+    st = lib().vocoder_norm_rotate_append(ops, cache.ref, ctypes.byref(c), _dtype(dtype), fp, pairs, int(adjacent), eps, heads,
+                                          qp, qt, qh, qw, op, ot, oh, k.data_ptr(), kt, kh, kw, v.data_ptr(), vt, vh, raw)
+    if other is not None:
+        _keep(other, q, k, v, freq, q_weight, k_weight, out, *cache.tensors, *batch.tensors)
+    if st:
+        _check_ops(st, ops)
+    return out if q is not None else None
+
+
+def cache_read(ops, cache: KVCache, batch: KVBatch, tokens: int, dtype=None, k=None, v=None, stream=None):
+    """(k, v) [tokens, kv_heads, head_dim]: the keys and values at the batch's
+    positions, rows starts[b] + i the position past[b] + i of sequence b
+    (vocoder_cache_read), in `dtype` (default float16) or that of k and v where
+    they are given.  Rows that belong to no sequence are left as they are."""
+    device, shape = ops.device, (tokens, cache.kv_heads, cache.head_dim)
+    if not device == cache.device == batch.device:
+        raise _apart(ops, cache, batch)
+    if dtype is None:
+        import torch
+        dtype = k.dtype if k is not None else v.dtype if v is not None else torch.float16
+    raw, other = (_raw_stream(device), None) if stream is None else _stream_of(stream, cache.k)
+    if k is None:
+        k = _new(other, shape, dtype, cache.k.device)
+    if v is None:
+        v = _new(other, shape, dtype, cache.k.device)
+    kt, kh = _heads("k", k, shape, dtype, device)
+    vt, vh = _heads("v", v, shape, dtype, device)
+    c = _with_tokens(batch, tokens)
+    st = lib().vocoder_cache_read(ops, cache.ref, ctypes.byref(c), _dtype(dtype), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+                                  raw)
+    if other is not None:
+        _keep(other, k, v, *cache.tensors, *batch.tensors)
+    if st:
+        _check_ops(st, ops)
+    return k, v
 
 
 def cache_attention(ops, cache: KVCache, batch: KVBatch, q, scale: float | None = None, causal: bool = True,

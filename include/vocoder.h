@@ -468,7 +468,11 @@ voc_status voc_dbg_peak(int what, int64_t n, double *value, void *hip_stream);
  *   vocoder_rms_norm         residual addition, RMS norm, 8-bit rows
  *   vocoder_quantize_rows    8-bit rows of any matrix (weights, activations)
  *   vocoder_matmul_int       8-bit integer product with row scales
+ *   vocoder_matmul_int_adapters  the same with a low-rank adapter a row
+ *   vocoder_norm_rotate      norm and rotation of query and key heads
  *   vocoder_cache_append     keys and values into a paged 8-bit cache
+ *   vocoder_norm_rotate_append   both, the keys on their way into the cache
+ *   vocoder_cache_read       the cache's tokens as rows again
  *   vocoder_cache_attention  attention over that cache
  *
  * All of them work on device buffers of the caller, are asynchronous on
@@ -486,7 +490,8 @@ voc_status voc_dbg_peak(int what, int64_t n, double *value, void *hip_stream);
  * so that what is computed from it is NaN.  Scales are never negative.
  *
  * Threading: as for voc_ctx, one handle per host thread and stream (the
- * handle owns the workspace in which split attention joins its parts).  The
+ * handle owns the workspace in which split attention joins its parts and
+ * the adapters' low-rank activations lie).  The
  * structs below are only read and may be shared.  All buffers of a call are
  * on the handle's device. */
 typedef struct voc_ops voc_ops;
@@ -548,6 +553,69 @@ voc_status vocoder_matmul_int(voc_ops *ops, int out_dtype, int64_t M, int64_t N,
                               void *y, int64_t ldy, void *hip_stream);
 
 /*
+ * The product with a low-rank adapter a row beside the shared weights:
+ *   y[m][n] = act((sum_k a[m][k] b[n][k]) * a_scale[m] * b_scale[n] + bias[n]
+ *                 + sum_r up[i][n][r] u[m][r])
+ *   u[m][r] = scale[i] a_scale[m] sum_k down[i][r][k] a[m][k],  i = adapter[m]
+ * adapter: int32 [M] on the device; a row whose number is outside
+ * [0, adapters->count) has no adapter.  Rows of one adapter are best adjacent.
+ * All else is as for vocoder_matmul_int.
+ * down and up hold dtype VOC_F16 or VOC_BF16; u and every sum are fp32.  For
+ * the matrix cores u is split into terms of the weights' dtype, fp16 two (22
+ * bits of a row's largest), bf16 two (16 bits) or, for fp32 outputs, three.
+ * rank: a multiple of 16 up to 256 (smaller adapters are padded with zeros);
+ * down_stride: elements between rows of down, at least K, a multiple of 8,
+ * the values between K and the next multiple of 8 readable; down and up are
+ * 16-byte aligned.  scale: fp32 [count], or NULL for 1.
+ * Uses the handle's workspace.
+ * Errors: VOC_INVALID_PARAMS, VOC_DEVICE_ERROR.
+ */
+typedef struct voc_adapters {
+  int dtype, count, rank;
+  int64_t down_stride;
+  const void *down;   /* [count][rank][down_stride] */
+  const void *up;     /* [count][N][rank] */
+  const float *scale; /* [count] or NULL */
+} voc_adapters;
+voc_status vocoder_matmul_int_adapters(voc_ops *ops, int out_dtype, int64_t M, int64_t N,
+                                       int64_t K, const int8_t *a, int64_t lda,
+                                       const float *a_scale, const int8_t *b, int64_t ldb,
+                                       const float *b_scale, const float *bias, int act,
+                                       const voc_adapters *adapters, const int32_t *adapter,
+                                       void *y, int64_t ldy, void *hip_stream);
+
+/*
+ * Norm and rotation of each head of a token in one pass, of `heads` query
+ * heads q and `kv_heads` key heads k (either number may be 0, its pointers are
+ * then not used):
+ *   y = x / sqrt(mean(x^2) + eps) * weight      (over the head's values; with
+ *                                               a NULL weight y = x)
+ *   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin) for `pairs` pairs,
+ *   pair i: values 2i and 2i + 1 (adjacent = 1) or i and i + pairs
+ *   (adjacent = 0), angle position[token] * freq[i]
+ * Values from 2 * pairs on are not rotated.  The angle is the product of the
+ * int32 position and the fp32 frequency, taken to its fraction of a turn in 64
+ * bits: far positions keep their angles.  The result is rounded once.  A head
+ * with a weight whose sum of squares is not finite in fp32 becomes NaN.
+ * q, k and their outputs: dtype, element [token][head][d] at token *
+ * token_stride + head * head_stride + d; an output may be its input itself
+ * (any other overlap is an error of the caller).  weights: fp32 [head_dim];
+ * freq: fp32 [pairs]; position: int32 [tokens] (NULL only with pairs = 0).
+ * 1 <= head_dim <= 256, 2 * pairs <= head_dim, tokens up to 2^26.
+ * Pointers and strides of 16-byte multiples, head_dim of 8 and pairs of 4 run
+ * faster.
+ * Errors: VOC_INVALID_PARAMS, VOC_DEVICE_ERROR.
+ */
+voc_status vocoder_norm_rotate(voc_ops *ops, int dtype, int64_t tokens, int head_dim,
+                               const int32_t *position, const float *freq, int pairs, int adjacent,
+                               float eps, int heads, const void *q, int64_t q_token_stride,
+                               int64_t q_head_stride, const float *q_weight, void *q_out,
+                               int64_t q_out_token_stride, int64_t q_out_head_stride, int kv_heads,
+                               const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                               const float *k_weight, void *k_out, int64_t k_out_token_stride,
+                               int64_t k_out_head_stride, void *hip_stream);
+
+/*
  * A paged cache in 8 bits.  A page holds page_tokens consecutive tokens of
  * one sequence for every cache head, with one key scale and one value scale
  * per page and head:
@@ -605,6 +673,42 @@ voc_status vocoder_cache_append(voc_ops *ops, const voc_kv_cache *cache, const v
                                 int dtype, const void *k, int64_t k_token_stride,
                                 int64_t k_head_stride, const void *v, int64_t v_token_stride,
                                 int64_t v_head_stride, void *hip_stream);
+
+/*
+ * vocoder_norm_rotate of new queries and keys, and vocoder_cache_append of
+ * those keys and of the values v, in one launch: row starts[b] + i of sequence
+ * b sits at position past[b] + i (past as the append reads it).  The keys go
+ * into the page's scale and codes from fp32, without a rounding to dtype.
+ * heads may be 0 (keys and values only); rows of q_out that belong to no
+ * sequence are not written.
+ * The number of workgroups, batch times the heads of the touched pages and the
+ * queries, stays below 2^24.
+ * Errors: VOC_INVALID_PARAMS, VOC_DEVICE_ERROR.
+ */
+voc_status vocoder_norm_rotate_append(voc_ops *ops, const voc_kv_cache *cache,
+                                      const voc_kv_batch *batch, int dtype, const float *freq,
+                                      int pairs, int adjacent, float eps, int heads, const void *q,
+                                      int64_t q_token_stride, int64_t q_head_stride,
+                                      const float *q_weight, void *q_out,
+                                      int64_t q_out_token_stride, int64_t q_out_head_stride,
+                                      const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                                      const float *k_weight, const void *v, int64_t v_token_stride,
+                                      int64_t v_head_stride, void *hip_stream);
+
+/*
+ * The cache's tokens as rows: row starts[b] + i of k and v becomes the key and
+ * value at position past[b] + i of sequence b, code * scale rounded to dtype
+ * once (strides as in vocoder_cache_append; either of k and v may be NULL).  The
+ * batch that appended tokens reads them back; past = 0 and the whole lengths
+ * as new tokens read whole sequences.  Rows that belong to no sequence, and
+ * positions in pages out of range, are not written.
+ * The number of workgroups stays below 2^24.
+ * Errors: VOC_INVALID_PARAMS, VOC_DEVICE_ERROR.
+ */
+voc_status vocoder_cache_read(voc_ops *ops, const voc_kv_cache *cache, const voc_kv_batch *batch,
+                              int dtype, void *k, int64_t k_token_stride, int64_t k_head_stride,
+                              void *v, int64_t v_token_stride, int64_t v_head_stride,
+                              void *hip_stream);
 
 /*
  * Attention of the new tokens' queries over the cache (their own keys and
