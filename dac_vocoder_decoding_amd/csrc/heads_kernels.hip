@@ -41,7 +41,8 @@ struct Unit {
   int at, hi;      // MODE < kAny: first value (kHalves: of the first and the second four)
   int unit, F, D;  // kAny
   bool adjacent, live, turns;
-  __device__ __forceinline__ Unit(int u, int F, int D, bool adjacent) : unit(u), F(F), D(D), adjacent(adjacent) {
+  __device__ __forceinline__ Unit(int u, int F, int D, bool adjacent)
+      : unit(u), F(F), D(D), adjacent(MODE == kAdjacent || (MODE == kAny && adjacent)) {
     const int turning = (F + 3) >> 2;
     turns = u < turning;
     if constexpr (MODE == kHalves) {
@@ -59,10 +60,10 @@ struct Unit {
       const int p = 4 * unit + (k >> 1);
       return p >= F ? -1 : adjacent ? 2 * p + (k & 1) : p + (k & 1) * F;
     }
-    const int d = 2 * F + 8 * (unit - ((F + 3) >> 2)) + k;
+    const int d = 2 * F + 8 * (unit - ((F + 3) >> 2)) + (adjacent ? k : (k >> 1) + 4 * (k & 1));
     return d < D ? d : -1;
   }
-  // Place 2i and 2i + 1 are a pair; behind the pairs of kHalves the first four
+  // Places 2i and 2i + 1 are a pair; behind pairs of halves the first four
   // values have the even places.
   template <int T>
   __device__ __forceinline__ void load(const typename Elem<T>::type* head, float (&v)[8]) const {
@@ -161,7 +162,7 @@ __device__ __forceinline__ void turn(const HeadShape& h, const Unit<MODE>& u, bo
   if (norm) {
     float sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum += v[k] * v[k];
+    for (int k = 0; k < 8; ++k) sum = fmaf(v[k], v[k], sum);  // (the same steps whatever the alignment)
 #pragma unroll
     for (int m = G / 2; m; m >>= 1) sum += __shfl_xor(sum, m);
     float rms = rsqrtf(sum / static_cast<float>(h.D) + h.eps);
@@ -292,8 +293,8 @@ __global__ __launch_bounds__(256) void step_few_kernel(const StepArgs a, int pag
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int d = MODE == kHalves ? (k & 1 ? u.hi : u.at) + (k >> 1) : u.value(k);
-        if (u.live && d >= 0) codes[static_cast<int64_t>(d) * P + t] = static_cast<int8_t>(code_of(v[k], inv));
+        const int d = u.value(k);
+        if (d >= 0) codes[static_cast<int64_t>(d) * P + t] = static_cast<int8_t>(code_of(v[k], inv));
       }
     }
   }

@@ -164,7 +164,8 @@ __device__ __forceinline__ float split_u(bool bf16, const float (&x)[8], i32x4 (
 // + lr) becomes the bits of fp32 values, acc sa sb + bias + the tokens'
 // low-rank terms.  One adapter after another among the wave's tokens (those of
 // one adapter are best adjacent), 32 ranks at a time; tokens of another
-// adapter enter the product as zeros.
+// adapter enter the product as zeros and keep what they have (a weight that is
+// not finite stays with its own tokens).
 template <int T, int FF, int FT, int NT>
 __device__ __forceinline__ void add_low_rank_terms(const IntMatmulArgs& a, int nw, int mw, const f4 (&sb)[FF], const f4 (&bi)[FF],
                                                    i32x4 (&acc)[FF][FT]) {
@@ -222,7 +223,8 @@ __device__ __forceinline__ void add_low_rank_terms(const IntMatmulArgs& a, int n
               d = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, w), __builtin_bit_cast(f16x8, uf[j][t]), d, 0, 0, 0);
           }
 #pragma unroll
-          for (int q = 0; q < 4; ++q) acc[i][j][q] = __float_as_int(fmaf(d[q], down[j], __int_as_float(acc[i][j][q])));
+          for (int q = 0; q < 4; ++q)
+            if (id[j] == pick) acc[i][j][q] = __float_as_int(fmaf(d[q], down[j], __int_as_float(acc[i][j][q])));
         }
       }
     }
