@@ -4,70 +4,355 @@
 //                 + sum_r up_i[n][r] u[m][r]),   i = adapter[m]
 //   u[m][r] = scale[i] sa[m] sum_k down_i[r][k] a[m][k].
 //
-// Two launches: u (fp32, in the handle's workspace), then the product, whose
+// Two launches: u into the handle's workspace, then the product, whose
 // epilogue adds the terms (int_matmul.h).  Codes are exact in fp16 and bf16, so
 // that u is a sum of exact products in fp32.
+//
+// v_mfma_f32_16x16x32: "A" are 16 ranks, "B" 16 rows, so that a lane ends up
+// with four consecutive ranks of one row.  down lies in the order in which the
+// lanes of a wave take it (vocoder.h): a load reads 1 KB in a row.  (Rows of
+// down as they are make a quarter of a wave touch 16 cache lines, one a cycle:
+// 8000 rows of 4096, 64 ranks, 27 us.)
+#include <type_traits>
+
 #include "int_matmul.h"
 
 namespace voc {
 
-// 8 codes of a row of K at k, zero past its end.
-__device__ __forceinline__ uint2 load_codes8(const int8_t* row, int k, int K) {
-  uint2 c = {0, 0};
-  if (k + 8 <= K) {
-    __builtin_memcpy(&c, row + k, 8);
+constexpr int kChunk = 128;  // codes of a row that a wave takes at a time: two steps of 64
+
+// 16 codes of a row of K at k, zero past its end.
+__device__ __forceinline__ i32x4 load_codes16(const int8_t* row, int k, int K) {
+  i32x4 c = {0, 0, 0, 0};
+  if (k + 16 <= K) {
+    __builtin_memcpy(&c, row + k, 16);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (k + i < K) (i < 4 ? c.x : c.y) |= (static_cast<uint32_t>(row[k + i]) & 0xffu) << (8 * (i & 3));
+    for (int i = 0; i < 16; ++i)
+      if (k + i < K) c[i >> 2] |= static_cast<int>((static_cast<uint32_t>(row[k + i]) & 0xffu) << (8 * (i & 3)));
   }
   return c;
 }
 
-// Eight weights of a row of K at k (16-byte aligned, ldd covers them).
+// Eight codes as eight values of the weights' type, exactly.
 template <bool BF16>
-__device__ __forceinline__ void load_down(const uint16_t* p, float (&w)[8]) {
-  if constexpr (BF16)
-    load8<EL_BF16>(reinterpret_cast<const __bf16*>(p), w);
-  else
-    load8<EL_F16>(reinterpret_cast<const _Float16*>(p), w);
+__device__ __forceinline__ i32x4 codes_to_16(uint32_t a, uint32_t b) {
+  i32x4 v;
+  if constexpr (BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = i < 2 ? a : b;
+      const float lo = static_cast<float>(static_cast<int8_t>(w >> (16 * (i & 1))));
+      const float hi = static_cast<float>(static_cast<int8_t>(w >> (16 * (i & 1) + 8)));
+      v[i] = static_cast<int>(__builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u));
+    }
+  } else {
+    // The byte, its sign bit flipped, as the low mantissa byte of 1024 + u, less 1152.
+    const f16x2 bias = {static_cast<_Float16>(1152.f), static_cast<_Float16>(1152.f)};
+    a ^= 0x80808080u;
+    b ^= 0x80808080u;
+    v[0] = __builtin_bit_cast(int, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, a, 0x04010400u)) - bias);
+    v[1] = __builtin_bit_cast(int, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, a, 0x04030402u)) - bias);
+    v[2] = __builtin_bit_cast(int, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, b, 0x04010400u)) - bias);
+    v[3] = __builtin_bit_cast(int, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, b, 0x04030402u)) - bias);
+  }
+  return v;
 }
 
-// A wave per token and four ranks.
 template <bool BF16>
-__global__ __launch_bounds__(256) void shrink_few_kernel(const AdaptArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int m = blockIdx.y, r0 = blockIdx.x * 16 + (threadIdx.x >> 6) * 4;
-  const int id = a.g.adapter[m], K = a.g.K;
-  if (id < 0 || id >= a.g.adapters) return;
-  const int8_t* row = a.g.a + static_cast<int64_t>(m) * a.g.lda;
-  const uint16_t* down = a.down + (static_cast<int64_t>(id) * a.g.rank + r0) * a.ldd;
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int k = lane * 8; k < K; k += 512) {
-    const uint2 c = load_codes8(row, k, K);
-    float w[4][8];
+__device__ __forceinline__ void multiply16(const i32x4& w, const i32x4& x, f32x4& acc) {
+  if constexpr (BF16)
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);
+  else
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, w), __builtin_bit_cast(f16x8, x), acc, 0, 0, 0);
+}
+
+// The weights of one chunk: RT blocks of 16 ranks, two steps, two halves.
+template <int RT>
+struct Weights {
+  i32x4 w[RT][2][2];
+};
+// down + this lane's place: block i, step s, half h are ((i steps + s) 2 + h) KB further.
+template <int RT>
+__device__ __forceinline__ void load_weights(const uint16_t* down, int steps, int chunk, Weights<RT>& g) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load_down<BF16>(down + i * a.ldd + k, w[i]);
+  for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float x = static_cast<float>(static_cast<int8_t>((j < 4 ? c.x : c.y) >> (8 * (j & 3))));
-      if (k + j < K) {
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] = fmaf(x, w[i][j], sum[i]);
+      for (int h = 0; h < 2; ++h)  // (a last step that is not there has codes of zero: any weights do, those of the one before)
+        g.w[i][s][h] = *reinterpret_cast<const i32x4*>(
+            down + ((static_cast<int64_t>(i) * steps + min(2 * chunk + s, steps - 1)) * 2 + h) * 512);
+}
+
+// Eight ranks of row m (place r of its chunk, in a group of LANES lanes that
+// hold the chunk) to the workspace: fp32 values, or their terms and the factor
+// that these are to be multiplied by.
+template <bool BF16, int LANES>
+__device__ __forceinline__ void store_u(const AdaptArgs& a, int64_t m, int block, int r, const float (&v)[8]) {
+  const int chunk = 8 * LANES, blocks = a.g.rank / chunk;
+  if (a.terms == 0) {
+    store8<EL_F32>(a.u + m * a.g.rank + block * chunk + r, v);
+    return;
+  }
+  float up = 1.f, down = 1.f;
+  if constexpr (!BF16) {
+    // fp16 reaches from the largest, brought to [2^14, 2^15), down to 2^-39 of it.
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, abs_bits(v[i]));
+#pragma unroll
+    for (int x = LANES / 2; x; x >>= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), x)));
+    const uint32_t e = min(max(top >> 23, 15u), 254u);
+    up = __uint_as_float((268u - e) << 23);
+    down = __uint_as_float((e - 14u) << 23);
+  }
+  // 16 rows by 32 ranks of a term are 1 KB in a row, as the lanes of the product take them.
+  uint16_t* t = a.g.ut + (((m >> 4) * blocks + block) * a.terms) * chunk * 16 + ((r >> 3) * 16 + (m & 15)) * 8;
+  float rest[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) rest[i] = v[i] * up;
+  for (int n = 0; n < a.terms; ++n, t += chunk * 16) {
+    union { i32x4 v; _Float16 h[8]; __bf16 b[8]; } o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (BF16) {
+        o.b[i] = static_cast<__bf16>(rest[i]);
+        rest[i] -= static_cast<float>(o.b[i]);
+      } else {
+        o.h[i] = static_cast<_Float16>(rest[i]);
+        rest[i] -= static_cast<float>(o.h[i]);
       }
     }
+    *reinterpret_cast<i32x4*>(t) = o.v;
   }
-  const float f = a.g.sa[m] * (a.scale ? a.scale[id] : 1.f);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) sum[i] = wave_sum(sum[i]) * f;
-  if (lane == 0) *reinterpret_cast<float4*>(a.u + static_cast<int64_t>(m) * a.g.rank + r0) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+  if (r == 0) a.g.uf[m * blocks + block] = down;
 }
 
-hipError_t launch_int_matmul_adapters(int dtype, const AdaptArgs& a, hipStream_t s, Form& form) {
-  if (a.g.up_bf16)
-    shrink_few_kernel<true><<<dim3(a.g.rank / 16, a.g.M), 256, 0, s>>>(a);
+// Few rows: a workgroup for a row and 16 RT ranks, K split over its eight
+// waves.  All 16 rows of the matrix product are this one (its codes reach 16
+// lanes in one read); bound by the latency of the loads.
+template <bool BF16, int RT>
+__global__ __launch_bounds__(512) void shrink_one_kernel(const AdaptArgs a, int blocks) {
+  __shared__ f32x4 s_acc[8][RT][4];
+  const int tid = threadIdx.x, lane = tid & 63, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int m = blockIdx.x / blocks, block = blockIdx.x % blocks;
+  const int id = a.g.adapter[m], K = a.g.K;
+  if (id < 0 || id >= a.g.adapters) return;
+  const int steps = (K + 63) / 64, chunks = (steps + 1) / 2;
+  const int8_t* row = a.g.a + static_cast<int64_t>(m) * a.g.lda;
+  const uint16_t* down = a.down + (static_cast<int64_t>(id) * (a.g.rank / 16) + block * RT) * steps * 1024 + lane * 8;
+  f32x4 acc[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+  for (int c = wave; c < chunks; c += 8) {
+    Weights<RT> g;
+    load_weights<RT>(down, steps, c, g);
+    i32x4 x[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) x[s] = load_codes16(row, c * kChunk + s * 64 + 16 * lg, K);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const i32x4 f = codes_to_16<BF16>(x[s][2 * h], x[s][2 * h + 1]);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) multiply16<BF16>(g.w[i][s][h], f, acc[i]);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+    if ((lane & 15) == 0) s_acc[wave][i][lg] = acc[i];
+  __syncthreads();
+  if (tid >= 2 * RT) return;
+  f32x4 v[2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    v[p] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v[p] += s_acc[w][tid >> 1][2 * (tid & 1) + p];
+  }
+  const float f = a.g.sa[m] * (a.scale ? a.scale[id] : 1.f);
+  float u[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) u[k] = v[k >> 2][k & 3] * f;
+  store_u<BF16, 2 * RT>(a, m, block, 8 * tid, u);
+}
+
+// Many rows: 16 TB of them and 16 RT ranks a workgroup, K split over its eight
+// waves, whose sums meet in LDS.  A wave reads whole lines of codes and turns
+// them over in its own part of LDS (rows of 128 bytes, unit u of row r at u ^
+// (r / 2 % 8)).  The rows' adapters are taken two at a time, so that a tile
+// over the border of two streams reads its codes once.
+template <bool BF16, int RT, int TB>
+__global__ __launch_bounds__(512) void shrink_tile_kernel(const AdaptArgs a, int blocks) {
+  constexpr int ROWS = 16 * TB, PITCH = 16 * RT + 4;
+  // Codes while the waves multiply (2 KB a wave and 16 rows), their sums, then u.
+  constexpr int SUMS = 8 * RT * TB * 1024, LDS = SUMS > 16384 * TB ? SUMS : 16384 * TB;
+  __shared__ __attribute__((aligned(16))) unsigned char smem[LDS];
+  __shared__ __attribute__((aligned(16))) float s_u[ROWS][PITCH];
+  __shared__ int s_id[ROWS];
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // Each XCD takes a contiguous range of rows: its L2 holds their adapters.
+  const int L = xcd_remap(blockIdx.x, gridDim.x);
+  const int m0 = L / blocks * ROWS, block = L % blocks;
+  const int K = a.g.K, steps = (K + 63) / 64, chunks = (steps + 1) / 2;
+  unsigned char* part = smem + wave * (2048 * TB);
+  int id[TB];
+#pragma unroll
+  for (int j = 0; j < TB; ++j) {
+    const int m = m0 + 16 * j + lr;
+    id[j] = m < a.g.M ? a.g.adapter[m] : -1;
+    if (id[j] >= a.g.adapters) id[j] = -1;
+    if (wave == 0 && lg == 0) s_id[16 * j + lr] = id[j];
+  }
+  // The lane's share of 8 rows x 128 codes: row lane / 8, unit lane % 8.
+  const int8_t* src[2 * TB];
+#pragma unroll
+  for (int q = 0; q < 2 * TB; ++q)
+    src[q] = a.g.a + static_cast<int64_t>(min(m0 + 8 * q + (lane >> 3), a.g.M - 1)) * a.g.lda;
+  const int64_t per = static_cast<int64_t>(a.g.rank / 16) * steps * 1024;  // weights of an adapter
+  const uint16_t* down0 = a.down + static_cast<int64_t>(block) * RT * steps * 1024 + lane * 8;
+
+  auto next_id = [&]() {
+    int pick = -1;
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {
+      const uint64_t left = __ballot(id[j] >= 0);
+      if (pick < 0 && left) pick = __builtin_amdgcn_readlane(id[j], __ffsll(static_cast<unsigned long long>(left)) - 1);
+    }
+#pragma unroll
+    for (int j = 0; j < TB; ++j)
+      if (id[j] == pick) id[j] = -1;
+    return pick;
+  };
+  while (true) {  // (the same for every wave: they hold the same numbers)
+    const int one = next_id(), two = one < 0 ? -1 : next_id();
+    if (one < 0) break;
+    f32x4 acc[2][RT][TB];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < TB; ++j) acc[n][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    i32x4 code[2 * TB];
+    auto fetch = [&](int c) {
+#pragma unroll
+      for (int q = 0; q < 2 * TB; ++q) code[q] = load_codes16(src[q], c * kChunk + 16 * (lane & 7), K);
+    };
+    if (wave < chunks) fetch(wave);
+    for (int c = wave; c < chunks; c += 8) {
+      Weights<RT> g;
+      load_weights<RT>(down0 + one * per, steps, c, g);
+#pragma unroll
+      for (int q = 0; q < 2 * TB; ++q) {
+        const int r = 8 * q + (lane >> 3);
+        *reinterpret_cast<i32x4*>(part + r * 128 + (((lane & 7) ^ ((r >> 1) & 7)) << 4)) = code[q];
+      }
+      if (c + 8 < chunks) fetch(c + 8);
+      wave_lds_sync();
+      i32x4 x[2][2][TB];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < TB; ++j) {
+          const i32x4 v = *reinterpret_cast<const i32x4*>(part + (16 * j + lr) * 128 + (((4 * s + lg) ^ ((lr >> 1) & 7)) << 4));
+          x[s][0][j] = codes_to_16<BF16>(v[0], v[1]);
+          x[s][1][j] = codes_to_16<BF16>(v[2], v[3]);
+        }
+      auto multiply = [&](int n) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+              for (int j = 0; j < TB; ++j) multiply16<BF16>(g.w[i][s][h], x[s][h][j], acc[n][i][j]);
+      };
+      multiply(0);
+      if (two >= 0) {
+        load_weights<RT>(down0 + two * per, steps, c, g);
+        multiply(1);
+      }
+      wave_lds_sync();
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int pick = n ? two : one;
+      if (pick < 0) break;
+      __syncthreads();  // every wave is done with its codes, or with the sums before
+      f32x4(*sums)[RT * TB][64] = reinterpret_cast<f32x4(*)[RT * TB][64]>(smem);
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < TB; ++j) sums[wave][i * TB + j][lane] = acc[n][i][j];
+      __syncthreads();
+      for (int b = wave; b < RT * TB; b += 8) {
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < 8; ++w) v += sums[w][b][lane];
+        *reinterpret_cast<f32x4*>(&s_u[16 * (b % TB) + lr][16 * (b / TB) + 4 * lg]) = v;
+      }
+      __syncthreads();
+      // Eight ranks of a row a thread; whole rows, so that a row's lanes agree.
+      if (tid < ROWS * 2 * RT) {
+        const int r = tid / (2 * RT), at = tid % (2 * RT) * 8;
+        if (s_id[r] == pick) {
+          const float f = a.g.sa[m0 + r] * (a.scale ? a.scale[pick] : 1.f);
+          float u[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) u[k] = s_u[r][at + k] * f;
+          store_u<BF16, 2 * RT>(a, m0 + r, block, at, u);
+        }
+      }
+    }
+    __syncthreads();  // (the next codes overwrite the sums)
+  }
+}
+
+template <bool BF16, int RT>
+static void go_shrink(const AdaptArgs& a, hipStream_t s) {
+  const int blocks = a.g.rank / (16 * RT);
+  if (a.g.M <= 64) {
+    shrink_one_kernel<BF16, RT><<<dim3(static_cast<unsigned>(a.g.M) * blocks), 512, 0, s>>>(a, blocks);
+    return;
+  }
+  auto groups = [&](int tb) { return static_cast<unsigned>((a.g.M + 16 * tb - 1) / (16 * tb)) * blocks; };
+  if (groups(2) >= 192)
+    shrink_tile_kernel<BF16, RT, 2><<<dim3(groups(2)), 512, 0, s>>>(a, blocks);
   else
-    shrink_few_kernel<false><<<dim3(a.g.rank / 16, a.g.M), 256, 0, s>>>(a);
+    shrink_tile_kernel<BF16, RT, 1><<<dim3(groups(1)), 512, 0, s>>>(a, blocks);
+}
+
+hipError_t launch_int_matmul_adapters(int dtype, const AdaptArgs& args, hipStream_t s, Form& form) {
+  AdaptArgs a = args;
+  // The workspace: terms of u and their factors, or u itself where the product
+  // takes it so.
+  const int chunk = a.g.rank < 64 ? a.g.rank : 64;
+  a.g.chunk = chunk;
+  a.terms = product_is_few(a.g) ? 0 : a.g.up_bf16 && dtype == EL_F32 ? 3 : 2;
+  a.u = static_cast<float*>(a.ws);
+  a.g.u = a.u;
+  a.g.ut = static_cast<uint16_t*>(a.ws);
+  a.g.uf = reinterpret_cast<float*>(a.g.ut + static_cast<int64_t>((a.g.M + 15) & ~15) * a.g.rank * 3);
+  auto shrink = [&](auto bf16) {
+    constexpr bool B = decltype(bf16)::value;
+    if (chunk == 16)
+      go_shrink<B, 1>(a, s);
+    else if (chunk == 32)
+      go_shrink<B, 2>(a, s);
+    else
+      go_shrink<B, 4>(a, s);
+  };
+  if (a.g.up_bf16)
+    shrink(std::true_type{});
+  else
+    shrink(std::false_type{});
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (dtype == EL_F32)

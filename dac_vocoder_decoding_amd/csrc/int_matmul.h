@@ -96,16 +96,18 @@ __device__ __forceinline__ float activate(float v, int act) {
 }
 
 // ------------------------------------------------------- low-rank terms
-// The terms of token m at features n .. n + 3: sum_r up[n][r] u[m][r] in fp32
-// (u: adapters.hip; n below N, rows past the last feature repeat it).
+// up is held in the order of matrix-core operands: 16 features by 32 ranks are
+// 1 KB in a row, feature f and rank r of it at (r / 8 * 16 + f) 8 + r % 8 (a
+// rank of 16 has the first half only).
+
+// The terms of token m at features n .. n + 3 (n a multiple of 4 below N):
+// sum_r up[n][r] u[m][r] in fp32.
 __device__ __forceinline__ f32x4 low_rank_terms(const IntMatmulArgs& a, int m, int n) {
   f32x4 add = {0.f, 0.f, 0.f, 0.f};
   const int id = a.adapter[m];
   if (id < 0 || id >= a.adapters) return add;
   const float* u = a.u + static_cast<int64_t>(m) * a.rank;
-  const uint16_t* up[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) up[i] = a.up + (static_cast<int64_t>(id) * a.N + min(n + i, a.N - 1)) * a.rank;
+  const uint16_t* up = a.up + (static_cast<int64_t>(id) * ((a.N + 15) >> 4) + (n >> 4)) * a.rank * 16 + (n & 15) * 8;
   for (int r = 0; r < a.rank; r += 8) {
     float x[8];
     load8<EL_F32>(u + r, x);
@@ -113,9 +115,9 @@ __device__ __forceinline__ f32x4 low_rank_terms(const IntMatmulArgs& a, int m, i
     for (int i = 0; i < 4; ++i) {
       float w[8];
       if (a.up_bf16)
-        load8<EL_BF16>(reinterpret_cast<const __bf16*>(up[i] + r), w);
+        load8<EL_BF16>(reinterpret_cast<const __bf16*>(up + r * 16 + i * 8), w);
       else
-        load8<EL_F16>(reinterpret_cast<const _Float16*>(up[i] + r), w);
+        load8<EL_F16>(reinterpret_cast<const _Float16*>(up + r * 16 + i * 8), w);
 #pragma unroll
       for (int k = 0; k < 8; ++k) add[i] = fmaf(w[k], x[k], add[i]);
     }
@@ -123,66 +125,25 @@ __device__ __forceinline__ f32x4 low_rank_terms(const IntMatmulArgs& a, int m, i
   return add;
 }
 
-// Eight of a token's u as matrix-core operands in NT terms that add up to
-// them: bf16 as they are, fp16 times 2^e such that the largest of the token's
-// 32 lies in [2^14, 2^15) (it is then held to 2^-22).  Returns 2^-e.
-template <int NT>
-__device__ __forceinline__ float split_u(bool bf16, const float (&x)[8], i32x4 (&f)[NT]) {
-  float down = 1.f, up = 1.f;
-  if (!bf16) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, abs_bits(x[i]));
-    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
-    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
-    const uint32_t e = min(max(top >> 23, 15u), 254u);
-    up = __uint_as_float((268u - e) << 23);
-    down = __uint_as_float((e - 14u) << 23);
-  }
-  float rest[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) rest[i] = x[i] * up;
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    union { i32x4 v; _Float16 h[8]; __bf16 b[8]; } o;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (bf16) {
-        o.b[i] = static_cast<__bf16>(rest[i]);
-        rest[i] -= static_cast<float>(o.b[i]);
-      } else {
-        o.h[i] = static_cast<_Float16>(rest[i]);
-        rest[i] -= static_cast<float>(o.h[i]);
-      }
-    }
-    f[t] = o.v;
-  }
-  return down;
-}
-
-// A wave's tile of sums acc (features nw + 16 i + 4 lg + q of token mw + 16 j
-// + lr) becomes the bits of fp32 values, acc sa sb + bias + the tokens'
-// low-rank terms.  One adapter after another among the wave's tokens (those of
-// one adapter are best adjacent), 32 ranks at a time; tokens of another
-// adapter enter the product as zeros and keep what they have (a weight that is
-// not finite stays with its own tokens).
-template <int T, int FF, int FT, int NT>
-__device__ __forceinline__ void add_low_rank_terms(const IntMatmulArgs& a, int nw, int mw, const f4 (&sb)[FF], const f4 (&bi)[FF],
-                                                   i32x4 (&acc)[FF][FT]) {
-  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+// The low-rank terms d of a wave's features nw + 16 i + 4 lg + q and tokens
+// mw + 16 j + lr.  One adapter after another among these tokens (those of one
+// adapter are best adjacent), 32 ranks at a time, u in NT terms with a factor
+// for each chunk of ranks; tokens of another adapter enter the product as zeros
+// and take nothing from it (a weight that is not finite stays with its own
+// tokens).
+template <bool BF16, int NT, int FF, int FT>
+__device__ __forceinline__ void low_rank_tile(const IntMatmulArgs& a, int nw, int mw, f32x4 (&d)[FF][FT]) {
+  const int lane = threadIdx.x & 63, lr = lane & 15;
   int id[FT];
 #pragma unroll
   for (int j = 0; j < FT; ++j) {
     const int m = mw + 16 * j + lr;
-    const float sa = a.sa[min(m, a.M - 1)];
     id[j] = m < a.M ? a.adapter[m] : -1;
     if (id[j] >= a.adapters) id[j] = -1;
-#pragma unroll
-    for (int i = 0; i < FF; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        acc[i][j][q] = __float_as_int(static_cast<float>(acc[i][j][q]) * sa * sb[i][q] + bi[i][q]);
   }
+  const int features = (a.N + 15) >> 4, blocks = a.rank / a.chunk;
+  const bool in = lane < 2 * a.chunk;  // (16 ranks fill half of a product's slots)
+#pragma unroll 1
   while (true) {
     int pick = -1;
 #pragma unroll
@@ -191,55 +152,64 @@ __device__ __forceinline__ void add_low_rank_terms(const IntMatmulArgs& a, int n
       if (pick < 0 && left) pick = __builtin_amdgcn_readlane(id[j], __ffsll(static_cast<unsigned long long>(left)) - 1);
     }
     if (pick < 0) break;
-    const uint16_t* up = a.up + static_cast<int64_t>(pick) * a.N * a.rank;
-    for (int r0 = 0; r0 < a.rank; r0 += 32) {
-      const int r = r0 + 8 * lg;
-      const bool in = r < a.rank;
-      i32x4 uf[FT][NT];
-      float down[FT];
-#pragma unroll
-      for (int j = 0; j < FT; ++j) {
-        float x[8];
-        if (in && id[j] == pick) {
-          load8<EL_F32>(a.u + static_cast<int64_t>(mw + 16 * j + lr) * a.rank + r, x);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = 0.f;
-        }
-        down[j] = split_u<NT>(a.up_bf16, x, uf[j]);
-      }
-#pragma unroll
-      for (int i = 0; i < FF; ++i) {
-        i32x4 w = {0, 0, 0, 0};
-        if (in) w = *reinterpret_cast<const i32x4*>(up + static_cast<int64_t>(min(nw + 16 * i + lr, a.N - 1)) * a.rank + r);
+    for (int block = 0; block < blocks; ++block)
+#pragma unroll 1
+      for (int r0 = 0; r0 < a.chunk; r0 += 32) {
+        i32x4 uf[FT][NT], w[FF];
+        float down[FT];
 #pragma unroll
         for (int j = 0; j < FT; ++j) {
-          f32x4 d = {0.f, 0.f, 0.f, 0.f};
+          const bool mine = id[j] == pick;
+          const int64_t at = static_cast<int64_t>((mw >> 4) + j) * blocks + block;
+          down[j] = mine ? a.uf[static_cast<int64_t>(mw + 16 * j + lr) * blocks + block] : 0.f;
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            if (a.up_bf16)
-              d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, uf[j][t]), d, 0, 0, 0);
-            else
-              d = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, w), __builtin_bit_cast(f16x8, uf[j][t]), d, 0, 0, 0);
+            uf[j][t] = i32x4{0, 0, 0, 0};
+            if (in && mine) uf[j][t] = *reinterpret_cast<const i32x4*>(a.ut + (at * NT + t) * a.chunk * 16 + r0 * 16 + lane * 8);
           }
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (id[j] == pick) acc[i][j][q] = __float_as_int(fmaf(d[q], down[j], __int_as_float(acc[i][j][q])));
         }
+#pragma unroll
+        for (int i = 0; i < FF; ++i) {
+          w[i] = i32x4{0, 0, 0, 0};
+          const uint16_t* up = a.up + (static_cast<int64_t>(pick) * features + min((nw >> 4) + i, features - 1)) * a.rank * 16;
+          if (in) w[i] = *reinterpret_cast<const i32x4*>(up + (block * a.chunk + r0) * 16 + lane * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < FF; ++i)
+#pragma unroll
+          for (int j = 0; j < FT; ++j) {
+            f32x4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              if constexpr (BF16)
+                p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[i]), __builtin_bit_cast(bf16x8, uf[j][t]), p, 0, 0, 0);
+              else
+                p = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, w[i]), __builtin_bit_cast(f16x8, uf[j][t]), p, 0, 0, 0);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (id[j] == pick) d[i][j][q] = fmaf(p[q], down[j], d[i][j][q]);
+          }
       }
-    }
 #pragma unroll
     for (int j = 0; j < FT; ++j)
       if (id[j] == pick) id[j] = -1;
   }
 }
 
-// 16-bit outputs round more than two terms leave out (bf16 2^-16, fp16 2^-22
-// of a token's largest u); fp32 outputs take three where the terms are bf16.
+// 16-bit outputs round more than two terms leave out (bf16 2^-17 of each u,
+// fp16 2^-22 of a token's largest); fp32 outputs take three where the terms
+// are bf16.
 template <int T, int FF, int FT>
-__device__ __forceinline__ void add_low_rank(const IntMatmulArgs& a, int nw, int mw, const f4 (&sb)[FF], const f4 (&bi)[FF],
-                                             i32x4 (&acc)[FF][FT]) {
-  add_low_rank_terms<T, FF, FT, T == EL_F32 ? 3 : 2>(a, nw, mw, sb, bi, acc);
+__device__ __forceinline__ void low_rank(const IntMatmulArgs& a, int nw, int mw, f32x4 (&d)[FF][FT]) {
+#pragma unroll
+  for (int i = 0; i < FF; ++i)
+#pragma unroll
+    for (int j = 0; j < FT; ++j) d[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (a.up_bf16)
+    low_rank_tile<true, T == EL_F32 ? 3 : 2>(a, nw, mw, d);
+  else
+    low_rank_tile<false, 2>(a, nw, mw, d);
 }
 
 // Four consecutive features n .. n + 3 of token m (n a multiple of 4).
@@ -345,7 +315,7 @@ __global__ __launch_bounds__(512) void int_matmul_few_kernel(const IntMatmulArgs
 constexpr int kStageK = 128;
 
 template <int T, int BF, int BT, int WF, int WT, int NS, bool DMA, bool ADAPT>
-__global__ __launch_bounds__(WF * WT * 64) void int_matmul_tile_kernel(const IntMatmulArgs a, int tf, int tt, int vec) {
+__global__ __launch_bounds__(WF * WT * 64, ADAPT ? 2 : 1) void int_matmul_tile_kernel(const IntMatmulArgs a, int tf, int tt, int vec) {
   typedef typename Elem<T>::type E;
   constexpr int NW = WF * WT;
   constexpr int FF = BF / WF / 16, FT = BT / WT / 16;
@@ -489,32 +459,61 @@ __global__ __launch_bounds__(WF * WT * 64) void int_matmul_tile_kernel(const Int
   __syncthreads();
   unsigned char* part = smem + wave * (NS * STAGE / NW);
   const int nw = n0 + wf * FF * 16, mw = m0 + wt * FT * 16;
-  f4 sb[FF], bi[FF];
-#pragma unroll
-  for (int i = 0; i < FF; ++i)
+  auto column_scales = [&](int i, f4& sb, f4& bi) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int n = min(nw + i * 16 + 4 * lg + e, a.N - 1);
-      sb[i][e] = a.sb[n];
-      bi[i][e] = a.bias ? a.bias[n] : 0.f;
+      sb[e] = a.sb[n];
+      bi[e] = a.bias ? a.bias[n] : 0.f;
     }
-  if constexpr (ADAPT) add_low_rank<T, FF, FT>(a, nw, mw, sb, bi, acc);
+  };
+  auto stage = [&](int i, int jj, const i32x4& sums, float sa, const f4& sb, const f4& bi, const f32x4& add) {
+    E e[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float v = static_cast<float>(sums[q]) * sa * sb[q] + bi[q];
+      if constexpr (ADAPT) v += add[q];
+      e[q] = static_cast<E>(activate<T>(v, a.act));
+    }
+    const int byte = (i * 16 + 4 * lg) * ES;
+    __builtin_memcpy(__builtin_assume_aligned(part + (jj * 16 + lr) * RC * 16 + (((byte >> 4) ^ (lr & (RC - 1))) << 4) + (byte & 15), 4 * ES),
+                     e, 4 * ES);
+  };
+  f4 sb[ADAPT ? 1 : FF], bi[ADAPT ? 1 : FF];
+  if constexpr (!ADAPT) {
+#pragma unroll
+    for (int i = 0; i < FF; ++i) column_scales(i, sb[i], bi[i]);
+  }
 #pragma unroll
   for (int j0 = 0; j0 < FT; j0 += CT) {
+    if constexpr (!ADAPT) {
 #pragma unroll
-    for (int jj = 0; jj < CT; ++jj) {
-      const float sa = a.sa[min(mw + (j0 + jj) * 16 + lr, a.M - 1)];
-      unsigned char* pr = part + (jj * 16 + lr) * RC * 16;
+      for (int jj = 0; jj < CT; ++jj) {
+        const float sa = a.sa[min(mw + (j0 + jj) * 16 + lr, a.M - 1)];
 #pragma unroll
-      for (int i = 0; i < FF; ++i) {
-        E e[4];
+        for (int i = 0; i < FF; ++i) stage(i, jj, acc[i][j0 + jj], sa, sb[i], bi[i], f32x4{});
+      }
+    } else {
+      // The low-rank terms of up to 4 x 2 blocks at a time, which is what the
+      // registers hold beside the sums.
+      constexpr int FI = FF < 4 ? FF : 4;
+      static_assert(CT % 2 == 0 && FF % FI == 0, "pairs of token blocks");
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float v = ADAPT ? __int_as_float(acc[i][j0 + jj][q]) : static_cast<float>(acc[i][j0 + jj][q]) * sa * sb[i][q] + bi[i][q];
-          e[q] = static_cast<E>(activate<T>(v, a.act));
+      for (int i0 = 0; i0 < FF; i0 += FI) {
+#pragma unroll
+        for (int jj = 0; jj < CT; jj += 2) {
+          f32x4 add[FI][2];
+          low_rank<T>(a, nw + 16 * i0, mw + (j0 + jj) * 16, add);
+#pragma unroll
+          for (int i = 0; i < FI; ++i) {
+            f4 sbv, biv;
+            column_scales(i0 + i, sbv, biv);
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+              stage(i0 + i, jj + p, acc[i0 + i][j0 + jj + p], a.sa[min(mw + (j0 + jj + p) * 16 + lr, a.M - 1)], sbv, biv, add[i][p]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        const int byte = (i * 16 + 4 * lg) * ES;
-        __builtin_memcpy(__builtin_assume_aligned(pr + (((byte >> 4) ^ (lr & (RC - 1))) << 4) + (byte & 15), 4 * ES), e, 4 * ES);
       }
     }
     wave_lds_sync();
@@ -598,12 +597,18 @@ static void go_tile(const IntMatmulArgs& a, hipStream_t s, Form& form) {
 //    more);
 //  * rows that are not 16-byte aligned go through registers in 64x64 tiles
 //    (689x1000x1501: 11.1; four waves 12.5, 128x64 17.4).
+static bool product_by_dma(const IntMatmulArgs& a) {
+  return a.K % 16 == 0 && a.lda % 16 == 0 && a.ldb % 16 == 0 && a.lda < (1 << 22) && a.ldb < (1 << 22) &&
+         (reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.b)) % 16 == 0;
+}
+static bool product_is_few(const IntMatmulArgs& a) {
+  return a.M <= 16 || static_cast<int64_t>(a.M) * a.N <= (product_by_dma(a) ? 1 << 17 : 1 << 18);
+}
 template <int T, bool ADAPT>
 static void go_int_matmul(const IntMatmulArgs& a, hipStream_t s, Form& form) {
   auto tiles = [&](int f, int t) { return static_cast<int64_t>((a.N + f - 1) / f) * ((a.M + t - 1) / t); };
-  const bool dma = a.K % 16 == 0 && a.lda % 16 == 0 && a.ldb % 16 == 0 && a.lda < (1 << 22) && a.ldb < (1 << 22) &&
-                   (reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.b)) % 16 == 0;
-  if (a.M <= 16 || static_cast<int64_t>(a.M) * a.N <= (dma ? 1 << 17 : 1 << 18)) {
+  const bool dma = product_by_dma(a);
+  if (product_is_few(a)) {
     if ((reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.b) | a.lda | a.ldb) % 4 == 0)
       go_few<T, false, ADAPT>(a, s, form);
     else

@@ -41,12 +41,17 @@ struct IntMatmulArgs {
   int64_t lda, ldb, ldy;
   int M, N, K;
   int act;            // VOC_ACT_*
-  // The adapters' part (adapters.hip): u[m][rank], up 16-bit [adapters][N][rank].
+  // The adapters' part (adapters.hip): up 16-bit, in the order of vocoder.h; the
+  // product of few tokens takes u[m][rank], the others terms of it of up's type,
+  // ut[m / 16][rank / chunk][terms][chunk / 8][m % 16][8], and the factors
+  // uf[m][rank / chunk].
   const float* u;
+  uint16_t* ut;
+  float* uf;
   const uint16_t* up;
-  const int32_t* adapter;  // of each row
-  int adapters, rank;      // rank: a multiple of 16
-  bool up_bf16;            // else fp16
+  const int32_t* adapter;    // of each row
+  int adapters, rank, chunk; // rank: 16, 32 or a multiple of chunk = 64
+  bool up_bf16;              // else fp16
 };
 hipError_t launch_int_matmul(int dtype, const IntMatmulArgs& a, hipStream_t s, Form& form);
 
@@ -54,11 +59,14 @@ hipError_t launch_int_matmul(int dtype, const IntMatmulArgs& a, hipStream_t s, F
 // then the product, which adds up_i u.
 struct AdaptArgs {
   IntMatmulArgs g;
-  const uint16_t* down;  // [adapters][rank][ldd]
-  int64_t ldd;
+  const uint16_t* down;  // [adapters][rank / 16][K / 64, rounded up][2][64][8]
   const float* scale;    // [adapters] or null
-  float* u;              // [M][rank]
+  void* ws;
+  // Set by the launch: where u goes, and its terms (0: fp32).
+  float* u;
+  int terms;
 };
+constexpr int64_t adapt_row_bytes(int rank) { return 6 * static_cast<int64_t>(rank) + 16; }  // of the workspace, at the most
 hipError_t launch_int_matmul_adapters(int dtype, const AdaptArgs& a, hipStream_t s, Form& form);
 
 // The cache and the sequences of one step, as every kernel reads them.

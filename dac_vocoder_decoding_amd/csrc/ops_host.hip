@@ -270,10 +270,8 @@ VOC_API voc_status vocoder_matmul_int_adapters(voc_ops* o, int out_dtype, int64_
   if (!ad) return fail(o, VOC_INVALID_PARAMS, "adapters is NULL");
   if (ad->dtype != VOC_F16 && ad->dtype != VOC_BF16) return fail(o, VOC_INVALID_PARAMS, "adapters hold fp16 or bf16");
   if (ad->count < 1 || ad->count > (1 << 24)) return fail(o, VOC_INVALID_PARAMS, "the number of adapters is out of range");
-  if (ad->rank < 16 || ad->rank > 256 || ad->rank % 16)
-    return fail(o, VOC_INVALID_PARAMS, "the adapters' rank must be a multiple of 16 up to 256");
-  if (!stride_ok(ad->down_stride, K) || ad->down_stride % 8)
-    return fail(o, VOC_INVALID_PARAMS, "down_stride must be a multiple of 8, at least K");
+  if (ad->rank != 16 && ad->rank != 32 && (ad->rank < 64 || ad->rank > 256 || ad->rank % 64))
+    return fail(o, VOC_INVALID_PARAMS, "the adapters' rank must be 16, 32, 64, 128, 192 or 256");
   if (M == 0 || N == 0) return VOC_OK;
   if (!ad->down || !ad->up || !adapter) return fail(o, VOC_INVALID_PARAMS, "NULL pointer");
   if (!aligned(ad->down, 16) || !aligned(ad->up, 16) || !aligned(ad->scale, 4) || !aligned(adapter, 4))
@@ -281,18 +279,16 @@ VOC_API voc_status vocoder_matmul_int_adapters(voc_ops* o, int out_dtype, int64_
   AdaptArgs p{};
   p.g = IntMatmulArgs{a, b, a_scale, b_scale, bias, y, lda, ldb, ldy, static_cast<int>(M), static_cast<int>(N),
                       static_cast<int>(K), act};
-  p.u = static_cast<float*>(o->ws);
-  p.g.u = p.u;
+  p.ws = o->ws;
   p.g.up = static_cast<const uint16_t*>(ad->up);
   p.g.adapter = adapter;
   p.g.adapters = ad->count;
   p.g.rank = ad->rank;
   p.g.up_bf16 = ad->dtype == VOC_BF16;
   p.down = static_cast<const uint16_t*>(ad->down);
-  p.ldd = ad->down_stride;
   p.scale = ad->scale;
-  // As many rows at a time as the workspace holds u of (at least 131072).
-  const int64_t most = VOC_OPS_WORKSPACE_BYTES / (4 * ad->rank) & ~int64_t(1023);
+  // As many rows at a time as the workspace holds u of (at least 86016).
+  const int64_t most = VOC_OPS_WORKSPACE_BYTES / adapt_row_bytes(ad->rank) & ~int64_t(1023);
   return on_device(o, "matmul_int_adapters", [&] {
     for (int64_t m = 0; m < M; m += most) {
       AdaptArgs part = p;

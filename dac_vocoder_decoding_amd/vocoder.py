@@ -99,7 +99,6 @@ class voc_adapters(ctypes.Structure):
         ("dtype", ctypes.c_int),
         ("count", ctypes.c_int),
         ("rank", ctypes.c_int),
-        ("down_stride", ctypes.c_int64),
         ("down", ctypes.c_void_p),
         ("up", ctypes.c_void_p),
         ("scale", ctypes.c_void_p),
@@ -780,8 +779,8 @@ def matmul_int(ops, a, a_scale, b, b_scale, bias=None, gelu: bool = False, dtype
 class Adapters:
     """Low-rank adapters of one product (voc_adapters): down [count, rank, K]
     and up [count, N, rank], both float16 or bfloat16, and scale fp32 [count]
-    (default 1).  They are laid out once, in tensors of their own with the rank
-    padded to a multiple of 16 and K to one of 8 by zeros; `set` replaces one."""
+    (default 1).  They are laid out once, in tensors of their own and in the
+    order that the kernels read, padded by zeros; `set` replaces one."""
 
     def __init__(self, down, up, scale=None):
         import torch
@@ -796,21 +795,32 @@ class Adapters:
         self.N = up.shape[1]
         if not (self.count and self.K and self.N) or not 1 <= self.rank <= 256:
             raise ValueError("adapters: ranks of 1 to 256, and at least one adapter, input and output are needed")
-        rank, stride = -(-self.rank // 16) * 16, -(-self.K // 8) * 8
+        rank = 16 if self.rank <= 16 else 32 if self.rank <= 32 else -(-self.rank // 64) * 64
         self.device = down.get_device()
-        self.down = torch.zeros(self.count, rank, stride, dtype=down.dtype, device=down.device)
-        self.up = torch.zeros(self.count, self.N, rank, dtype=up.dtype, device=up.device)
+        # [adapter][16 ranks][64 inputs][their halves of 8][4 groups of 16][rank][8]
+        self.down = torch.zeros(self.count, rank // 16, -(-self.K // 64), 2, 4, 16, 8, dtype=down.dtype, device=down.device)
+        # [adapter][16 features][8 ranks][feature][8]
+        self.up = torch.zeros(self.count, -(-self.N // 16), rank // 8, 16, 8, dtype=up.dtype, device=up.device)
         self.scale = torch.ones(self.count, device=down.device)
-        self.down[:, :self.rank, :self.K] = down
-        self.up[:, :, :self.rank] = up
+        for i in range(self.count):
+            self._lay(i, down[i], up[i])
         if scale is not None:
             if scale.shape != (self.count,) or scale.device != down.device:
                 raise ValueError(f"adapters: scale [{self.count}] on {down.device} is needed")
             self.scale.copy_(scale)
         self.tensors = self.down, self.up, self.scale
-        self.c = voc_adapters(VOC_F16 if down.dtype == torch.float16 else VOC_BF16, self.count, rank, stride,
-                              self.down.data_ptr(), self.up.data_ptr(), self.scale.data_ptr())
+        self.c = voc_adapters(VOC_F16 if down.dtype == torch.float16 else VOC_BF16, self.count, rank, self.down.data_ptr(),
+                              self.up.data_ptr(), self.scale.data_ptr())
         self.ref = ctypes.byref(self.c)
+
+    def _lay(self, index: int, down, up) -> None:
+        _, blocks, steps, _, _, _, _ = self.down.shape
+        rows = down.new_zeros(blocks * 16, steps * 64)
+        rows[:down.shape[0], :self.K] = down
+        self.down[index] = rows.view(blocks, 16, steps, 4, 2, 8).permute(0, 2, 4, 3, 1, 5)
+        rows = up.new_zeros(self.up.shape[1] * 16, blocks * 16)
+        rows[:self.N, :up.shape[1]] = up
+        self.up[index] = rows.view(-1, 16, blocks * 2, 8).transpose(1, 2)
 
     def set(self, index: int, down, up, scale: float = 1.0) -> None:
         """Replaces adapter `index` by down [r, K] and up [N, r] (r up to the
@@ -820,10 +830,7 @@ class Adapters:
             raise ValueError(f"adapter {index}: there are {self.count}")
         if r > self.rank or tuple(down.shape) != (r, self.K) or tuple(up.shape) != (self.N, r):
             raise ValueError(f"adapter: down [r, {self.K}] and up [{self.N}, r], r up to {self.rank}, are needed")
-        self.down[index].zero_()
-        self.up[index].zero_()
-        self.down[index, :r, :self.K] = down
-        self.up[index, :, :r] = up
+        self._lay(index, down, up)
         self.scale[index] = scale
 
 

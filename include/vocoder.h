@@ -563,19 +563,23 @@ voc_status vocoder_matmul_int(voc_ops *ops, int out_dtype, int64_t M, int64_t N,
  * down and up hold dtype VOC_F16 or VOC_BF16; u and every sum are fp32.  For
  * the matrix cores u is split into terms of the weights' dtype, fp16 two (22
  * bits of a row's largest), bf16 two (16 bits) or, for fp32 outputs, three.
- * rank: a multiple of 16 up to 256 (smaller adapters are padded with zeros);
- * down_stride: elements between rows of down, at least K, a multiple of 8,
- * the values between K and the next multiple of 8 readable; down and up are
- * 16-byte aligned.  scale: fp32 [count], or NULL for 1.
+ * rank: 16, 32, 64, 128, 192 or 256 (others are padded with zeros).  down is
+ * held in the order in which a wave reads it, with K padded by zeros to
+ * 64 S, S = (K + 63) / 64: down[i][r][k] with r = 16 p + lr and
+ * k = 64 s + 16 lg + 8 h + e (lr < 16, lg < 4, h < 2, e < 8) is element
+ *   ((((i rank / 16 + p) S + s) 2 + h) 64 + 16 lg + lr) 8 + e.
+ * and up, with N padded by zeros to 16 S, S = (N + 15) / 16: up[i][n][r] with
+ * n = 16 p + f (f < 16) and r = 8 c + e (e < 8) is element
+ *   ((i S + p) rank / 8 + c) 128 + 8 f + e.
+ * Both are 16-byte aligned.  scale: fp32 [count], or
+ * NULL for 1.
  * Uses the handle's workspace.
  * Errors: VOC_INVALID_PARAMS, VOC_DEVICE_ERROR.
  */
 typedef struct voc_adapters {
   int dtype, count, rank;
-  int64_t down_stride;
-  const void *down;   /* [count][rank][down_stride] */
-  const void *up;     /* [count][N][rank] */
-  const float *scale; /* [count] or NULL */
+  const void *down, *up;
+  const float *scale;
 } voc_adapters;
 voc_status vocoder_matmul_int_adapters(voc_ops *ops, int out_dtype, int64_t M, int64_t N,
                                        int64_t K, const int8_t *a, int64_t lda,

@@ -129,8 +129,9 @@ def test_adapters_that_are_not_finite_stay_with_their_rows(ops):
         a, sa, b, sb, ads, down, up = case(g, M, N, K, 16, 3, F16)
         ids = numbers(g, M, 3, "any")
         want = V.matmul_int_adapters(ops, a, sa, b, sb, ads, ids, dtype=F32)
-        ads.down[1, 3, 5] = float("nan")
-        ads.up[2, 7, 2] = float("inf")
+        down[1, 3, 5], up[2, 7, 2] = float("nan"), float("inf")
+        for i in (1, 2):
+            ads.set(i, down[i], up[i], ads.scale[i].item())
         y = V.matmul_int_adapters(ops, a, sa, b, sb, ads, ids, dtype=F32)
         assert y[ids == 1].isnan().all()
         assert not y[ids == 2][:, 7].isfinite().any()
@@ -220,8 +221,8 @@ def test_adapters_refusals(ops):
 
     held = dict(dtype=V.VOC_F32)
     for kw in (dict(M=-1), dict(K=0), dict(act=2), dict(a=None), dict(adapter=None), dict(adapter=ids.data_ptr() + 2), dict(y=None),
-               dict(ref=0), dict(count=0), dict(count=-1), dict(rank=0), dict(rank=8), dict(rank=24), dict(rank=272),
-               dict(down_stride=63), dict(down_stride=68), dict(down=None), dict(up=None), dict(down=w.data_ptr() + 8),
+               dict(ref=0), dict(count=0), dict(count=-1), dict(rank=0), dict(rank=8), dict(rank=24), dict(rank=48), dict(rank=96), dict(rank=320),
+               dict(down=None), dict(up=None), dict(down=w.data_ptr() + 8),
                dict(up=w.data_ptr() + 2), dict(scale=s.data_ptr() + 1), dict(M=1 << 24, N=1 << 24)):
         assert mm(**kw) == V.VOC_INVALID_PARAMS, kw
         assert V.voc_ops_last_error(ops), kw
