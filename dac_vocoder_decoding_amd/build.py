@@ -17,7 +17,8 @@ OUT = os.path.join(HERE, "libvocoder.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["conv_gemm.hip", "fused_ru.hip", "stream_kernels.hip", "peak_kernels.hip", "runtime.hip",
            "host_config.cpp", "rows_kernels.hip", "int_matmul.hip", "cache_kernels.hip", "attention.hip",
-           "adapters.hip", "heads_kernels.hip", "cache_read.hip", "ops_host.hip"]
+           "adapters.hip", "heads_kernels.hip", "step_f32.hip",
+           "step_bf16.hip", "step_f16.hip", "cache_read.hip", "ops_host.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",

@@ -47,4 +47,19 @@ __device__ __forceinline__ uint32_t rescaled4(uint32_t c, float ratio) {
   return r;
 }
 
+// Eight codes in a row, codes8's own bits, of values that all lie within the
+// page's scale (inv > 0: they are finite, and |v inv| rounds to 127 at the
+// most): 1.5 2^23 added to the rounded product leaves its nearest integer, ties
+// to even, in the sum's low bits.
+__device__ __forceinline__ uint2 codes8_within(const float (&v)[8], float inv) {
+#pragma clang fp contract(off)
+  uint32_t t[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) t[k] = __float_as_uint(v[k] * inv + 12582912.f);
+  auto four = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0c0c0400u), __builtin_amdgcn_perm(b, a, 0x0c0c0400u), 0x05040100u);
+  };
+  return inv > 0.f ? make_uint2(four(t[0], t[1], t[2], t[3]), four(t[4], t[5], t[6], t[7])) : make_uint2(0, 0);
+}
+
 }  // namespace voc

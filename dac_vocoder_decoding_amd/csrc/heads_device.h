@@ -1,0 +1,344 @@
+// heads_device.h -- device building blocks of the RMS norm of each head with
+// the rotation by position.
+//
+//   y = x / sqrt(mean(x^2) + eps) * w           (over a head's D values)
+//   (a, b) -> (a cos - b sin, b cos + a sin)    for each of F pairs of y,
+//   angle = position * freq[pair]
+//
+// A head's values lie in units of eight, one a lane: four pairs where values
+// rotate, eight values in a row behind them.  G lanes (a power of two) hold a
+// head, so that its sum is a shuffle among them.
+#pragma once
+#include "cache_device.h"
+
+namespace voc {
+
+// How a unit's pairs lie: 2i, 2i + 1 or i, i + F, both read in whole words;
+// or either of them at any alignment and F, value by value.
+enum Pairs { kAdjacent = 0, kHalves = 1, kAny = 2 };
+
+// Two fours of consecutive elements (aligned to their size) at the even and the
+// odd places.
+template <int T>
+__device__ __forceinline__ void load_fours(const typename Elem<T>::type* p, const typename Elem<T>::type* q, float (&v)[8]) {
+  typename Elem<T>::type e[4], f[4];
+  __builtin_memcpy(e, __builtin_assume_aligned(p, sizeof(e)), sizeof(e));
+  __builtin_memcpy(f, __builtin_assume_aligned(q, sizeof(f)), sizeof(f));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = static_cast<float>(e[i]);
+    v[2 * i + 1] = static_cast<float>(f[i]);
+  }
+}
+template <int T>
+__device__ __forceinline__ void store_fours(typename Elem<T>::type* p, typename Elem<T>::type* q, const float (&v)[8]) {
+  typename Elem<T>::type e[4], f[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    e[i] = static_cast<typename Elem<T>::type>(v[2 * i]);
+    f[i] = static_cast<typename Elem<T>::type>(v[2 * i + 1]);
+  }
+  __builtin_memcpy(__builtin_assume_aligned(p, sizeof(e)), e, sizeof(e));
+  __builtin_memcpy(__builtin_assume_aligned(q, sizeof(f)), f, sizeof(f));
+}
+
+// The place of a lane's unit in its head.
+template <int MODE>
+struct Unit {
+  int at, hi;      // MODE < kAny: first value (kHalves: of the first and the second four)
+  int unit, F, D;  // kAny
+  bool adjacent, live, turns;
+  __device__ __forceinline__ Unit(int u, int F, int D, bool adjacent)
+      : unit(u), F(F), D(D), adjacent(MODE == kAdjacent || (MODE == kAny && adjacent)) {
+    const int turning = (F + 3) >> 2;
+    turns = u < turning;
+    if constexpr (MODE == kHalves) {
+      at = turns ? 4 * u : 8 * u;
+      hi = turns ? F + 4 * u : 8 * u + 4;
+    } else {
+      at = 8 * u;
+      hi = at + 4;
+    }
+    live = turns || 2 * F + 8 * (u - turning) < D;
+  }
+  // The value that sits at place k of the unit, or -1.
+  __device__ __forceinline__ int value(int k) const {
+    if (turns) {
+      const int p = 4 * unit + (k >> 1);
+      return p >= F ? -1 : adjacent ? 2 * p + (k & 1) : p + (k & 1) * F;
+    }
+    const int d = 2 * F + 8 * (unit - ((F + 3) >> 2)) + (adjacent ? k : (k >> 1) + 4 * (k & 1));
+    return d < D ? d : -1;
+  }
+  // Places 2i and 2i + 1 are a pair; behind pairs of halves the first four
+  // values have the even places.
+  template <int T>
+  __device__ __forceinline__ void load(const typename Elem<T>::type* head, float (&v)[8]) const {
+    if constexpr (MODE == kAny) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int d = value(k);
+        v[k] = d >= 0 ? static_cast<float>(head[d]) : 0.f;
+      }
+    } else if (!live) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = 0.f;
+    } else if constexpr (MODE == kAdjacent) {
+      load8<T>(head + at, v);
+    } else {
+      load_fours<T>(head + at, head + hi, v);
+    }
+  }
+  template <int T>
+  __device__ __forceinline__ void store(typename Elem<T>::type* head, const float (&v)[8]) const {
+    if constexpr (MODE == kAny) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int d = value(k);
+        if (d >= 0) head[d] = static_cast<typename Elem<T>::type>(v[k]);
+      }
+    } else if (live) {
+      if constexpr (MODE == kAdjacent) {
+        store8<T>(head + at, v);
+      } else {
+        store_fours<T>(head + at, head + hi, v);
+      }
+    }
+  }
+  // The same of values as they are stored (MODE < kAny, a unit that is there),
+  // to be widened later.
+  template <class E>
+  __device__ __forceinline__ void load_raw(const E* head, E (&e)[8]) const {
+    if constexpr (MODE == kAdjacent) {
+      __builtin_memcpy(e, __builtin_assume_aligned(head + at, 16), 8 * sizeof(E));
+    } else {
+      __builtin_memcpy(e, __builtin_assume_aligned(head + at, 4 * sizeof(E)), 4 * sizeof(E));
+      __builtin_memcpy(e + 4, __builtin_assume_aligned(head + hi, 4 * sizeof(E)), 4 * sizeof(E));
+    }
+  }
+  template <class E>
+  __device__ __forceinline__ void widen(const E (&e)[8], float (&v)[8]) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = static_cast<float>(e[MODE == kHalves ? (k >> 1) + 4 * (k & 1) : k]);
+  }
+  // The unit's codes into a row of D codes.
+  __device__ __forceinline__ void store_codes(int8_t* row, const float (&v)[8], float inv) const {
+    if constexpr (MODE == kAdjacent) {
+      if (live) *reinterpret_cast<uint2*>(row + at) = codes8_within(v, inv);
+    } else if constexpr (MODE == kHalves) {
+      if (!live) return;
+      const float o[8] = {v[0], v[2], v[4], v[6], v[1], v[3], v[5], v[7]};
+      const uint2 c = codes8_within(o, inv);
+      *reinterpret_cast<uint32_t*>(row + at) = c.x;
+      *reinterpret_cast<uint32_t*>(row + hi) = c.y;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int d = value(k);
+        if (d >= 0) row[d] = static_cast<int8_t>(code_of(v[k], inv));
+      }
+    }
+  }
+};
+
+// cos and sin of `turns` (revolutions): the fraction of a quarter turn in 64
+// bits, where a far position's angle keeps its places (at 2^20 radians fp32
+// holds steps of 1/16), the rest in fp32.  The polynomials are minimax fits of
+// sin(pi t / 2) and cos(pi t / 2) over |t| <= 1/2 (errors 3e-12 and 5e-11).
+__device__ __forceinline__ void cos_sin(double turns, float& c, float& s) {
+  const double r = (turns - __builtin_rint(turns)) * 4.0;
+  const double q = __builtin_rint(r);
+  const float t = static_cast<float>(r - q), z = t * t;
+  float a = fmaf(z, 0.000158206531f, -0.00468126638f);
+  a = fmaf(z, a, 0.0796925798f);
+  a = fmaf(z, a, -0.645964086f);
+  const float sn = fmaf(t, 1.57079637f, t * z * a);
+  float b = fmaf(z, 0.000903629872f, -0.0208600704f);
+  b = fmaf(z, b, 0.253669202f);
+  b = fmaf(z, b, -1.23370051f);
+  const float cn = fmaf(z, b, 1.f);
+  const int quarter = static_cast<int>(q) & 3;
+  const float x = quarter & 1 ? sn : cn, y = quarter & 1 ? cn : sn;
+  c = quarter == 1 || quarter == 2 ? -x : x;
+  s = quarter >= 2 ? -y : y;
+}
+
+// The sum over a head's G lanes, the same bits in each.
+template <int CTRL>
+__device__ __forceinline__ float plus_lane(float x) {
+  return x + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), CTRL, 0xf, 0xf, true));
+}
+template <int G>
+__device__ __forceinline__ float head_sum(float x) {
+  x = plus_lane<0xb1>(x);                      // lane ^ 1
+  x = plus_lane<0x4e>(x);                      // lane ^ 2
+  if constexpr (G > 4) x = plus_lane<0x141>(x);   // the other four of eight, mirrored
+  if constexpr (G > 8) x = plus_lane<0x140>(x);   // the other eight of sixteen, mirrored
+  if constexpr (G > 16) x += __shfl_xor(x, 16);
+  if constexpr (G > 32) x += __shfl_xor(x, 32);
+  return x;
+}
+
+// A lane's part of the rotation: its pairs' frequencies in revolutions.
+struct Frequencies {
+  double f[4];
+  template <int MODE>
+  __device__ __forceinline__ Frequencies(const HeadShape& h, const Unit<MODE>& u) {
+    constexpr double kTurn = 0.15915494309189535;  // 1 / (2 pi)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = 4 * u.unit + i;
+      f[i] = p < h.pairs ? static_cast<double>(h.freq[p]) * kTurn : 0.0;
+    }
+  }
+  __device__ __forceinline__ void at(int position, float (&c)[4], float (&s)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cos_sin(static_cast<double>(position) * f[i], c[i], s[i]);
+  }
+  // By the hardware's functions of a fraction of a turn, for what becomes codes
+  // of 7 bits.
+  __device__ __forceinline__ void coarse(int position, float (&c)[4], float (&s)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const double turns = static_cast<double>(position) * f[i];
+      const float r = static_cast<float>(turns - __builtin_rint(turns));
+      c[i] = __builtin_amdgcn_cosf(r);
+      s[i] = __builtin_amdgcn_sinf(r);
+    }
+  }
+};
+
+template <int MODE>
+__device__ __forceinline__ void load_weight(const Unit<MODE>& u, const float* w, float (&v)[8]) {
+  if (w) {
+    u.template load<EL_F32>(w, v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = 1.f;
+  }
+}
+
+// The norm's weights and the rotation of one position in one matrix a pair:
+// (a, b) -> (a ac - b bs, b bc + a as).
+struct Turn {
+  float ac[4], bs[4], bc[4], as[4];
+  __device__ __forceinline__ void set(const float (&w)[8], const float (&c)[4], const float (&s)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ac[i] = w[2 * i] * c[i];
+      bs[i] = w[2 * i + 1] * s[i];
+      bc[i] = w[2 * i + 1] * c[i];
+      as[i] = w[2 * i] * s[i];
+    }
+  }
+};
+
+// One head in place: the norm, then the rotation.  A head with a norm whose sum
+// of squares is not finite becomes NaN; without one, values that do not rotate
+// stay as they are.
+template <int G, int MODE>
+__device__ __forceinline__ void turn(const HeadShape& h, const Unit<MODE>& u, bool norm, const Turn& m, float (&v)[8]) {
+  if (norm) {
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum = fmaf(v[k], v[k], sum);  // (the same steps whatever the alignment)
+    sum = head_sum<G>(sum);
+    float rms = __builtin_amdgcn_rsqf(fmaf(sum, h.per, h.eps));
+    if (abs_bits(sum) >= kInfBits) rms = __uint_as_float(0x7fc00000u);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= rms;
+  }
+  if (norm || u.turns) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = v[2 * i], b = v[2 * i + 1];
+      v[2 * i] = fmaf(a, m.ac[i], -(b * m.bs[i]));
+      v[2 * i + 1] = fmaf(b, m.bc[i], a * m.as[i]);
+    }
+  }
+}
+
+// The same with the weights and the angles apart, where they are kept for many
+// heads of many tokens.
+template <int G, int MODE>
+__device__ __forceinline__ void turn(const HeadShape& h, const Unit<MODE>& u, bool norm, const float (&w)[8],
+                                     const float (&c)[4], const float (&s)[4], float (&v)[8]) {
+  if (norm) {
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum = fmaf(v[k], v[k], sum);
+    sum = head_sum<G>(sum);
+    float rms = __builtin_amdgcn_rsqf(fmaf(sum, h.per, h.eps));
+    if (abs_bits(sum) >= kInfBits) rms = __uint_as_float(0x7fc00000u);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= rms * w[k];
+  }
+  if (u.turns) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = v[2 * i], b = v[2 * i + 1];
+      v[2 * i] = fmaf(a, c[i], -(b * s[i]));
+      v[2 * i + 1] = fmaf(b, c[i], a * s[i]);
+    }
+  }
+}
+
+// A wave turns one token's heads of a set: rounds first, first + step, .. of
+// 64 / G heads each.  The loads of two rounds are in flight
+// together (of one as fast, of four 44 us for 36: 10336 x 40 heads x 128 bf16).
+template <int T, int MODE, int G>
+__device__ __forceinline__ void turn_set(const HeadShape& h, const Unit<MODE>& u, const HeadSet& set, const Turn& m,
+                                         int64_t row, int first, int step) {
+  typedef typename Elem<T>::type E;
+  constexpr int GW = 64 / G, ROUNDS = 2;
+  const int lane = threadIdx.x & 63;
+  const E* x = static_cast<const E*>(set.x) + row * set.x_t;
+  E* y = static_cast<E*>(set.y) + row * set.y_t;
+  for (int r = first; r * GW < set.heads; r += ROUNDS * step) {
+    float v[ROUNDS][8];
+#pragma unroll
+    for (int n = 0; n < ROUNDS; ++n) {
+      const int head = (r + n * step) * GW + lane / G;
+      if (head < set.heads) u.template load<T>(x + head * set.x_h, v[n]);
+    }
+#pragma unroll
+    for (int n = 0; n < ROUNDS; ++n) {
+      const int head = (r + n * step) * GW + lane / G;
+      if (head >= set.heads) continue;  // (a whole group of lanes: the sums stay inside one)
+      turn<G>(h, u, set.w != nullptr, m, v[n]);
+      u.template store<T>(y + head * set.y_h, v[n]);
+    }
+  }
+}
+
+// What a wave keeps over the tokens that it turns.
+template <int T, int MODE, int G>
+struct Turner {
+  Unit<MODE> u;
+  Frequencies f;
+  float wq[8], wk[8];
+  __device__ __forceinline__ Turner(const HeadShape& h, const HeadSet& q, const HeadSet& k)
+      : u((threadIdx.x & 63) % G, h.pairs, h.D, h.adjacent), f(h, u) {
+    load_weight(u, q.w, wq);
+    load_weight(u, k.w, wk);
+  }
+  // A token's heads, this wave's share of them: rounds part, part + parts, ..
+  // of the queries' and then the keys' heads.
+  __device__ __forceinline__ void token(const HeadShape& h, const HeadSet& q, const HeadSet& k, int64_t row, int position,
+                                        int part, int parts) const {
+    float c[4], s[4];
+    f.at(position, c, s);
+    Turn m;
+    const int rounds = (q.heads + 64 / G - 1) / (64 / G);
+    if (q.heads) {
+      m.set(wq, c, s);
+      turn_set<T, MODE, G>(h, u, q, m, row, part, parts);
+    }
+    if (k.heads) {
+      m.set(wk, c, s);
+      turn_set<T, MODE, G>(h, u, k, m, row, (part + parts - rounds % parts) % parts, parts);
+    }
+  }
+};
+
+}  // namespace voc

@@ -125,7 +125,7 @@ struct HeadShape {
   const float* freq;
   int D, pairs;  // the first 2 * pairs values rotate
   int adjacent;  // pairs 2i, 2i + 1; else i, i + pairs
-  float eps;
+  float eps, per;  // per: 1 / D
 };
 constexpr int kHeadMaxD = 256;
 struct NormRotateArgs {
@@ -144,7 +144,7 @@ struct StepArgs {
   int64_t v_t, v_h;
   int batch;
 };
-int64_t step_workgroups(const StepArgs& a);  // of one sequence, at the most
+int64_t step_workgroups(int dtype, const StepArgs& a);  // of one sequence
 hipError_t launch_step(int dtype, const StepArgs& a, hipStream_t s, Form& form);
 
 struct ReadArgs {

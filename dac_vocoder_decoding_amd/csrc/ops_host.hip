@@ -155,7 +155,7 @@ voc_status check_heads(voc_ops* o, int dtype, int head_dim, const float* freq, i
   if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(o, VOC_INVALID_PARAMS, "eps must be finite and not negative");
   if (pairs && !freq) return fail(o, VOC_INVALID_PARAMS, "freq is NULL");
   if (!aligned(freq, 4)) return fail(o, VOC_INVALID_PARAMS, "freq must be 4-byte aligned");
-  *h = HeadShape{freq, head_dim, pairs, adjacent, eps};
+  *h = HeadShape{freq, head_dim, pairs, adjacent, eps, 1.f / static_cast<float>(head_dim)};
   return VOC_OK;
 }
 
@@ -352,7 +352,7 @@ VOC_API voc_status vocoder_norm_rotate_append(voc_ops* o, const voc_kv_cache* ca
   a.v_t = v_t;
   a.v_h = v_h;
   a.batch = static_cast<int>(batch->batch);
-  if (step_workgroups(a) * a.batch >= 1 << 24) return fail(o, VOC_INVALID_PARAMS, "too many tokens for one call");
+  if (step_workgroups(dtype, a) * a.batch >= 1 << 23) return fail(o, VOC_INVALID_PARAMS, "too many tokens for one call");
   return on_device(o, "norm_rotate_append", [&] { return launch_step(dtype, a, static_cast<hipStream_t>(hip_stream), o->form); });
 }
 

@@ -1,0 +1,372 @@
+// step_kernels.h -- norm and rotation of new queries and keys, the keys
+// quantised straight into the paged 8-bit cache beside the values.
+#pragma once
+#include <type_traits>
+
+#include "heads_device.h"
+#include "step_plan.h"
+
+namespace voc {
+
+// Workgroup roles along x: the pages that a sequence's new tokens touch times
+// its cache heads, keys and then values; behind them the queries.
+template <int T, int MODE, int G>
+__global__ __launch_bounds__(256) void step_few_kernel(const StepArgs a, int pages, int parts) {
+  typedef typename Elem<T>::type E;
+  constexpr int TC = 256 / G;  // tokens at a time
+  __shared__ uint32_t s_max[4];
+  const int tid = threadIdx.x;
+  const int b = blockIdx.y;
+  const int cached = pages * 2 * a.c.heads;
+  if (static_cast<int>(blockIdx.x) >= cached) {
+    const Seq s = load_seq(a.c, b);
+    const int wave = (blockIdx.x - cached) * 4 + (tid >> 6), i = wave / parts;
+    if (i < s.count) Turner<T, MODE, G>(a.h, a.q, HeadSet{}).token(a.h, a.q, HeadSet{}, s.start + i, s.past + i, wave % parts, parts);
+    return;
+  }
+  const int j = blockIdx.x / (2 * a.c.heads), y = blockIdx.x % (2 * a.c.heads), head = y >> 1;
+  const bool value = y & 1;
+  const PageShare sh = page_share(a.c, b, j, head);
+  const int lo = sh.lo, hi = sh.hi;
+  if (hi <= lo) return;
+  const int P = 1 << a.c.page_log, D = a.h.D;
+  int8_t* codes = (value ? a.c.v : a.c.k) + sh.slot * P * D;
+  float* scales = value ? a.c.vs : a.c.ks;
+  const float old = lo ? scales[sh.slot] : 0.f;
+  const Unit<MODE> u(tid % G, value ? 0 : a.h.pairs, D, a.h.adjacent);
+  float w[8];
+  load_weight(u, value ? nullptr : a.k.w, w);
+  const Frequencies f(a.h, u);
+  const E* src = (value ? static_cast<const E*>(a.v) + head * a.v_h : static_cast<const E*>(a.k.x) + head * a.k.x_h) +
+                 (sh.token - lo) * (value ? a.v_t : a.k.x_t);
+  const int64_t st = value ? a.v_t : a.k.x_t;
+  float v[8];
+  auto load = [&](int t) {
+    u.template load<T>(src + t * st, v);
+    if (!value) {
+      float c[4], s[4];
+      f.at(static_cast<int>(sh.first) + t, c, s);
+      Turn m;
+      m.set(w, c, s);
+      turn<G>(a.h, u, a.k.w != nullptr, m, v);
+    }
+  };
+  uint32_t top = 0;
+  for (int t = lo + tid / G; t < hi; t += TC) {
+    load(t);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max(top, abs_bits(v[k]));
+  }
+  top = wave_max(top);
+  if ((tid & 63) == 0) s_max[tid >> 6] = top;
+  __syncthreads();
+  top = max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3]));
+  const float scale = joint_scale(old, top), inv = inverse_of(scale);
+  if (lo && scale != old) {
+    const float ratio = inv > 0.f ? old * inv : 0.f;
+    for (int i = tid; i < lo * D; i += 256) {
+      const int t = i / D, d = i - t * D;
+      int8_t* p = codes + (value ? d * P + t : i);
+      *p = static_cast<int8_t>(__builtin_rintf(static_cast<float>(*p) * ratio));
+    }
+  }
+  for (int t = lo + tid / G; t < hi; t += TC) {
+    if (hi - lo > TC) load(t);  // (else its values are still here)
+    if (!value) {
+      u.store_codes(codes + static_cast<int64_t>(t) * D, v, inv);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int d = u.value(k);
+        if (d >= 0) codes[static_cast<int64_t>(d) * P + t] = static_cast<int8_t>(code_of(v[k], inv));
+      }
+    }
+  }
+  if (tid == 0) scales[sh.slot] = scale;
+}
+
+// The largest magnitude of eight values as the bits of an fp32 number (16-bit
+// values compare like their bits too, NaN above infinity above the others).
+template <int T>
+__device__ __forceinline__ uint32_t raw_max(const typename Elem<T>::type (&e)[8]) {
+  if constexpr (T == EL_F32) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max(top, abs_bits(e[k]));
+    return top;
+  } else {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    uint32_t w[4];
+    __builtin_memcpy(w, e, 16);
+    u16x2 m = __builtin_bit_cast(u16x2, w[0] & 0x7fff7fffu);
+#pragma unroll
+    for (int k = 1; k < 4; ++k) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[k] & 0x7fff7fffu));
+    const unsigned short top = m[0] > m[1] ? m[0] : m[1];
+    return abs_bits(static_cast<float>(__builtin_bit_cast(typename Elem<T>::type, top)));
+  }
+}
+
+// Many new tokens, rows of whole words.  A workgroup takes one page for some of
+// the cache heads, keys or values; WPP waves a page and head, NP units of eight
+// values a lane, so that the rows stay in registers between their largest value
+// and their codes.  The angles of the page's tokens are worked out once for all
+// of its heads.  Keys go out as they lie; values are turned over in LDS
+// ([d][token], rows of P + 4 bytes) and stored whole.  Queries as above.
+template <int T, int MODE, int G, int WPP, int NP>
+__global__ __launch_bounds__(WPP < 4 ? 256 : 64 * WPP, NP > 4 ? 2 : 4) void step_page_kernel(const StepArgs a, int pages, int groups, int per,
+                                                                            int parts) {
+  typedef typename Elem<T>::type E;
+  constexpr int NW = WPP < 4 ? 4 : WPP, TOGETHER = NW / WPP;  // page and head pairs at a time
+  constexpr int LANES = 64 * WPP, STEP = LANES / G;           // tokens a pass
+  extern __shared__ __attribute__((aligned(16))) unsigned char s_page[];
+  __shared__ uint32_t s_max[2][NW];
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const int b = blockIdx.y, jobs = pages * 2 * groups;
+  if (static_cast<int>(blockIdx.x) >= jobs) {
+    const Seq s = load_seq(a.c, b);
+    const int w = (blockIdx.x - jobs) * NW + wave, i = w / parts;
+    if (i < s.count) Turner<T, MODE, G>(a.h, a.q, HeadSet{}).token(a.h, a.q, HeadSet{}, s.start + i, s.past + i, w % parts, parts);
+    return;
+  }
+  const int group = blockIdx.x % groups, j = blockIdx.x / (2 * groups);
+  const bool value = (blockIdx.x / groups) & 1;
+  const PageShare sh = page_share(a.c, b, j, 0);
+  const int lo = sh.lo, hi = sh.hi;
+  if (hi <= lo) return;
+  const int log = a.c.page_log, P = 1 << log, D = a.h.D;
+  const int at = tid % LANES, sub = tid / LANES;  // lane of the page, which page of those together
+  const int heads = a.c.heads;
+  int turn_of = 0;
+  // The largest magnitude of a page and head over its waves.
+  auto page_max = [&](uint32_t top) {
+    top = wave_max(top);
+    if constexpr (WPP > 1) {
+      if ((tid & 63) == 0) s_max[turn_of][wave] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < WPP; ++w) top = max(top, s_max[turn_of][sub * WPP + w]);
+      turn_of ^= 1;
+    }
+    return top;
+  };
+  if (!value) {
+    const Unit<MODE> u(at % G, a.h.pairs, D, a.h.adjacent);
+    float c[NP][4], s[NP][4], w[8];
+    load_weight(u, a.k.w, w);
+    const Frequencies f(a.h, u);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) f.coarse(static_cast<int>(sh.first) + p * STEP + at / G, c[p], s[p]);
+    // The next head's rows are on their way while this one's are worked on.
+    E raw[NP][8] = {};  // (rows that are not the page's new tokens count nowhere below)
+    auto fetch = [&](int head) {
+      const E* src = static_cast<const E*>(a.k.x) + head * a.k.x_h + (sh.token - lo) * a.k.x_t;
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const int t = p * STEP + at / G;
+        if (u.live && t >= lo && t < hi) u.load_raw(src + t * a.k.x_t, raw[p]);
+      }
+    };
+    const int first = group * per * TOGETHER + sub;
+    if (first < heads) fetch(first);
+    for (int it = 0; it < per; ++it) {
+      const int head = first + it * TOGETHER;
+      const bool work = head < heads;
+      if (WPP == 1 && !work) break;
+      const int64_t slot = sh.slot + (work ? head : 0);
+      const float old = lo ? a.c.ks[slot] : 0.f;
+      float v[NP][8];
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        u.widen(raw[p], v[p]);
+        if (!u.live) {  // (part of a head's sum)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[p][k] = 0.f;
+        }
+      }
+      if (it + 1 < per && head + TOGETHER < heads) fetch(head + TOGETHER);
+      uint32_t top = 0;
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const int t = p * STEP + at / G;
+        turn<G>(a.h, u, a.k.w != nullptr, w, c[p], s[p], v[p]);
+        if (work && t >= lo && t < hi) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) top = max(top, abs_bits(v[p][k]));
+        }
+      }
+      top = page_max(top);
+      if (!work) continue;
+      const float scale = joint_scale(old, top), inv = inverse_of(scale);
+      int8_t* codes = a.c.k + slot * P * D;
+      if (lo && scale != old) {
+        const float ratio = inv > 0.f ? old * inv : 0.f;
+        for (int x = at; x < lo * D >> 4; x += LANES) {
+          uint4* q = reinterpret_cast<uint4*>(codes) + x;
+          uint4 r = *q;
+          r.x = rescaled4(r.x, ratio);
+          r.y = rescaled4(r.y, ratio);
+          r.z = rescaled4(r.z, ratio);
+          r.w = rescaled4(r.w, ratio);
+          *q = r;
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const int t = p * STEP + at / G;
+        if (t >= lo && t < hi) u.store_codes(codes + t * D, v[p], inv);
+      }
+      if (at == 0) a.c.ks[slot] = scale;
+    }
+    return;
+  }
+  // Values: units of 4 tokens x 8, unit lane % G along the row.
+  constexpr int NU = (NP + 3) / 4;
+  const int pitch = P + 4;
+  unsigned char* image = s_page + sub * (D * pitch);
+  const int d8 = at % G * 8;
+  const bool row = d8 < D;
+  auto sync = [&] {
+    if constexpr (WPP > 1)
+      __syncthreads();
+    else
+      wave_lds_sync();
+  };
+  E raw[NU][4][8] = {};
+  auto fetch = [&](int head) {
+    const E* src = static_cast<const E*>(a.v) + head * a.v_h + (sh.token - lo) * a.v_t + d8;
+#pragma unroll
+    for (int n = 0; n < NU; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 4 * (n * STEP + at / G) + i;
+        if (row && t >= lo && t < hi) __builtin_memcpy(raw[n][i], __builtin_assume_aligned(src + t * a.v_t, 16), 8 * sizeof(E));
+      }
+  };
+  const int first = group * per * TOGETHER + sub;
+  if (first < heads) fetch(first);
+  for (int it = 0; it < per; ++it) {
+    const int head = first + it * TOGETHER;
+    const bool work = head < heads;
+    if (WPP == 1 && !work) break;
+    const int64_t slot = sh.slot + (work ? head : 0);
+    const float old = lo ? a.c.vs[slot] : 0.f;
+    int8_t* codes = a.c.v + slot * P * D;
+    float v[NU][4][8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int n = 0; n < NU; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 4 * (n * STEP + at / G) + i;
+        if (work && row && t >= lo && t < hi) top = max(top, raw_max<T>(raw[n][i]));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[n][i][k] = static_cast<float>(raw[n][i][k]);
+      }
+    if (it + 1 < per && head + TOGETHER < heads) fetch(head + TOGETHER);
+    if (lo > 0 || hi < P) {  // some of the page stays
+      for (int x = at; x < P * D >> 4; x += LANES) {
+        const uint4 c = reinterpret_cast<const uint4*>(codes)[x];
+        uint32_t* q = reinterpret_cast<uint32_t*>(image + x * 16 + (x >> (log - 4)) * 4);
+        q[0] = c.x;
+        q[1] = c.y;
+        q[2] = c.z;
+        q[3] = c.w;
+      }
+    }
+    top = page_max(top);
+    if (WPP == 1) wave_lds_sync();
+    const float scale = joint_scale(old, top), inv = inverse_of(scale);
+    if (lo && scale != old) {
+      const float ratio = inv > 0.f ? old * inv : 0.f;
+      for (int x = at; x < P * D >> 2; x += LANES)
+        if (4 * (x & ((P >> 2) - 1)) < lo) {
+          uint32_t* q = reinterpret_cast<uint32_t*>(image + x * 4 + (x >> (log - 2)) * 4);
+          const int n = lo - 4 * (x & ((P >> 2) - 1));  // older tokens in this word
+          const uint32_t keep = n >= 4 ? ~0u : (1u << (8 * n)) - 1;
+          *q = (rescaled4(*q, ratio) & keep) | (*q & ~keep);
+        }
+    }
+    if (lo) sync();
+#pragma unroll
+    for (int n = 0; n < NU; ++n) {
+      const int t4 = 4 * (n * STEP + at / G);
+      if (!row || t4 >= P || t4 + 4 <= lo || t4 >= hi) continue;
+      uint2 c[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] = codes8_within(v[n][i], inv);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w |= (((k < 4 ? c[i].x : c[i].y) >> (8 * (k & 3))) & 0xffu) << (8 * i);
+        unsigned char* q = image + (d8 + k) * pitch + t4;
+        if (t4 >= lo && t4 + 4 <= hi) {
+          *reinterpret_cast<uint32_t*>(q) = w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (t4 + i >= lo && t4 + i < hi) q[i] = static_cast<unsigned char>(w >> (8 * i));
+        }
+      }
+    }
+    sync();
+    if (work) {
+      for (int x = at; x < P * D >> 4; x += LANES) {
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(image + x * 16 + (x >> (log - 4)) * 4);
+        reinterpret_cast<uint4*>(codes)[x] = make_uint4(q[0], q[1], q[2], q[3]);
+      }
+      if (at == 0) a.c.vs[slot] = scale;
+    }
+    sync();  // (the next head's image)
+  }
+}
+
+template <int T, int MODE, int G, int WPP, int NP>
+static void go_step_page(const StepArgs& a, const StepPlan& p, hipStream_t s) {
+  constexpr int NW = WPP < 4 ? 4 : WPP;
+  if constexpr (64 * WPP * NP >= 16 * G && 64 * WPP * NP <= 128 * G) {  // (a page size that there is)
+    const size_t lds = static_cast<size_t>(NW / WPP) * a.h.D * ((1 << a.c.page_log) + 4);
+    step_page_kernel<T, MODE, G, WPP, NP>
+        <<<dim3(static_cast<unsigned>(p.workgroups), a.batch), NW * 64, lds, s>>>(a, p.pages, p.groups, p.per, p.parts);
+  }
+}
+
+template <int T, int MODE, int G>
+static void go_step(const StepArgs& a, const StepPlan& p, hipStream_t s) {
+  if constexpr (MODE != kAny && G < 64) {
+    if (p.page) {
+      switch (p.wpp * p.np) {
+        case 1: go_step_page<T, MODE, G, 1, 1>(a, p, s); return;
+        case 2: go_step_page<T, MODE, G, 1, 2>(a, p, s); return;
+        case 4: go_step_page<T, MODE, G, 1, 4>(a, p, s); return;
+        case 8: go_step_page<T, MODE, G, 2, 4>(a, p, s); return;
+        case 16: go_step_page<T, MODE, G, 4, 4>(a, p, s); return;
+        case 32: go_step_page<T, MODE, G, 4, 8>(a, p, s); return;
+        default: go_step_page<T, MODE, G, 8, 8>(a, p, s); return;
+      }
+    }
+  }
+  step_few_kernel<T, MODE, G><<<dim3(static_cast<unsigned>(p.workgroups), a.batch), 256, 0, s>>>(a, p.pages, p.parts);
+}
+
+template <int T>
+static void go_step_type(const StepArgs& a, const StepPlan& p, hipStream_t s) {
+  auto lanes = [&](auto mode) {
+    constexpr int MODE = decltype(mode)::value;
+    switch (p.g) {
+      case 4: go_step<T, MODE, 4>(a, p, s); break;
+      case 8: go_step<T, MODE, 8>(a, p, s); break;
+      case 16: go_step<T, MODE, 16>(a, p, s); break;
+      case 32: go_step<T, MODE, 32>(a, p, s); break;
+      default: go_step<T, MODE, 64>(a, p, s); break;
+    }
+  };
+  if (p.mode == kAdjacent)
+    lanes(std::integral_constant<int, kAdjacent>{});
+  else if (p.mode == kHalves)
+    lanes(std::integral_constant<int, kHalves>{});
+  else
+    lanes(std::integral_constant<int, kAny>{});
+}
+
+}  // namespace voc
