@@ -103,7 +103,9 @@ static StepPlan plan_step(int dtype, const StepArgs& a) {
   // words, are worth the page's image.
   const int lanes = P * p.g;
   p.page = a.c.max_new > 8 && p.mode != kAny && lanes <= 4096;
-  const int64_t queries = static_cast<int64_t>(a.c.max_new) * p.parts;
+  const int64_t want = static_cast<int64_t>(a.c.tokens) * p.parts / 8192;
+  p.run = !p.page || want < 1 ? 1 : want < 8 ? static_cast<int>(want) : 8;
+  const int64_t queries = a.q.heads ? (static_cast<int64_t>(a.c.max_new) + p.run - 1) / p.run * p.parts : 0;
   if (!p.page) {
     p.workgroups = static_cast<int64_t>(p.pages) * 2 * a.c.heads + (queries + 3) / 4;
     return p;

@@ -114,7 +114,7 @@ __device__ __forceinline__ uint32_t raw_max(const typename Elem<T>::type (&e)[8]
 // ([d][token], rows of P + 4 bytes) and stored whole.  Queries as above.
 template <int T, int MODE, int G, int WPP, int NP>
 __global__ __launch_bounds__(WPP < 4 ? 256 : 64 * WPP, NP > 4 ? 2 : 4) void step_page_kernel(const StepArgs a, int pages, int groups, int per,
-                                                                            int parts) {
+                                                                            int parts, int run) {
   typedef typename Elem<T>::type E;
   constexpr int NW = WPP < 4 ? 4 : WPP, TOGETHER = NW / WPP;  // page and head pairs at a time
   constexpr int LANES = 64 * WPP, STEP = LANES / G;           // tokens a pass
@@ -123,9 +123,12 @@ __global__ __launch_bounds__(WPP < 4 ? 256 : 64 * WPP, NP > 4 ? 2 : 4) void step
   const int tid = threadIdx.x, wave = tid >> 6;
   const int b = blockIdx.y, jobs = pages * 2 * groups;
   if (static_cast<int>(blockIdx.x) >= jobs) {
+    // A wave takes `run` tokens in a row (parts is 1 where run is more).
     const Seq s = load_seq(a.c, b);
-    const int w = (blockIdx.x - jobs) * NW + wave, i = w / parts;
-    if (i < s.count) Turner<T, MODE, G>(a.h, a.q, HeadSet{}).token(a.h, a.q, HeadSet{}, s.start + i, s.past + i, w % parts, parts);
+    const int w = (blockIdx.x - jobs) * NW + wave, i0 = w / parts * run;
+    if (i0 >= s.count) return;
+    const Turner<T, MODE, G> turner(a.h, a.q, HeadSet{});
+    for (int i = i0; i < min(i0 + run, s.count); ++i) turner.token(a.h, a.q, HeadSet{}, s.start + i, s.past + i, w % parts, parts);
     return;
   }
   const int group = blockIdx.x % groups, j = blockIdx.x / (2 * groups);
@@ -327,7 +330,7 @@ static void go_step_page(const StepArgs& a, const StepPlan& p, hipStream_t s) {
   if constexpr (64 * WPP * NP >= 16 * G && 64 * WPP * NP <= 128 * G) {  // (a page size that there is)
     const size_t lds = static_cast<size_t>(NW / WPP) * a.h.D * ((1 << a.c.page_log) + 4);
     step_page_kernel<T, MODE, G, WPP, NP>
-        <<<dim3(static_cast<unsigned>(p.workgroups), a.batch), NW * 64, lds, s>>>(a, p.pages, p.groups, p.per, p.parts);
+        <<<dim3(static_cast<unsigned>(p.workgroups), a.batch), NW * 64, lds, s>>>(a, p.pages, p.groups, p.per, p.parts, p.run);
   }
 }
 

@@ -8,7 +8,7 @@ namespace voc {
 
 // How a step's work is cut.
 struct StepPlan {
-  int g, mode, pages, parts, wpp, np, groups, per;
+  int g, mode, pages, parts, wpp, np, groups, per, run;
   bool page;  // by step_page_kernel
   int64_t workgroups;  // of a sequence
 };

@@ -701,8 +701,8 @@ voc_status vocoder_norm_rotate_append(voc_ops *ops, const voc_kv_cache *cache,
 
 /*
  * The cache's tokens as rows: row starts[b] + i of k and v becomes the key and
- * value at position past[b] + i of sequence b, code * scale rounded to dtype
- * once (strides as in vocoder_cache_append; either of k and v may be NULL).  The
+ * value at position past[b] + i of sequence b, code * scale in fp32, rounded to
+ * dtype (strides as in vocoder_cache_append; either of k and v may be NULL).  The
  * batch that appended tokens reads them back; past = 0 and the whole lengths
  * as new tokens read whole sequences.  Rows that belong to no sequence, and
  * positions in pages out of range, are not written.
