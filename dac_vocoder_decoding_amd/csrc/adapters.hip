@@ -246,8 +246,11 @@ __global__ __launch_bounds__(512) void shrink_tile_kernel(const AdaptArgs a, int
     };
     if (wave < chunks) fetch(wave);
     for (int c = wave; c < chunks; c += 8) {
-      Weights<RT> g;
-      load_weights<RT>(down0 + one * per, steps, c, g);
+      // Both adapters' weights at once where the registers hold them.
+      constexpr bool BOTH = RT * TB <= 4;
+      Weights<RT> g[BOTH ? 2 : 1];
+      load_weights<RT>(down0 + one * per, steps, c, g[0]);
+      if (BOTH && two >= 0) load_weights<RT>(down0 + two * per, steps, c, g[BOTH]);
 #pragma unroll
       for (int q = 0; q < 2 * TB; ++q) {
         const int r = 8 * q + (lane >> 3);
@@ -264,7 +267,7 @@ __global__ __launch_bounds__(512) void shrink_tile_kernel(const AdaptArgs a, int
           x[s][0][j] = codes_to_16<BF16>(v[0], v[1]);
           x[s][1][j] = codes_to_16<BF16>(v[2], v[3]);
         }
-      auto multiply = [&](int n) {
+      auto multiply = [&](int n, const Weights<RT>& g) {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -274,10 +277,10 @@ __global__ __launch_bounds__(512) void shrink_tile_kernel(const AdaptArgs a, int
 #pragma unroll
               for (int j = 0; j < TB; ++j) multiply16<BF16>(g.w[i][s][h], x[s][h][j], acc[n][i][j]);
       };
-      multiply(0);
+      multiply(0, g[0]);
       if (two >= 0) {
-        load_weights<RT>(down0 + two * per, steps, c, g);
-        multiply(1);
+        if (!BOTH) load_weights<RT>(down0 + two * per, steps, c, g[0]);
+        multiply(1, g[BOTH]);
       }
       wave_lds_sync();
     }

@@ -132,15 +132,8 @@ __device__ __forceinline__ f32x4 low_rank_terms(const IntMatmulArgs& a, int m, i
 // and take nothing from it (a weight that is not finite stays with its own
 // tokens).
 template <bool BF16, int NT, int FF, int FT>
-__device__ __forceinline__ void low_rank_tile(const IntMatmulArgs& a, int nw, int mw, f32x4 (&d)[FF][FT]) {
+__device__ __forceinline__ void low_rank_tile(const IntMatmulArgs& a, int nw, int mw, int (&id)[FT], f32x4 (&d)[FF][FT]) {
   const int lane = threadIdx.x & 63, lr = lane & 15;
-  int id[FT];
-#pragma unroll
-  for (int j = 0; j < FT; ++j) {
-    const int m = mw + 16 * j + lr;
-    id[j] = m < a.M ? a.adapter[m] : -1;
-    if (id[j] >= a.adapters) id[j] = -1;
-  }
   const int features = (a.N + 15) >> 4, blocks = a.rank / a.chunk;
   const bool in = lane < 2 * a.chunk;  // (16 ranks fill half of a product's slots)
 #pragma unroll 1
@@ -201,15 +194,15 @@ __device__ __forceinline__ void low_rank_tile(const IntMatmulArgs& a, int nw, in
 // fp16 2^-22 of a token's largest); fp32 outputs take three where the terms
 // are bf16.
 template <int T, int FF, int FT>
-__device__ __forceinline__ void low_rank(const IntMatmulArgs& a, int nw, int mw, f32x4 (&d)[FF][FT]) {
+__device__ __forceinline__ void low_rank(const IntMatmulArgs& a, int nw, int mw, int (&id)[FT], f32x4 (&d)[FF][FT]) {
 #pragma unroll
   for (int i = 0; i < FF; ++i)
 #pragma unroll
     for (int j = 0; j < FT; ++j) d[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (a.up_bf16)
-    low_rank_tile<true, T == EL_F32 ? 3 : 2>(a, nw, mw, d);
+    low_rank_tile<true, T == EL_F32 ? 3 : 2>(a, nw, mw, id, d);
   else
-    low_rank_tile<false, 2>(a, nw, mw, d);
+    low_rank_tile<false, 2>(a, nw, mw, id, d);
 }
 
 // Four consecutive features n .. n + 3 of token m (n a multiple of 4).
@@ -460,9 +453,16 @@ __global__ __launch_bounds__(WF * WT * 64, ADAPT ? 2 : 1) void int_matmul_tile_k
   unsigned char* part = smem + wave * (NS * STAGE / NW);
   const int nw = n0 + wf * FF * 16, mw = m0 + wt * FT * 16;
   auto column_scales = [&](int i, f4& sb, f4& bi) {
+    const int n0 = nw + i * 16 + 4 * lg;
+    if (ADAPT && n0 + 4 <= a.N) {
+      __builtin_memcpy(&sb, a.sb + n0, 16);
+      bi = f4{0.f, 0.f, 0.f, 0.f};
+      if (a.bias) __builtin_memcpy(&bi, a.bias + n0, 16);
+      return;
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int n = min(nw + i * 16 + 4 * lg + e, a.N - 1);
+      const int n = min(n0 + e, a.N - 1);
       sb[e] = a.sb[n];
       bi[e] = a.bias ? a.bias[n] : 0.f;
     }
@@ -498,20 +498,29 @@ __global__ __launch_bounds__(WF * WT * 64, ADAPT ? 2 : 1) void int_matmul_tile_k
       // registers hold beside the sums.
       constexpr int FI = FF < 4 ? FF : 4;
       static_assert(CT % 2 == 0 && FF % FI == 0, "pairs of token blocks");
+      float sa[CT];
+      int ids[CT];
+#pragma unroll
+      for (int jj = 0; jj < CT; ++jj) {
+        const int m = mw + (j0 + jj) * 16 + lr;
+        sa[jj] = a.sa[min(m, a.M - 1)];
+        ids[jj] = m < a.M ? a.adapter[m] : -1;
+        if (ids[jj] >= a.adapters) ids[jj] = -1;
+      }
 #pragma unroll
       for (int i0 = 0; i0 < FF; i0 += FI) {
+        f4 sbv[FI], biv[FI];
+#pragma unroll
+        for (int i = 0; i < FI; ++i) column_scales(i0 + i, sbv[i], biv[i]);
 #pragma unroll
         for (int jj = 0; jj < CT; jj += 2) {
           f32x4 add[FI][2];
-          low_rank<T>(a, nw + 16 * i0, mw + (j0 + jj) * 16, add);
+          int id[2] = {ids[jj], ids[jj + 1]};
+          low_rank<T>(a, nw + 16 * i0, mw + (j0 + jj) * 16, id, add);
 #pragma unroll
-          for (int i = 0; i < FI; ++i) {
-            f4 sbv, biv;
-            column_scales(i0 + i, sbv, biv);
+          for (int i = 0; i < FI; ++i)
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
-              stage(i0 + i, jj + p, acc[i0 + i][j0 + jj + p], a.sa[min(mw + (j0 + jj + p) * 16 + lr, a.M - 1)], sbv, biv, add[i][p]);
-          }
+            for (int p = 0; p < 2; ++p) stage(i0 + i, jj + p, acc[i0 + i][j0 + jj + p], sa[jj + p], sbv[i], biv[i], add[i][p]);
           __builtin_amdgcn_sched_barrier(0);
         }
       }

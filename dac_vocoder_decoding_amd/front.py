@@ -25,6 +25,18 @@ Per layer, with h the residual stream:
     q8 = rows8(norm(h + delta))            rms_norm
     delta = Wd rows8(gelu(Wu q8 + bu))     matmul_int with GELU, quantize_rows, matmul_int
 
+With Shape(qk_norm=True) each query and key head has an RMS norm before the
+rotation, and both and the append are one call (norm_rotate_append).  With
+`adapters` > 0 every product has that many low-rank adapters (a voice each) for
+streams to choose from, beside the shared weights (matmul_int_adapters):
+
+    front = Front(shape, weights, rows=32, max_frames=250, adapters=8, rank=16)
+    front.set_adapter(3, make_adapter(shape, 16, seed))
+    latent = front.step(frames, adapter=numbers)        # int32 [rows], -1: none
+
+`save` takes the streams' histories out of the caches (cache_read), `load` puts
+them into another Front of the same shape.
+
 `python -m dac_vocoder_decoding_amd.front` runs it ahead of the causal codec
 workload (32 streams in 25-frame chunks) with random weights.
 """
@@ -47,6 +59,7 @@ class Shape:
     layers: int = 2
     window: int = 72         # positions that a query sees, itself included (0: all)
     rotary_base: float = 10000.0
+    qk_norm: bool = False    # an RMS norm of each query and key head
 
 
 def make_weights(shape: Shape, seed: int, device="cuda") -> dict:
@@ -66,15 +79,38 @@ def make_weights(shape: Shape, seed: int, device="cuda") -> dict:
         out[p + "o"] = normal(c, shape.heads * shape.head_dim, std=(shape.heads * shape.head_dim) ** -0.5)
         out[p + "up"], out[p + "up_bias"] = normal(shape.hidden, c, std=c ** -0.5), normal(shape.hidden, std=0.01)
         out[p + "down"] = normal(c, shape.hidden, std=shape.hidden ** -0.5)
+        if shape.qk_norm:
+            out[p + "q_norm"], out[p + "k_norm"] = 1 + normal(shape.head_dim, std=0.1), 1 + normal(shape.head_dim, std=0.1)
+    return out
+
+
+def products(shape: Shape) -> dict:
+    """name -> (inputs, outputs) of a layer's products."""
+    c, wide = shape.channels, shape.heads * shape.head_dim
+    return {"qkv": (c, wide + 2 * shape.kv_heads * shape.head_dim), "o": (wide, c), "up": (c, shape.hidden),
+            "down": (shape.hidden, c)}
+
+
+def make_adapter(shape: Shape, rank: int, seed: int, device="cuda") -> dict:
+    """A random low-rank adapter: name -> (down [rank, inputs], up [outputs,
+    rank]) of every layer's products, whose terms are about a third of them."""
+    g = torch.Generator(device=device)
+    g.manual_seed(seed)
+    out = {}
+    for i in range(shape.layers):
+        for name, (k, n) in products(shape).items():
+            down = torch.randn(rank, k, generator=g, device=device) * k ** -0.5
+            out[f"layers.{i}.{name}"] = down, torch.randn(n, rank, generator=g, device=device) * 0.3 * rank ** -0.5
     return out
 
 
 class Front:
-    """The stage's 8-bit weights and the caches of `rows` streams of up to
-    max_frames frames."""
+    """The stage's 8-bit weights, the caches of `rows` streams of up to
+    max_frames frames, and room for `adapters` low-rank adapters of up to
+    `rank`."""
 
     def __init__(self, shape: Shape, weights: dict, rows: int, max_frames: int, page_tokens: int = 16,
-                 device: int = 0):
+                 device: int = 0, adapters: int = 0, rank: int = 16):
         self.shape, self.rows, self.max_frames = shape, rows, max_frames
         self.ops = V.open_ops(device)
         self.device = torch.device("cuda", device)
@@ -91,6 +127,12 @@ class Front:
         half = torch.arange(0, shape.head_dim, 2, device=self.device, dtype=torch.float32)
         angle = torch.outer(torch.arange(max_frames, device=self.device), shape.rotary_base ** (-half / shape.head_dim))
         self.cos, self.sin = angle.cos().half(), angle.sin().half()
+        self.freq = shape.rotary_base ** (-half / shape.head_dim)
+        self.adapters = {}
+        if adapters:
+            zeros = lambda *size: torch.zeros(adapters, *size, dtype=torch.float16, device=self.device)     # noqa: E731
+            self.adapters = {f"layers.{i}.{name}": V.Adapters(zeros(rank, k), zeros(n, rank))
+                             for i in range(shape.layers) for name, (k, n) in products(shape).items()}
 
     def close(self) -> None:
         """Releases the operators' handle (after the streams were synchronized)."""
@@ -103,6 +145,44 @@ class Front:
         self.frames = 0
         self.past.zero_()
 
+    def set_adapter(self, index: int, weights: dict, scale: float = 1.0) -> None:
+        """Makes `weights` (as make_adapter gives them; products that are not
+        named have no term) the adapter `index`."""
+        unknown = set(weights) - set(self.adapters)
+        if unknown:
+            raise ValueError(f"adapter: no products {sorted(unknown)} to adapt")
+        for name, store in self.adapters.items():
+            if name in weights:
+                store.set(index, *weights[name], scale)
+            else:
+                store.set(index, store.down.new_zeros(1, store.K), store.up.new_zeros(store.N, 1), 0.0)
+
+    def _history(self):
+        """A batch of every stream's frames so far, as new tokens."""
+        starts = torch.arange(self.rows + 1, dtype=torch.int32, device=self.device) * self.frames
+        return V.KVBatch(self.table, torch.zeros_like(self.past), starts, self.frames, self.frames)
+
+    def save(self) -> dict:
+        """The streams' histories: frames, and each layer's keys and values
+        [rows * frames, kv_heads, head_dim] in fp32, from which load makes the
+        same codes."""
+        layers = [V.cache_read(self.ops, c, self._history(), self.rows * self.frames, dtype=torch.float32)
+                  for c in self.caches] if self.frames else []
+        return {"frames": self.frames, "layers": layers}
+
+    def load(self, state: dict) -> None:
+        """Goes on from the histories that save gave."""
+        frames, sh = state["frames"], self.shape
+        want = (self.rows * frames, sh.kv_heads, sh.head_dim)
+        if frames > self.max_frames or (frames and (len(state["layers"]) != sh.layers or any(
+                tuple(x.shape) != want for kv in state["layers"] for x in kv))):
+            raise ValueError(f"state: {sh.layers} layers of keys and values {want}, of up to {self.max_frames} frames, are needed")
+        self.reset()
+        self.frames = frames
+        for cache, (k, v) in zip(self.caches, state["layers"]):
+            V.cache_append(self.ops, cache, self._history(), k.to(self.device), v.to(self.device))
+        self.past += frames
+
     def _rotate(self, x, t: int) -> None:
         """Rotates x [rows * t, heads, head_dim] by its positions, in place."""
         c = self.cos[self.frames:self.frames + t].repeat(self.rows, 1)[:, None]
@@ -111,9 +191,10 @@ class Front:
         a_new, b_new = a * c - b * s, b * c + a * s
         x[..., 0::2], x[..., 1::2] = a_new, b_new
 
-    def step(self, frames):
+    def step(self, frames, adapter=None):
         """Latent frames [rows, channels, t] (fp32) of the next t frames
-        [rows, channels, t] (fp32) of every stream."""
+        [rows, channels, t] (fp32) of every stream; adapter: int32 [rows], the
+        low-rank adapter of each stream (-1: none)."""
         sh, ops = self.shape, self.ops
         rows, c, t = frames.shape
         if (rows, c) != (self.rows, sh.channels) or t < 1 or self.frames + t > self.max_frames:
@@ -123,17 +204,33 @@ class Front:
         batch = V.KVBatch(self.table, self.past, starts, t, self.frames + t)
         h, delta = frames.transpose(1, 2).reshape(rows * t, c).half(), None
         nq, nk, d = sh.heads, sh.kv_heads, sh.head_dim
+        if adapter is not None:
+            if not self.adapters or adapter.shape != (rows,):
+                raise ValueError(f"adapter: int32 [{rows}] is needed, and a Front with adapters")
+            numbers = adapter.to(self.device, torch.int32)[:, None].expand(rows, t).reshape(-1)
         for i in range(sh.layers):
             w = lambda name: self.w[f"layers.{i}.{name}"]          # noqa: E731
+
+            def product(name, x8, s, **kw):
+                if adapter is None:
+                    return V.matmul_int(ops, x8, s, *w(name), dtype=torch.float16, **kw)
+                return V.matmul_int_adapters(ops, x8, s, *w(name), self.adapters[f"layers.{i}.{name}"], numbers,
+                                             dtype=torch.float16, **kw)
+
             q8, s, h = V.rms_norm(ops, h, w("norm1"), residual=delta)
-            qkv = V.matmul_int(ops, q8, s, *w("qkv"), dtype=torch.float16).view(rows * t, nq + 2 * nk, d)
-            self._rotate(qkv[:, :nq + nk], t)
-            V.cache_append(ops, self.caches[i], batch, qkv[:, nq:nq + nk], qkv[:, nq + nk:])
-            a = V.cache_attention(ops, self.caches[i], batch, qkv[:, :nq], window=sh.window)
-            delta = V.matmul_int(ops, *V.quantize_rows(ops, a.view(rows * t, nq * d)), *w("o"), dtype=torch.float16)
+            qkv = product("qkv", q8, s).view(rows * t, nq + 2 * nk, d)
+            q, k, v = qkv[:, :nq], qkv[:, nq:nq + nk], qkv[:, nq + nk:]
+            if sh.qk_norm:
+                V.norm_rotate_append(ops, self.caches[i], batch, q, k, v, freq=self.freq, q_weight=w("q_norm"),
+                                     k_weight=w("k_norm"), adjacent=True, out=q)
+            else:
+                self._rotate(qkv[:, :nq + nk], t)
+                V.cache_append(ops, self.caches[i], batch, k, v)
+            a = V.cache_attention(ops, self.caches[i], batch, q, window=sh.window)
+            delta = product("o", *V.quantize_rows(ops, a.view(rows * t, nq * d)))
             q8, s, h = V.rms_norm(ops, h, w("norm2"), residual=delta)
-            u = V.matmul_int(ops, q8, s, *w("up"), bias=w("up_bias"), gelu=True, dtype=torch.float16)
-            delta = V.matmul_int(ops, *V.quantize_rows(ops, u), *w("down"), dtype=torch.float16)
+            u = product("up", q8, s, bias=w("up_bias"), gelu=True)
+            delta = product("down", *V.quantize_rows(ops, u))
         q8, s, _ = V.rms_norm(ops, h, self.w["norm"], residual=delta)
         self.frames += t
         self.past += t
@@ -141,14 +238,25 @@ class Front:
         return out.view(rows, t, c).transpose(1, 2).contiguous()
 
 
-def main() -> int:
+def main(argv=None) -> int:
+    import argparse
     import time
 
     from . import inputs as I
+    p = argparse.ArgumentParser(prog="python -m dac_vocoder_decoding_amd.front", description="Times the stage ahead of the causal codec.")
+    p.add_argument("--qk-norm", action="store_true", help="an RMS norm of each query and key head")
+    p.add_argument("--adapters", type=int, default=0, help="low-rank adapters that the streams take in turn")
+    p.add_argument("--rank", type=int, default=16)
+    args = p.parse_args(argv)
     cfg = I.config(7)
     rows, ck, total = cfg["batch"], cfg["chunk"], cfg["frames"]
-    shape = Shape(channels=cfg["latent_channels"])
-    front = Front(shape, make_weights(shape, cfg["seed"]), rows, total)
+    shape = Shape(channels=cfg["latent_channels"], qk_norm=args.qk_norm)
+    front = Front(shape, make_weights(shape, cfg["seed"]), rows, total, adapters=args.adapters, rank=args.rank)
+    adapter = None
+    if args.adapters:
+        for i in range(args.adapters):
+            front.set_adapter(i, make_adapter(shape, args.rank, cfg["seed"] + i))
+        adapter = (torch.arange(rows, device="cuda") % args.adapters).to(torch.int32)
     ctx = V.open_context(cfg, I.make_weights(cfg))
     frames = torch.from_numpy(I.make_latent(cfg)).cuda()
     try:
@@ -159,7 +267,7 @@ def main() -> int:
             t_front = t_all = 0.0
             for k in range(0, total, ck):
                 t0 = time.perf_counter()
-                latent = front.step(frames[:, :, k:k + ck].contiguous())
+                latent = front.step(frames[:, :, k:k + ck].contiguous(), adapter)
                 torch.cuda.synchronize()
                 t1 = time.perf_counter()
                 V.stream_decode(ctx, latent)

@@ -802,8 +802,7 @@ class Adapters:
         # [adapter][16 features][8 ranks][feature][8]
         self.up = torch.zeros(self.count, -(-self.N // 16), rank // 8, 16, 8, dtype=up.dtype, device=up.device)
         self.scale = torch.ones(self.count, device=down.device)
-        for i in range(self.count):
-            self._lay(i, down[i], up[i])
+        self._lay(slice(None), down, up)
         if scale is not None:
             if scale.shape != (self.count,) or scale.device != down.device:
                 raise ValueError(f"adapters: scale [{self.count}] on {down.device} is needed")
@@ -813,14 +812,16 @@ class Adapters:
                               self.up.data_ptr(), self.scale.data_ptr())
         self.ref = ctypes.byref(self.c)
 
-    def _lay(self, index: int, down, up) -> None:
+    def _lay(self, which, down, up) -> None:
+        """down [.., r, K] and up [.., N, r] into the adapters `which`."""
+        import torch.nn.functional as F
         _, blocks, steps, _, _, _, _ = self.down.shape
-        rows = down.new_zeros(blocks * 16, steps * 64)
-        rows[:down.shape[0], :self.K] = down
-        self.down[index] = rows.view(blocks, 16, steps, 4, 2, 8).permute(0, 2, 4, 3, 1, 5)
-        rows = up.new_zeros(self.up.shape[1] * 16, blocks * 16)
-        rows[:self.N, :up.shape[1]] = up
-        self.up[index] = rows.view(-1, 16, blocks * 2, 8).transpose(1, 2)
+        r = blocks * 16 - down.shape[-2]
+        down = F.pad(down, (0, steps * 64 - self.K, 0, r)).unflatten(-1, (steps, 4, 2, 8)).unflatten(-5, (blocks, 16))
+        lead = down.dim() - 6
+        self.down[which] = down.permute(*range(lead), *(lead + i for i in (0, 2, 4, 3, 1, 5)))
+        up = F.pad(up, (0, r, 0, self.up.shape[1] * 16 - self.N)).unflatten(-1, (blocks * 2, 8)).unflatten(-3, (-1, 16))
+        self.up[which] = up.transpose(-3, -2)
 
     def set(self, index: int, down, up, scale: float = 1.0) -> None:
         """Replaces adapter `index` by down [r, K] and up [N, r] (r up to the
@@ -963,8 +964,9 @@ def norm_rotate(ops, q, k=None, position=None, freq=None, q_weight=None, k_weigh
     raw, other = (_raw_stream(device), None) if stream is None else _stream_of(stream, q)
     pairs, fp = _turning(freq, dim, device)
     if q_out is None:
-        q_out = _new(other, shape, dtype, q.device)
-    ot, oh = _heads("q_out", q_out, shape, dtype, device)
+        q_out, ot, oh = _new(other, shape, dtype, q.device), heads * dim, dim
+    else:
+        ot, oh = _heads("q_out", q_out, shape, dtype, device)
     qw = None if q_weight is None else _vector("q_weight", q_weight, dim, device)
     kv_heads = kp = kt = kh = kw = kop = kot = koh = 0
     if k is not None:
@@ -972,8 +974,9 @@ def norm_rotate(ops, q, k=None, position=None, freq=None, q_weight=None, k_weigh
         kshape = (tokens, kv_heads, dim)
         kt, kh = _heads("k", k, kshape, dtype, device)
         if k_out is None:
-            k_out = _new(other, kshape, dtype, q.device)
-        kot, koh = _heads("k_out", k_out, kshape, dtype, device)
+            k_out, kot, koh = _new(other, kshape, dtype, q.device), kv_heads * dim, dim
+        else:
+            kot, koh = _heads("k_out", k_out, kshape, dtype, device)
         kp, kop = k.data_ptr(), k_out.data_ptr()
         kw = None if k_weight is None else _vector("k_weight", k_weight, dim, device)
     if pairs and position is None:
@@ -1043,8 +1046,9 @@ def norm_rotate_append(ops, cache: KVCache, batch: KVBatch, q, k, v, freq=None, 
         qshape = (tokens, heads, dim)
         qt, qh = _heads("q", q, qshape, dtype, device)
         if out is None:
-            out = _new(other, qshape, dtype, q.device)
-        ot, oh = _heads("out", out, qshape, dtype, device)
+            out, ot, oh = _new(other, qshape, dtype, q.device), heads * dim, dim
+        else:
+            ot, oh = _heads("out", out, qshape, dtype, device)
         qp, op = q.data_ptr(), out.data_ptr()
     c = _with_tokens(batch, tokens)
     st = lib().vocoder_norm_rotate_append(ops, cache.ref, ctypes.byref(c), _dtype(dtype), fp, pairs, int(adjacent), eps, heads,
@@ -1068,12 +1072,16 @@ def cache_read(ops, cache: KVCache, batch: KVBatch, tokens: int, dtype=None, k=N
         import torch
         dtype = k.dtype if k is not None else v.dtype if v is not None else torch.float16
     raw, other = (_raw_stream(device), None) if stream is None else _stream_of(stream, cache.k)
+    kt = vt = shape[1] * shape[2]
+    kh = vh = shape[2]
     if k is None:
         k = _new(other, shape, dtype, cache.k.device)
+    else:
+        kt, kh = _heads("k", k, shape, dtype, device)
     if v is None:
         v = _new(other, shape, dtype, cache.k.device)
-    kt, kh = _heads("k", k, shape, dtype, device)
-    vt, vh = _heads("v", v, shape, dtype, device)
+    else:
+        vt, vh = _heads("v", v, shape, dtype, device)
     c = _with_tokens(batch, tokens)
     st = lib().vocoder_cache_read(ops, cache.ref, ctypes.byref(c), _dtype(dtype), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
                                   raw)
