@@ -452,37 +452,16 @@ __global__ __launch_bounds__(WF * WT * 64, ADAPT ? 2 : 1) void int_matmul_tile_k
   __syncthreads();
   unsigned char* part = smem + wave * (NS * STAGE / NW);
   const int nw = n0 + wf * FF * 16, mw = m0 + wt * FT * 16;
-  auto column_scales = [&](int i, f4& sb, f4& bi) {
-    const int n0 = nw + i * 16 + 4 * lg;
-    if (ADAPT && n0 + 4 <= a.N) {
-      __builtin_memcpy(&sb, a.sb + n0, 16);
-      bi = f4{0.f, 0.f, 0.f, 0.f};
-      if (a.bias) __builtin_memcpy(&bi, a.bias + n0, 16);
-      return;
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int n = min(n0 + e, a.N - 1);
-      sb[e] = a.sb[n];
-      bi[e] = a.bias ? a.bias[n] : 0.f;
-    }
-  };
-  auto stage = [&](int i, int jj, const i32x4& sums, float sa, const f4& sb, const f4& bi, const f32x4& add) {
-    E e[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float v = static_cast<float>(sums[q]) * sa * sb[q] + bi[q];
-      if constexpr (ADAPT) v += add[q];
-      e[q] = static_cast<E>(activate<T>(v, a.act));
-    }
-    const int byte = (i * 16 + 4 * lg) * ES;
-    __builtin_memcpy(__builtin_assume_aligned(part + (jj * 16 + lr) * RC * 16 + (((byte >> 4) ^ (lr & (RC - 1))) << 4) + (byte & 15), 4 * ES),
-                     e, 4 * ES);
-  };
-  f4 sb[ADAPT ? 1 : FF], bi[ADAPT ? 1 : FF];
+  f4 sb[FF], bi[FF];
   if constexpr (!ADAPT) {
 #pragma unroll
-    for (int i = 0; i < FF; ++i) column_scales(i, sb[i], bi[i]);
+    for (int i = 0; i < FF; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int n = min(nw + i * 16 + 4 * lg + e, a.N - 1);
+        sb[i][e] = a.sb[n];
+        bi[i][e] = a.bias ? a.bias[n] : 0.f;
+      }
   }
 #pragma unroll
   for (int j0 = 0; j0 < FT; j0 += CT) {
@@ -490,14 +469,44 @@ __global__ __launch_bounds__(WF * WT * 64, ADAPT ? 2 : 1) void int_matmul_tile_k
 #pragma unroll
       for (int jj = 0; jj < CT; ++jj) {
         const float sa = a.sa[min(mw + (j0 + jj) * 16 + lr, a.M - 1)];
+        unsigned char* pr = part + (jj * 16 + lr) * RC * 16;
 #pragma unroll
-        for (int i = 0; i < FF; ++i) stage(i, jj, acc[i][j0 + jj], sa, sb[i], bi[i], f32x4{});
+        for (int i = 0; i < FF; ++i) {
+          E e[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) e[q] = static_cast<E>(activate<T>(static_cast<float>(acc[i][j0 + jj][q]) * sa * sb[i][q] + bi[i][q], a.act));
+          const int byte = (i * 16 + 4 * lg) * ES;
+          __builtin_memcpy(__builtin_assume_aligned(pr + (((byte >> 4) ^ (lr & (RC - 1))) << 4) + (byte & 15), 4 * ES), e, 4 * ES);
+        }
       }
     } else {
       // The low-rank terms of up to 4 x 2 blocks at a time, which is what the
       // registers hold beside the sums.
       constexpr int FI = FF < 4 ? FF : 4;
       static_assert(CT % 2 == 0 && FF % FI == 0, "pairs of token blocks");
+      auto column_scales = [&](int i, f4& sb, f4& bi) {
+        const int n0 = nw + i * 16 + 4 * lg;
+        if (n0 + 4 <= a.N) {
+          __builtin_memcpy(&sb, a.sb + n0, 16);
+          bi = f4{0.f, 0.f, 0.f, 0.f};
+          if (a.bias) __builtin_memcpy(&bi, a.bias + n0, 16);
+          return;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int n = min(n0 + e, a.N - 1);
+          sb[e] = a.sb[n];
+          bi[e] = a.bias ? a.bias[n] : 0.f;
+        }
+      };
+      auto stage = [&](int i, int jj, const i32x4& sums, float sa, const f4& sb, const f4& bi, const f32x4& add) {
+        E e[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) e[q] = static_cast<E>(activate<T>(static_cast<float>(sums[q]) * sa * sb[q] + bi[q] + add[q], a.act));
+        const int byte = (i * 16 + 4 * lg) * ES;
+        unsigned char* pr = part + (jj * 16 + lr) * RC * 16;
+        __builtin_memcpy(__builtin_assume_aligned(pr + (((byte >> 4) ^ (lr & (RC - 1))) << 4) + (byte & 15), 4 * ES), e, 4 * ES);
+      };
       float sa[CT];
       int ids[CT];
 #pragma unroll
