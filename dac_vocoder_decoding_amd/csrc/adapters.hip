@@ -21,17 +21,31 @@ namespace voc {
 
 constexpr int kChunk = 128;  // codes of a row that a wave takes at a time: two steps of 64
 
-// 16 codes of a row of K at k, zero past its end.
+// 16 codes of a row of K at k, zero past its end: the last 16 of the row,
+// shifted, where fewer are left.
 __device__ __forceinline__ i32x4 load_codes16(const int8_t* row, int k, int K) {
-  i32x4 c = {0, 0, 0, 0};
-  if (k + 16 <= K) {
-    __builtin_memcpy(&c, row + k, 16);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (k + i < K) c[i >> 2] |= static_cast<int>((static_cast<uint32_t>(row[k + i]) & 0xffu) << (8 * (i & 3)));
+  uint64_t c[2] = {0, 0};
+  if (K < 16) {
+#pragma unroll 1
+    for (int i = K - 1; i >= k; --i) {  // (K - k < 16)
+      c[1] = c[1] << 8 | c[0] >> 56;
+      c[0] = c[0] << 8 | static_cast<uint8_t>(row[i]);
+    }
+    return __builtin_bit_cast(i32x4, c);
   }
-  return c;
+  const int at = min(k, K - 16), n = k - at;
+  __builtin_memcpy(c, row + at, 16);
+  if (n > 0) {
+    const int bits = 8 * (n & 7);
+    if (n >= 8) {
+      c[0] = c[1];
+      c[1] = 0;
+    }
+    if (bits) c[0] = c[0] >> bits | c[1] << (64 - bits);
+    c[1] >>= bits;
+    if (n >= 16) c[0] = 0;
+  }
+  return __builtin_bit_cast(i32x4, c);
 }
 
 // Eight codes as eight values of the weights' type, exactly.
@@ -72,17 +86,21 @@ template <int RT>
 struct Weights {
   i32x4 w[RT][2][2];
 };
-// down + this lane's place: block i, step s, half h are ((i steps + s) 2 + h) KB further.
+// Step s of them.  down + this lane's place: block i, step s, half h are
+// ((i steps + s) 2 + h) KB further.
 template <int RT>
-__device__ __forceinline__ void load_weights(const uint16_t* down, int steps, int chunk, Weights<RT>& g) {
+__device__ __forceinline__ void load_step(const uint16_t* down, int steps, int chunk, int s, Weights<RT>& g) {
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int h = 0; h < 2; ++h)  // (a last step that is not there has codes of zero: any weights do, those of the one before)
+      g.w[i][s][h] = *reinterpret_cast<const i32x4*>(
+          down + ((static_cast<int64_t>(i) * steps + min(2 * chunk + s, steps - 1)) * 2 + h) * 512);
+}
+template <int RT>
+__device__ __forceinline__ void load_weights(const uint16_t* down, int steps, int chunk, Weights<RT>& g) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)  // (a last step that is not there has codes of zero: any weights do, those of the one before)
-        g.w[i][s][h] = *reinterpret_cast<const i32x4*>(
-            down + ((static_cast<int64_t>(i) * steps + min(2 * chunk + s, steps - 1)) * 2 + h) * 512);
+  for (int s = 0; s < 2; ++s) load_step<RT>(down, steps, chunk, s, g);
 }
 
 // Eight ranks of row m (place r of its chunk, in a group of LANES lanes that
@@ -189,8 +207,8 @@ __global__ __launch_bounds__(512) void shrink_one_kernel(const AdaptArgs a, int 
 template <bool BF16, int RT, int TB>
 __global__ __launch_bounds__(512) void shrink_tile_kernel(const AdaptArgs a, int blocks) {
   constexpr int ROWS = 16 * TB, PITCH = 16 * RT + 4;
-  // Codes while the waves multiply (2 KB a wave and 16 rows), their sums, then u.
-  constexpr int SUMS = 8 * RT * TB * 1024, LDS = SUMS > 16384 * TB ? SUMS : 16384 * TB;
+  // Codes while the waves multiply (2 KB a wave and 16 rows), then their sums for two adapters.
+  constexpr int SUMS = 2 * 8 * RT * TB * 1024, LDS = SUMS > 16384 * TB ? SUMS : 16384 * TB;
   __shared__ __attribute__((aligned(16))) unsigned char smem[LDS];
   __shared__ __attribute__((aligned(16))) float s_u[ROWS][PITCH];
   __shared__ int s_id[ROWS];
@@ -214,6 +232,9 @@ __global__ __launch_bounds__(512) void shrink_tile_kernel(const AdaptArgs a, int
 #pragma unroll
   for (int q = 0; q < 2 * TB; ++q)
     src[q] = a.g.a + static_cast<int64_t>(min(m0 + 8 * q + (lane >> 3), a.g.M - 1)) * a.g.lda;
+  // The row whose u this thread will store.
+  const int my_row = min(tid / (2 * RT), ROWS - 1);
+  const float my_scale = a.g.sa[min(m0 + my_row, a.g.M - 1)];
   const int64_t per = static_cast<int64_t>(a.g.rank / 16) * steps * 1024;  // weights of an adapter
   const uint16_t* down0 = a.down + static_cast<int64_t>(block) * RT * steps * 1024 + lane * 8;
 
@@ -232,6 +253,7 @@ __global__ __launch_bounds__(512) void shrink_tile_kernel(const AdaptArgs a, int
   while (true) {  // (the same for every wave: they hold the same numbers)
     const int one = next_id(), two = one < 0 ? -1 : next_id();
     if (one < 0) break;
+    const float scale1 = a.scale ? a.scale[one] : 1.f, scale2 = a.scale ? a.scale[max(two, 0)] : 1.f;
     f32x4 acc[2][RT][TB];
 #pragma unroll
     for (int n = 0; n < 2; ++n)
@@ -241,22 +263,35 @@ __global__ __launch_bounds__(512) void shrink_tile_kernel(const AdaptArgs a, int
         for (int j = 0; j < TB; ++j) acc[n][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     i32x4 code[2 * TB];
     auto fetch = [&](int c) {
+      const int k = c * kChunk + 16 * (lane & 7);
+      if ((c + 1) * kChunk <= K) {
 #pragma unroll
-      for (int q = 0; q < 2 * TB; ++q) code[q] = load_codes16(src[q], c * kChunk + 16 * (lane & 7), K);
+        for (int q = 0; q < 2 * TB; ++q) __builtin_memcpy(&code[q], src[q] + k, 16);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 2 * TB; ++q) code[q] = load_codes16(src[q], k, K);
+      }
     };
-    if (wave < chunks) fetch(wave);
+    // Weights stay on their way: a step's registers take the next product's as
+    // soon as they were used (the second adapter's of this chunk, or, where both
+    // adapters' fit, those of the next chunk).
+    constexpr bool BOTH = RT * TB <= 4;
+    Weights<RT> g[BOTH ? 2 : 1];
+    const uint16_t* down1 = down0 + one * per;
+    const uint16_t* down2 = down0 + max(two, 0) * per;
+    if (wave < chunks) {
+      load_weights<RT>(down1, steps, wave, g[0]);
+      if (BOTH && two >= 0) load_weights<RT>(down2, steps, wave, g[BOTH]);
+      fetch(wave);
+    }
     for (int c = wave; c < chunks; c += 8) {
-      // Both adapters' weights at once where the registers hold them.
-      constexpr bool BOTH = RT * TB <= 4;
-      Weights<RT> g[BOTH ? 2 : 1];
-      load_weights<RT>(down0 + one * per, steps, c, g[0]);
-      if (BOTH && two >= 0) load_weights<RT>(down0 + two * per, steps, c, g[BOTH]);
 #pragma unroll
       for (int q = 0; q < 2 * TB; ++q) {
         const int r = 8 * q + (lane >> 3);
         *reinterpret_cast<i32x4*>(part + r * 128 + (((lane & 7) ^ ((r >> 1) & 7)) << 4)) = code[q];
       }
-      if (c + 8 < chunks) fetch(c + 8);
+      const bool more = c + 8 < chunks;
+      if (more) fetch(c + 8);
       wave_lds_sync();
       i32x4 x[2][2][TB];
 #pragma unroll
@@ -267,51 +302,59 @@ __global__ __launch_bounds__(512) void shrink_tile_kernel(const AdaptArgs a, int
           x[s][0][j] = codes_to_16<BF16>(v[0], v[1]);
           x[s][1][j] = codes_to_16<BF16>(v[2], v[3]);
         }
-      auto multiply = [&](int n, const Weights<RT>& g) {
+      auto multiply = [&](int n, int s, const Weights<RT>& w) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int i = 0; i < RT; ++i)
 #pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-              for (int j = 0; j < TB; ++j) multiply16<BF16>(g.w[i][s][h], x[s][h][j], acc[n][i][j]);
+            for (int j = 0; j < TB; ++j) multiply16<BF16>(w.w[i][s][h], x[s][h][j], acc[n][i][j]);
       };
-      multiply(0, g[0]);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        multiply(0, s, g[0]);
+        if (!BOTH && two >= 0)
+          load_step<RT>(down2, steps, c, s, g[0]);
+        else if (more)
+          load_step<RT>(down1, steps, c + 8, s, g[0]);
+      }
       if (two >= 0) {
-        if (!BOTH) load_weights<RT>(down0 + two * per, steps, c, g[0]);
-        multiply(1, g[BOTH]);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          multiply(1, s, g[BOTH]);
+          if (more) load_step<RT>(BOTH ? down2 : down1, steps, c + 8, s, g[BOTH]);
+        }
       }
       wave_lds_sync();
     }
+    __syncthreads();  // every wave is done with its codes
+    f32x4(*sums)[2][RT * TB][64] = reinterpret_cast<f32x4(*)[2][RT * TB][64]>(smem);
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int pick = n ? two : one;
-      if (pick < 0) break;
-      __syncthreads();  // every wave is done with its codes, or with the sums before
-      f32x4(*sums)[RT * TB][64] = reinterpret_cast<f32x4(*)[RT * TB][64]>(smem);
+    for (int n = 0; n < 2; ++n)
+      if (n == 0 || two >= 0) {
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int j = 0; j < TB; ++j) sums[wave][i * TB + j][lane] = acc[n][i][j];
-      __syncthreads();
-      for (int b = wave; b < RT * TB; b += 8) {
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < 8; ++w) v += sums[w][b][lane];
-        *reinterpret_cast<f32x4*>(&s_u[16 * (b % TB) + lr][16 * (b / TB) + 4 * lg]) = v;
+          for (int j = 0; j < TB; ++j) sums[wave][n][i * TB + j][lane] = acc[n][i][j];
       }
-      __syncthreads();
-      // Eight ranks of a row a thread; whole rows, so that a row's lanes agree.
-      if (tid < ROWS * 2 * RT) {
-        const int r = tid / (2 * RT), at = tid % (2 * RT) * 8;
-        if (s_id[r] == pick) {
-          const float f = a.g.sa[m0 + r] * (a.scale ? a.scale[pick] : 1.f);
-          float u[8];
+    __syncthreads();
+    for (int b = wave; b < RT * TB; b += 8) {
+      const int n = two >= 0 && s_id[16 * (b % TB) + lr] == two;  // the lane's row is the second adapter's
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int k = 0; k < 8; ++k) u[k] = s_u[r][at + k] * f;
-          store_u<BF16, 2 * RT>(a, m0 + r, block, at, u);
-        }
+      for (int w = 0; w < 8; ++w) v += sums[w][n][b][lane];
+      *reinterpret_cast<f32x4*>(&s_u[16 * (b % TB) + lr][16 * (b / TB) + 4 * lg]) = v;
+    }
+    __syncthreads();
+    // Eight ranks of a row a thread; whole rows, so that a row's lanes agree.
+    if (tid < ROWS * 2 * RT) {
+      const int at = tid % (2 * RT) * 8, mine = s_id[my_row];
+      if (mine == one || (two >= 0 && mine == two)) {
+        const float f = my_scale * (mine == one ? scale1 : scale2);
+        float u[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[k] = s_u[my_row][at + k] * f;
+        store_u<BF16, 2 * RT>(a, m0 + my_row, block, at, u);
       }
     }
     __syncthreads();  // (the next codes overwrite the sums)
