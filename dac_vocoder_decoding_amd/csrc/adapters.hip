@@ -149,7 +149,8 @@ __device__ __forceinline__ void store_u(const AdaptArgs& a, int64_t m, int block
 
 // Few rows: a workgroup for a row and 16 RT ranks, K split over its eight
 // waves.  All 16 rows of the matrix product are this one (its codes reach 16
-// lanes in one read); bound by the latency of the loads.
+// lanes in one read); bound by the latency of the loads: 32 rows of 1024, 16
+// ranks 3.4 us, of 4096, 64 ranks 8.3.
 template <bool BF16, int RT>
 __global__ __launch_bounds__(512) void shrink_one_kernel(const AdaptArgs a, int blocks) {
   __shared__ f32x4 s_acc[8][RT][4];
@@ -200,7 +201,10 @@ __global__ __launch_bounds__(512) void shrink_one_kernel(const AdaptArgs a, int 
 }
 
 // Many rows: 16 TB of them and 16 RT ranks a workgroup, K split over its eight
-// waves, whose sums meet in LDS.  A wave reads whole lines of codes and turns
+// waves, whose sums meet in LDS.  Bound by the latency of each wave's few rounds
+// of loads: 8000 rows of 4096 in runs of 250, 64 ranks 20 us (32 MB of codes
+// and 128 MB of weights from the L2; one adapter for all 14), 800 rows in runs of
+// 25, 32 ranks 9.  A wave reads whole lines of codes and turns
 // them over in its own part of LDS (rows of 128 bytes, unit u of row r at u ^
 // (r / 2 % 8)).  The rows' adapters are taken two at a time, so that a tile
 // over the border of two streams reads its codes once.
@@ -364,10 +368,17 @@ __global__ __launch_bounds__(512) void shrink_tile_kernel(const AdaptArgs a, int
 template <bool BF16, int RT>
 static void go_shrink(const AdaptArgs& a, hipStream_t s) {
   const int blocks = a.g.rank / (16 * RT);
-  if (a.g.M <= 64) {
+  // A workgroup a row up to 512 rows, whatever their adapters (us, a row / tiles,
+  // K 4096 and 64 ranks: 64 rows of an adapter each 8.2 / 49, of runs of 25 8.4 /
+  // 11.8; 512 rows 14.1 / 48 and 15.7 / 13.6; K 1024 and 16 ranks: 64 rows 3.4 /
+  // 8.6, 512 rows in runs 4.5 / 4.5).
+  if (a.g.M <= 512) {
     shrink_one_kernel<BF16, RT><<<dim3(static_cast<unsigned>(a.g.M) * blocks), 512, 0, s>>>(a, blocks);
     return;
   }
+  // 32 rows a workgroup, so that the weights are read half as often, where that
+  // leaves most of the CUs one (8000 rows of 4096, 64 ranks, runs of 250: 20 us,
+  // with 16 rows 27; 2000 rows 16 rows 14).
   auto groups = [&](int tb) { return static_cast<unsigned>((a.g.M + 16 * tb - 1) / (16 * tb)) * blocks; };
   if (groups(2) >= 192)
     shrink_tile_kernel<BF16, RT, 2><<<dim3(groups(2)), 512, 0, s>>>(a, blocks);

@@ -37,9 +37,11 @@ def held(cache, table, past, new, which):
     (32, 7, 64, 1, [31, 0], [40, 33], True, "step_page", (1, 4)), (16, 2, 128, 4, [1], [50], False, "step_page", (1, 4)),
     (64, 3, 64, 1, [60, 5], [9, 128], True, "step_page", (2, 4)), (128, 3, 32, 1, [100], [200], False, "step_page", (2, 4)),
     (32, 3, 96, 1, [9], [100], True, "step_page", (2, 4)), (64, 3, 128, 4, [63, 0], [10, 64], False, "step_page", (4, 4)),
-    (32, 1, 160, 2, [30], [9], True, "step_page", (4, 4)), (128, 3, 128, 1, [127, 0], [130, 256], True, "step_page", (4, 8)),
+    (32, 1, 160, 2, [30], [29], True, "step_page", (4, 4)), (128, 3, 128, 1, [127, 0], [130, 256], True, "step_page", (4, 8)),
     (64, 2, 256, 1, [5], [70], False, "step_page", (4, 8)), (128, 2, 256, 2, [100], [300], False, "step_page", (8, 8)),
-    (16, 2, 64, 1, [5], [8], True, "step", (8, 0)), (64, 1, 128, 4, [60], [8], False, "step", (16, 1)),
+    (16, 2, 64, 1, [5], [1], True, "step_page", (1, 2)), (64, 1, 128, 4, [60], [12], False, "step", (16, 1)),
+    (64, 2, 64, 1, [60, 3], [1, 2], True, "step", (8, 0)), (128, 3, 256, 1, [127, 3, 0], [1, 5, 12], False, "step", (32, 1)),
+    (32, 1, 64, 3, [31, 32], [2, 1], False, "step_page", (1, 4)),
     # Enough pages for several heads a workgroup, some groups short of a head; tokens in runs.
     (64, 5, 128, 1, [3 * i for i in range(7)], [4000 - 31 * i for i in range(7)], False, "step_page", (4, 4)),
     (16, 9, 64, 1, [i for i in range(60)], [500 - 7 * i for i in range(60)], True, "step_page", (1, 2))])
