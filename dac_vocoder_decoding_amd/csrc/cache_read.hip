@@ -5,9 +5,14 @@
 namespace voc {
 
 template <int T, bool VEC>
-__device__ __forceinline__ void put8(typename Elem<T>::type* p, const float (&v)[8]) {
+__device__ __forceinline__ void put8(typename Elem<T>::type* p, const float (&v)[8], bool stream) {
   if constexpr (VEC) {
-    store8<T>(p, v);
+    if (stream) {
+      stream8<T>(p, v);
+      asm volatile("");  // (else the compiler makes one plain store of both)
+    } else {
+      store8<T>(p, v);
+    }
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k) p[k] = static_cast<typename Elem<T>::type>(v[k]);
@@ -64,7 +69,7 @@ __global__ __launch_bounds__(256) void cache_read_kernel(const ReadArgs a, int b
       float v[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = value_at(k < 4 ? c[i].x : c[i].y, k & 3, scale);
-      put8<T, VEC>(static_cast<E*>(a.k) + (sh.token + t - lo) * a.k_t + head * a.k_h + d, v);
+      put8<T, VEC>(static_cast<E*>(a.k) + (sh.token + t - lo) * a.k_t + head * a.k_h + d, v, a.stream);
     }
     return;
   }
@@ -109,7 +114,7 @@ __global__ __launch_bounds__(256) void cache_read_kernel(const ReadArgs a, int b
       float v[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = value_at(w[k], t, scale);
-      put8<T, VEC>(out + (sh.token + t4 + t - lo) * a.v_t, v);
+      put8<T, VEC>(out + (sh.token + t4 + t - lo) * a.v_t, v, a.stream);
     }
   }
 }
@@ -155,7 +160,9 @@ static void pick_read(const ReadArgs& a, hipStream_t s, Form& form) {
     go_read<T, false>(a, s, form);
 }
 
-hipError_t launch_read(int dtype, const ReadArgs& a, hipStream_t s, Form& form) {
+hipError_t launch_read(int dtype, const ReadArgs& args, hipStream_t s, Form& form) {
+  ReadArgs a = args;
+  a.stream = 2 * static_cast<int64_t>(a.c.tokens) * a.c.heads * a.D * elem_size(dtype) > kStreamBytes;
   if (dtype == EL_F32)
     pick_read<EL_F32>(a, s, form);
   else if (dtype == EL_BF16)

@@ -30,7 +30,7 @@ __device__ __forceinline__ void load_fours(const typename Elem<T>::type* p, cons
     v[2 * i + 1] = static_cast<float>(f[i]);
   }
 }
-template <int T>
+template <int T, bool STREAM>
 __device__ __forceinline__ void store_fours(typename Elem<T>::type* p, typename Elem<T>::type* q, const float (&v)[8]) {
   typename Elem<T>::type e[4], f[4];
 #pragma unroll
@@ -38,8 +38,14 @@ __device__ __forceinline__ void store_fours(typename Elem<T>::type* p, typename 
     e[i] = static_cast<typename Elem<T>::type>(v[2 * i]);
     f[i] = static_cast<typename Elem<T>::type>(v[2 * i + 1]);
   }
-  __builtin_memcpy(__builtin_assume_aligned(p, sizeof(e)), e, sizeof(e));
-  __builtin_memcpy(__builtin_assume_aligned(q, sizeof(f)), f, sizeof(f));
+  typedef uint32_t W __attribute__((ext_vector_type(sizeof(e) / 4)));
+  if constexpr (STREAM) {
+    __builtin_nontemporal_store(__builtin_bit_cast(W, e), reinterpret_cast<W*>(p));
+    __builtin_nontemporal_store(__builtin_bit_cast(W, f), reinterpret_cast<W*>(q));
+  } else {
+    *reinterpret_cast<W*>(p) = __builtin_bit_cast(W, e);
+    *reinterpret_cast<W*>(q) = __builtin_bit_cast(W, f);
+  }
 }
 
 // The place of a lane's unit in its head.
@@ -89,7 +95,7 @@ struct Unit {
       load_fours<T>(head + at, head + hi, v);
     }
   }
-  template <int T>
+  template <int T, bool STREAM>
   __device__ __forceinline__ void store(typename Elem<T>::type* head, const float (&v)[8]) const {
     if constexpr (MODE == kAny) {
 #pragma unroll
@@ -99,9 +105,12 @@ struct Unit {
       }
     } else if (live) {
       if constexpr (MODE == kAdjacent) {
-        store8<T>(head + at, v);
+        if constexpr (STREAM)
+          stream8<T>(head + at, v);
+        else
+          store8<T>(head + at, v);
       } else {
-        store_fours<T>(head + at, head + hi, v);
+        store_fours<T, STREAM>(head + at, head + hi, v);
       }
     }
   }
@@ -286,7 +295,7 @@ __device__ __forceinline__ void turn(const HeadShape& h, const Unit<MODE>& u, bo
 // A wave turns one token's heads of a set: rounds first, first + step, .. of
 // 64 / G heads each.  The loads of two rounds are in flight
 // together (of one as fast, of four 44 us for 36: 10336 x 40 heads x 128 bf16).
-template <int T, int MODE, int G>
+template <int T, int MODE, int G, bool STREAM>
 __device__ __forceinline__ void turn_set(const HeadShape& h, const Unit<MODE>& u, const HeadSet& set, const Turn& m,
                                          int64_t row, int first, int step) {
   typedef typename Elem<T>::type E;
@@ -306,7 +315,7 @@ __device__ __forceinline__ void turn_set(const HeadShape& h, const Unit<MODE>& u
       const int head = (r + n * step) * GW + lane / G;
       if (head >= set.heads) continue;  // (a whole group of lanes: the sums stay inside one)
       turn<G>(h, u, set.w != nullptr, m, v[n]);
-      u.template store<T>(y + head * set.y_h, v[n]);
+      u.template store<T, STREAM>(y + head * set.y_h, v[n]);
     }
   }
 }
@@ -324,6 +333,7 @@ struct Turner {
   }
   // A token's heads, this wave's share of them: rounds part, part + parts, ..
   // of the queries' and then the keys' heads.
+  template <bool STREAM>
   __device__ __forceinline__ void token(const HeadShape& h, const HeadSet& q, const HeadSet& k, int64_t row, int position,
                                         int part, int parts) const {
     float c[4], s[4];
@@ -332,11 +342,11 @@ struct Turner {
     const int rounds = (q.heads + 64 / G - 1) / (64 / G);
     if (q.heads) {
       m.set(wq, c, s);
-      turn_set<T, MODE, G>(h, u, q, m, row, part, parts);
+      turn_set<T, MODE, G, STREAM>(h, u, q, m, row, part, parts);
     }
     if (k.heads) {
       m.set(wk, c, s);
-      turn_set<T, MODE, G>(h, u, k, m, row, (part + parts - rounds % parts) % parts, parts);
+      turn_set<T, MODE, G, STREAM>(h, u, k, m, row, (part + parts - rounds % parts) % parts, parts);
     }
   }
 };

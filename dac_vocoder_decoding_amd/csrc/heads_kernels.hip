@@ -7,15 +7,24 @@
 
 namespace voc {
 
-// A wave goes on with the token that is a grid further.
+// A wave goes on with the token that is a grid further.  Bound by memory: 10336
+// tokens of 40 heads x 128 d in bf16 (212 MB) 38 us, 5.6 TB/s; 32 tokens of 32
+// heads x 64 d, all latency, 4.0.
 template <int T, int MODE, int G>
 __global__ __launch_bounds__(256) void norm_rotate_kernel(const NormRotateArgs a, int parts) {
   const Turner<T, MODE, G> turner(a.h, a.q, a.k);
   const int64_t all = a.tokens * parts, step = static_cast<int64_t>(gridDim.x) * 4;
-  for (int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); w < all; w += step) {
-    const int64_t row = w / parts;
-    turner.token(a.h, a.q, a.k, row, a.position ? a.position[row] : 0, static_cast<int>(w % parts), parts);
-  }
+  auto run = [&](auto stream) {
+    for (int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); w < all; w += step) {
+      const int64_t row = w / parts;
+      turner.template token<decltype(stream)::value>(a.h, a.q, a.k, row, a.position ? a.position[row] : 0,
+                                                     static_cast<int>(w % parts), parts);
+    }
+  };
+  if (a.h.stream)
+    run(std::true_type{});
+  else
+    run(std::false_type{});
 }
 
 // Lanes that hold a head.
@@ -76,7 +85,9 @@ static int token_parts(int q_heads, int k_heads, int g, int64_t tokens) {
   return parts > 1 ? static_cast<int>(parts) : 1;
 }
 
-hipError_t launch_norm_rotate(int dtype, const NormRotateArgs& a, hipStream_t s, Form& form) {
+hipError_t launch_norm_rotate(int dtype, const NormRotateArgs& args, hipStream_t s, Form& form) {
+  NormRotateArgs a = args;
+  a.h.stream = a.tokens * (a.q.heads + a.k.heads) * a.h.D * elem_size(dtype) > kStreamBytes;
   const int g = head_lanes(a.h.D, a.h.pairs), mode = pairs_mode(a.h, whole_words(a.q, dtype) && whole_words(a.k, dtype));
   const int parts = token_parts(a.q.heads, a.k.heads, g, a.tokens);
   form = Form{"heads", {g, mode}};
@@ -126,7 +137,9 @@ static StepPlan plan_step(int dtype, const StepArgs& a) {
 
 int64_t step_workgroups(int dtype, const StepArgs& a) { return plan_step(dtype, a).workgroups; }
 
-hipError_t launch_step(int dtype, const StepArgs& a, hipStream_t s, Form& form) {
+hipError_t launch_step(int dtype, const StepArgs& args, hipStream_t s, Form& form) {
+  StepArgs a = args;
+  a.h.stream = static_cast<int64_t>(a.c.tokens) * a.q.heads * a.h.D * elem_size(dtype) > kStreamBytes;
   const StepPlan p = plan_step(dtype, a);
   if (p.page)
     form = Form{"step_page", {p.wpp, p.np}};

@@ -126,8 +126,14 @@ struct HeadShape {
   int D, pairs;  // the first 2 * pairs values rotate
   int adjacent;  // pairs 2i, 2i + 1; else i, i + pairs
   float eps, per;  // per: 1 / D
+  bool stream;     // set by the launch: outputs go past the caches
 };
 constexpr int kHeadMaxD = 256;
+// Outputs of more than this go past the caches: an XCD's L2 (4 MB) keeps none of
+// it for a reader, and the inputs keep their place (us, through them / past them,
+// buffers in turn: 10336 tokens of 40 x 128 d in bf16 48.6 / 37.7; cache read of 2
+// x 65536 x 8 x 128 d 143 / 138).
+constexpr int64_t kStreamBytes = 8 << 20;
 struct NormRotateArgs {
   HeadShape h;
   HeadSet q, k;             // k.heads 0: none
@@ -153,6 +159,7 @@ struct ReadArgs {
   void* v;  // or null
   int64_t k_t, k_h, v_t, v_h;
   int D, batch;
+  bool stream;  // set by the launch
 };
 int64_t read_workgroups(const ReadArgs& a);  // of one sequence
 hipError_t launch_read(int dtype, const ReadArgs& a, hipStream_t s, Form& form);

@@ -25,6 +25,16 @@ __device__ __forceinline__ void load8(const typename Elem<T>::type* p, float (&v
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(x.e[i]);
 }
+// The same past the caches, for outputs that they would not keep for a reader.
+template <int T>
+__device__ __forceinline__ void stream8(typename Elem<T>::type* p, const float (&v)[8]) {
+  typedef typename Elem<T>::type E;
+  union { i32x4 u[sizeof(E) / 2]; E e[8]; } x;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x.e[i] = static_cast<E>(v[i]);
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(E) / 2; ++i) __builtin_nontemporal_store(x.u[i], reinterpret_cast<i32x4*>(p) + i);
+}
 template <int T>
 __device__ __forceinline__ void store8(typename Elem<T>::type* p, const float (&v)[8]) {
   typedef typename Elem<T>::type E;

@@ -155,7 +155,7 @@ voc_status check_heads(voc_ops* o, int dtype, int head_dim, const float* freq, i
   if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(o, VOC_INVALID_PARAMS, "eps must be finite and not negative");
   if (pairs && !freq) return fail(o, VOC_INVALID_PARAMS, "freq is NULL");
   if (!aligned(freq, 4)) return fail(o, VOC_INVALID_PARAMS, "freq must be 4-byte aligned");
-  *h = HeadShape{freq, head_dim, pairs, adjacent, eps, 1.f / static_cast<float>(head_dim)};
+  *h = HeadShape{freq, head_dim, pairs, adjacent, eps, 1.f / static_cast<float>(head_dim), false};
   return VOC_OK;
 }
 

@@ -21,7 +21,7 @@ __global__ __launch_bounds__(256) void step_few_kernel(const StepArgs a, int pag
   if (static_cast<int>(blockIdx.x) >= cached) {
     const Seq s = load_seq(a.c, b);
     const int wave = (blockIdx.x - cached) * 4 + (tid >> 6), i = wave / parts;
-    if (i < s.count) Turner<T, MODE, G>(a.h, a.q, HeadSet{}).token(a.h, a.q, HeadSet{}, s.start + i, s.past + i, wave % parts, parts);
+    if (i < s.count) Turner<T, MODE, G>(a.h, a.q, HeadSet{}).template token<false>(a.h, a.q, HeadSet{}, s.start + i, s.past + i, wave % parts, parts);
     return;
   }
   const int j = blockIdx.x / (2 * a.c.heads), y = blockIdx.x % (2 * a.c.heads), head = y >> 1;
@@ -128,7 +128,14 @@ __global__ __launch_bounds__(WPP < 4 ? 256 : 64 * WPP, NP > 4 ? 2 : 4) void step
     const int w = (blockIdx.x - jobs) * NW + wave, i0 = w / parts * run;
     if (i0 >= s.count) return;
     const Turner<T, MODE, G> turner(a.h, a.q, HeadSet{});
-    for (int i = i0; i < min(i0 + run, s.count); ++i) turner.token(a.h, a.q, HeadSet{}, s.start + i, s.past + i, w % parts, parts);
+    auto tokens = [&](auto stream) {
+      for (int i = i0; i < min(i0 + run, s.count); ++i)
+        turner.template token<decltype(stream)::value>(a.h, a.q, HeadSet{}, s.start + i, s.past + i, w % parts, parts);
+    };
+    if (a.h.stream)
+      tokens(std::true_type{});
+    else
+      tokens(std::false_type{});
     return;
   }
   const int group = blockIdx.x % groups, j = blockIdx.x / (2 * groups);
