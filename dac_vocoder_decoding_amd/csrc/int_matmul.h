@@ -518,18 +518,18 @@ __global__ __launch_bounds__(WF * WT * 64, ADAPT ? 2 : 1) void int_matmul_tile_k
       }
 #pragma unroll
       for (int i0 = 0; i0 < FF; i0 += FI) {
-        f4 sbv[FI], biv[FI];
-#pragma unroll
-        for (int i = 0; i < FI; ++i) column_scales(i0 + i, sbv[i], biv[i]);
 #pragma unroll
         for (int jj = 0; jj < CT; jj += 2) {
           f32x4 add[FI][2];
           int id[2] = {ids[jj], ids[jj + 1]};
           low_rank<T>(a, nw + 16 * i0, mw + (j0 + jj) * 16, id, add);
 #pragma unroll
-          for (int i = 0; i < FI; ++i)
+          for (int i = 0; i < FI; ++i) {
+            f4 sbv, biv;
+            column_scales(i0 + i, sbv, biv);
 #pragma unroll
-            for (int p = 0; p < 2; ++p) stage(i0 + i, jj + p, acc[i0 + i][j0 + jj + p], sa[jj + p], sbv[i], biv[i], add[i][p]);
+            for (int p = 0; p < 2; ++p) stage(i0 + i, jj + p, acc[i0 + i][j0 + jj + p], sa[jj + p], sbv, biv, add[i][p]);
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
       }
