@@ -752,7 +752,12 @@ voc_status vocoder_cache_attention(voc_ops *ops, const voc_kv_cache *cache,
  *   "rows"                        groups of 8 values a thread, waves a row
  *   "product_few", "product_few_shifted"   features, tokens of a workgroup
  *   "product_tile", "product_tile_rows"    the same (fed by DMA, through registers)
+ *   (with adapters the same: the product's kernel, which runs last)
  *   "append", "append_page"       threads of a workgroup, page_tokens
+ *   "heads"                       lanes of a head, pairs read: 0 adjacent, 1 halves, 2 one by one
+ *   "step"                        the same (norm, rotation and append by rows)
+ *   "step_page"                   waves of a page and head, rows of a lane (by pages)
+ *   "read", "read_any"            codes of a workgroup, page_tokens (whole words, any alignment)
  *   "attend_few", "attend_many"   query rows of a workgroup, parts of the keys
  * shape may be NULL.  No error state is touched. */
 const char *voc_dbg_last_kernel(const voc_ops *ops, int shape[2]);
