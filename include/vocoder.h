@@ -573,7 +573,8 @@ voc_status vocoder_matmul_int(voc_ops *ops, int out_dtype, int64_t M, int64_t N,
  *   ((i S + p) rank / 8 + c) 128 + 8 f + e.
  * Both are 16-byte aligned.  scale: fp32 [count], or
  * NULL for 1.
- * Uses the handle's workspace.
+ * Uses the handle's workspace: two graphs that were captured on one handle
+ * must not run at once, as two streams must not use it.
  * Errors: VOC_INVALID_PARAMS, VOC_DEVICE_ERROR.
  */
 typedef struct voc_adapters {
@@ -686,7 +687,7 @@ voc_status vocoder_cache_append(voc_ops *ops, const voc_kv_cache *cache, const v
  * heads may be 0 (keys and values only); rows of q_out that belong to no
  * sequence are not written.
  * The number of workgroups, batch times the heads of the touched pages and the
- * queries, stays below 2^24.
+ * queries, stays below 2^23.
  * Errors: VOC_INVALID_PARAMS, VOC_DEVICE_ERROR.
  */
 voc_status vocoder_norm_rotate_append(voc_ops *ops, const voc_kv_cache *cache,
