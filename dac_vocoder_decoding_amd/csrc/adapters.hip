@@ -165,7 +165,6 @@ __global__ __launch_bounds__(512) void shrink_one_kernel(const AdaptArgs a, int 
   f32x4 acc[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
   for (int c = wave; c < chunks; c += 8) {
     Weights<RT> g;
     load_weights<RT>(down, steps, c, g);
