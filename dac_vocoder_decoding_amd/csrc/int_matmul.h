@@ -290,6 +290,161 @@ __global__ __launch_bounds__(512) void int_matmul_few_kernel(const IntMatmulArgs
   store4<T, ADAPT>(a, vec, m, n, a.sa[m], v, add);
 }
 
+// The epilogue of a 256 x 256 tile whose rows have up to two adapters of up to
+// 64 ranks: their operands come to LDS in one go, where the main loop's stages
+// were (u of the 256 tokens 64 KB, up of 256 features 32 KB an adapter; the rows
+// of 16 tokens that a wave turns over lie behind).  The waves then wait once for
+// memory, not once for every few blocks (8000 x 8192 x 4096, 64 ranks, runs of
+// 250, both launches: 319 us, 337 by blocks).  False where a tile has more of either.
+template <int T, bool BF16, int FF, int FT>
+__device__ __forceinline__ bool staged_epilogue(const IntMatmulArgs& a, unsigned char* smem, int n0, int m0, int wf, int wt, int vec,
+                                                i32x4 (&acc)[FF][FT]) {
+  typedef typename Elem<T>::type E;
+  constexpr int NT = 2, ES = sizeof(E), RC = FF * 16 * ES / 16;
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (a.rank > 64) return false;
+  // The tile's adapters: every wave looks at all 256 rows, so that all agree.
+  int all[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int m = m0 + 64 * q + lane;
+    all[q] = m < a.M ? a.adapter[m] : -1;
+    if (all[q] >= a.adapters) all[q] = -1;
+  }
+  auto next = [&] {
+    int pick = -1;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint64_t left = __ballot(all[q] >= 0);
+      if (pick < 0 && left) pick = __builtin_amdgcn_readlane(all[q], __ffsll(static_cast<unsigned long long>(left)) - 1);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (all[q] == pick) all[q] = -1;
+    return pick;
+  };
+  const int one = next(), two = next();
+  if (next() >= 0) return false;
+  const int features = (a.N + 15) >> 4, steps = (a.rank + 31) >> 5;
+  const int nw = n0 + wf * FF * 16, mw = m0 + wt * FT * 16;
+  const uint32_t lds = lds_addr(smem);
+  constexpr uint32_t kUp = 65536;
+  if (one >= 0) {
+    // Both are contiguous: 16 rows by the rank are rank / 32 KB of each.
+    const int groups = min(16, ((a.M + 15) >> 4) - (m0 >> 4)), blocks = min(16, features - (n0 >> 4));
+    const i4 us = buf_rsrc(a.ut + static_cast<int64_t>(m0 >> 4) * NT * a.rank * 16, static_cast<uint32_t>(groups * NT * a.rank * 32));
+    for (int b = wave; b < a.rank; b += 8) dma16(us, b * 1024 + lane * 16, lds + b * 1024);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int pick = n ? two : one;
+      if (pick < 0) continue;
+      const i4 ws = buf_rsrc(a.up + (static_cast<int64_t>(pick) * features + (n0 >> 4)) * a.rank * 16, static_cast<uint32_t>(blocks * a.rank * 32));
+      for (int b = wave; b < a.rank / 2; b += 8) dma16(ws, b * 1024 + lane * 16, lds + kUp + n * 32768 + b * 1024);
+    }
+  }
+  f4 sb[FF], bi[FF];
+#pragma unroll
+  for (int i = 0; i < FF; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int n = min(nw + i * 16 + 4 * lg + e, a.N - 1);
+      sb[i][e] = a.sb[n];
+      bi[i][e] = a.bias ? a.bias[n] : 0.f;
+    }
+  float sa[FT], down[FT];
+  int id[FT];
+#pragma unroll
+  for (int j = 0; j < FT; ++j) {
+    const int m = mw + 16 * j + lr;
+    sa[j] = a.sa[min(m, a.M - 1)];
+    id[j] = m < a.M ? a.adapter[m] : -1;
+    if (id[j] >= a.adapters) id[j] = -1;
+    down[j] = id[j] >= 0 ? a.uf[m] : 0.f;
+  }
+  wait_vm<0>();
+  lds_barrier();
+  const bool in = lane < 2 * a.chunk;  // (16 ranks fill half of a product's slots)
+  unsigned char* part = smem + 131072 + wave * 4096;
+#pragma unroll
+  for (int j = 0; j < FT; ++j) {
+    i32x4 uf[2][NT];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        uf[s][t] = i32x4{0, 0, 0, 0};
+        if (in && s < steps)
+          uf[s][t] = *reinterpret_cast<const i32x4*>(smem + (((wt * FT + j) * NT + t) * a.rank * 16 + s * 512 + lane * 8) * 2);
+      }
+    bool has[2];
+    has[0] = one >= 0 && __ballot(id[j] == one) != 0;
+    has[1] = two >= 0 && __ballot(id[j] == two) != 0;
+#pragma unroll
+    for (int i = 0; i < FF; ++i) {
+      f32x4 add = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        if (!has[n]) continue;
+        f32x4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (s >= steps) continue;
+          i32x4 w = {0, 0, 0, 0};
+          if (in) w = *reinterpret_cast<const i32x4*>(smem + kUp + n * 32768 + ((wf * FF + i) * a.rank * 16 + s * 512 + lane * 8) * 2);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            if constexpr (BF16)
+              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, uf[s][t]), p, 0, 0, 0);
+            else
+              p = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, w), __builtin_bit_cast(f16x8, uf[s][t]), p, 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (id[j] == (n ? two : one)) add[q] = p[q] * down[j];
+      }
+      E e[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        e[q] = static_cast<E>(activate<T>(static_cast<float>(acc[i][j][q]) * sa[j] * sb[i][q] + bi[i][q] + add[q], a.act));
+      const int byte = (i * 16 + 4 * lg) * ES;
+      __builtin_memcpy(__builtin_assume_aligned(part + lr * RC * 16 + (((byte >> 4) ^ (lr & (RC - 1))) << 4) + (byte & 15), 4 * ES), e, 4 * ES);
+    }
+    wave_lds_sync();
+    if (vec) {
+#pragma unroll
+      for (int q = 0; q < 16 * RC / 64; ++q) {
+        const int x = q * 64 + lane, t = x / RC, c = x % RC;
+        const int m = mw + j * 16 + t, n = nw + c * (16 / ES);
+        const i32x4 v = *reinterpret_cast<const i32x4*>(part + t * RC * 16 + ((c ^ (t & (RC - 1))) << 4));
+        if (m < a.M && n < a.N) {
+          E* y = static_cast<E*>(a.y) + static_cast<int64_t>(m) * a.ldy + n;
+          if (n + 16 / ES <= a.N) {
+            __builtin_nontemporal_store(v, reinterpret_cast<i32x4*>(y));
+          } else {
+            const E* e = reinterpret_cast<const E*>(&v);
+#pragma unroll
+            for (int k = 0; k < 16 / ES; ++k)
+              if (n + k < a.N) y[k] = e[k];
+          }
+        }
+      }
+    } else {
+      constexpr int NF = FF * 16;
+#pragma unroll 4
+      for (int q = 0; q < 16 * NF / 64; ++q) {
+        const int x = q * 64 + lane, t = x / NF, f = x % NF;
+        const int m = mw + j * 16 + t, n = nw + f, byte = f * ES;
+        const E v = *reinterpret_cast<const E*>(part + t * RC * 16 + (((byte >> 4) ^ (t & (RC - 1))) << 4) + (byte & 15));
+        if (m < a.M && n < a.N) static_cast<E*>(a.y)[static_cast<int64_t>(m) * a.ldy + n] = v;
+      }
+    }
+    wave_lds_sync();
+  }
+  return true;
+}
+
 // ------------------------------------------------------------- tiles
 // BF features x BT tokens per workgroup, WF x WT waves.  K passes in stages
 // of 128 codes (whole cache lines) through a ring of NS stages in LDS.  A
@@ -316,7 +471,9 @@ __global__ __launch_bounds__(WF * WT * 64, ADAPT ? 2 : 1) void int_matmul_tile_k
   constexpr int LW = TB / NW;
   constexpr int STAGE = TB * 1024;
   static_assert(TB % NW == 0 && NW % 2 == 0 && (NS - 2) * LW <= 63, "whole blocks per wave");
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[NS * STAGE];
+  // The largest tile's epilogue keeps the adapters' operands in LDS.
+  constexpr bool STAGED = ADAPT && DMA && BF == 256 && BT == 256 && T != EL_F32;
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[NS * STAGE + (STAGED ? 32768 : 0)];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lg = lane >> 4;
@@ -452,6 +609,11 @@ __global__ __launch_bounds__(WF * WT * 64, ADAPT ? 2 : 1) void int_matmul_tile_k
   __syncthreads();
   unsigned char* part = smem + wave * (NS * STAGE / NW);
   const int nw = n0 + wf * FF * 16, mw = m0 + wt * FT * 16;
+  if constexpr (STAGED) {
+    if (a.up_bf16 ? staged_epilogue<T, true, FF, FT>(a, smem, n0, m0, wf, wt, vec, acc)
+                  : staged_epilogue<T, false, FF, FT>(a, smem, n0, m0, wf, wt, vec, acc))
+      return;
+  }
   f4 sb[FF], bi[FF];
   if constexpr (!ADAPT) {
 #pragma unroll

@@ -601,7 +601,8 @@ voc_status vocoder_matmul_int_adapters(voc_ops *ops, int out_dtype, int64_t M, i
  * Values from 2 * pairs on are not rotated.  The angle is the product of the
  * int32 position and the fp32 frequency, taken to its fraction of a turn in 64
  * bits: far positions keep their angles.  The result is rounded once.  A head
- * with a weight whose sum of squares is not finite in fp32 becomes NaN.
+ * with a weight whose sum of squares is not finite in fp32 becomes NaN (with
+ * eps 0 one of zeros does too, 0 / 0).
  * q, k and their outputs: dtype, element [token][head][d] at token *
  * token_stride + head * head_stride + d; an output may be its input itself
  * (any other overlap is an error of the caller).  weights: fp32 [head_dim];

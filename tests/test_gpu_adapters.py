@@ -232,3 +232,47 @@ def test_adapters_refusals(ops):
     assert L.vocoder_matmul_int_adapters(ops, 0, 4, 4, 64, q.data_ptr(), 64, s.data_ptr(), q.data_ptr(), 64, s.data_ptr(), None, 0,
                                          ctypes.byref(c), ids.data_ptr(), x.data_ptr(), 64, None) == V.VOC_INVALID_PARAMS
     assert mm(M=0, a=None) == V.VOC_OK and mm() == V.VOC_OK and mm(scale=None) == V.VOC_OK
+
+
+@pytest.mark.parametrize("dtype,held", [(F16, F16), (BF16, BF16), (BF16, F16)])
+@pytest.mark.parametrize("rank", [3, 16, 32, 50, 64])
+@pytest.mark.parametrize("pattern", ["runs of 250", "runs of 300, some none", "two mixed", "first tile only", "none"])
+def test_adapters_in_tiles_of_two(ops, dtype, held, rank, pattern):
+    """Tiles of 256 rows with up to two adapters, whose operands are kept in
+    LDS, and tiles with more of them in the same call; ragged edges."""
+    g = gen(rank)
+    M, N, K, count = 3331, 3900, 272, 5
+    a, sa, b, sb, ads, down, up = case(g, M, N, K, rank, count, held)
+    m = torch.arange(M, device="cuda")
+    if pattern == "runs of 250":
+        ids = (m // 250) % count
+    elif pattern == "runs of 300, some none":
+        ids = (m // 300) % (count + 1) - 1
+    elif pattern == "two mixed":
+        ids = torch.where(torch.rand(M, generator=g, device="cuda") < 0.4, 3, torch.where(m % 7 == 0, -1, 1))
+    elif pattern == "first tile only":
+        ids = torch.where(m < 256, m % count, torch.where(m == 3330, 2, -1))
+    else:
+        ids = torch.full_like(m, -7)
+    ids, bias = ids.to(torch.int32), randn(g, N)
+    for width in (N, N + 3):
+        big = torch.full((M + 1, width), 7.0, dtype=dtype, device="cuda")
+        y = V.matmul_int_adapters(ops, a, sa, b, sb, ads, ids, bias=bias, gelu=rank == 16, out=big[:M, :N])
+        assert V.voc_dbg_last_kernel(ops) == ("product_tile", (256, 256))
+        check(y, a, sa, b, sb, ads, down, up, ids, bias, rank == 16)
+        assert (big[M:] == 7).all() and (big[:, N:] == 7).all()
+        none = ids < 0
+        plain = V.matmul_int(ops, a, sa, b, sb, bias=bias, gelu=rank == 16, dtype=dtype)
+        assert torch.equal(y[none], plain[none])
+
+
+def test_adapters_that_are_not_finite_in_tiles_of_two(ops):
+    g = gen(17)
+    a, sa, b, sb, ads, down, up = case(g, 3331, 3900, 272, 32, 3, BF16)
+    ids = torch.where(torch.rand(3331, generator=g, device="cuda") < 0.5, 1, 2).to(torch.int32)
+    ids[::5] = -1
+    want = V.matmul_int_adapters(ops, a, sa, b, sb, ads, ids, dtype=BF16)
+    down[1, 3, 5], up[1, 7, 2] = float("nan"), float("inf")
+    ads.set(1, down[1], up[1], ads.scale[1].item())
+    y = V.matmul_int_adapters(ops, a, sa, b, sb, ads, ids, dtype=BF16)
+    assert y[ids == 1].isnan().all() and torch.equal(y[ids != 1], want[ids != 1])
